@@ -1,4 +1,4 @@
-"""MI355X (gfx950) varlen gated delta-rule hot path.
+"""MI355X (gfx950) varlen gated delta-rule hot path, and the softmax-attention operators beside it.
 
 A thin binding over libgdn's C ABI (include/gdn.h).  These functions only marshal arguments: they
 check that tensors are device-resident and contiguous, allocate outputs with torch when the
@@ -16,7 +16,9 @@ from . import _abi
 from ._abi import GdnError, PATH_NAMES, lib  # noqa: F401
 
 __all__ = ["conv1d_varlen", "conv1d_varlen_capture", "prepare_qk_gates", "prepare_qk_gates_strided", "scan_varlen",
-           "scan_varlen_capture", "scan_varlen_strided", "scan_varlen_noalloc", "scan_workspace_bytes", "decode_step", "GdnError", "lib"]
+           "scan_varlen_capture", "scan_varlen_strided", "scan_varlen_noalloc", "scan_workspace_bytes", "decode_step",
+           "qk_norm_rope_varlen", "attention_varlen", "attention_prefix_varlen", "attention_workspace_bytes", "GdnError",
+           "lib"]
 
 _DTYPE = {torch.float32: _abi.F32, torch.bfloat16: _abi.BF16, torch.float16: _abi.F16}
 _TORCH = {v: k for k, v in _DTYPE.items()}
@@ -350,3 +352,176 @@ def decode_step(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, *,
                                _ptr(dev_status, "dev_status"), _stream(x.device))
     _check(st, "gdn_decode_step")
     return out, state_out, conv_state_out
+
+
+def _head_view(t: torch.Tensor, heads: int, D: int, like: torch.Tensor, what: str):
+    """(device address, row and head strides) of a [rows, heads, D] tensor with contiguous heads."""
+    if t.dtype != like.dtype:
+        raise TypeError(f"{what}: dtype {t.dtype} differs from {like.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{what} must be on {like.device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{what} must be [rows, {heads}, {D}], got {tuple(shape)}")
+    row, head, elem = t.stride()
+    if elem != 1 and D != 1:
+        raise ValueError(f"{what}: the elements of a head must be contiguous")
+    # the stride of an axis of one entry names nothing
+    return t.data_ptr(), (row if shape[0] > 1 else D * heads, head if heads > 1 else D)
+
+
+def _flat(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, like: torch.Tensor, what: str):
+    """Device address of a contiguous vector of n entries (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{what} must be on {like.device}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {n} entries")
+    return t.data_ptr()
+
+
+def _need_gpu(q: torch.Tensor):
+    if q.dim() != 3:
+        raise ValueError(f"q must be [N, heads, D], got {tuple(q.shape)}")
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+
+
+def qk_norm_rope_varlen(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], offsets: torch.Tensor, *,
+                        inv_freq: torch.Tensor, q_weight=None, k_weight=None, eps: float = 1e-6,
+                        interleaved: bool = False, past=None, positions=None, kv_begin=None, q_out=None, k_out=None,
+                        v_out=None, dev_status=None):
+    """Per-head RMS norm of q and k, rotary positions, and the write of the new keys and values into
+    the cache (gdn_qk_norm_rope_varlen).
+
+    q [N, H, D], k, v [N, HK, D] (v may be None), with contiguous heads and any token and head strides;
+    offsets int32 [B+1]; inv_freq fp32 [rot/2]; q_weight, k_weight fp32 [D] or None (ones).  Token i of
+    sequence b has position positions[b] + i (positions int32 [B], default past) and, with kv_begin
+    (int64 [B]), goes to row kv_begin[b] + past[b] + i of k_out and v_out [rows, HK, D]; without
+    kv_begin to the row of its own index.  q_out may be q; outputs not given are allocated (k_out and
+    v_out only without kv_begin).  Returns (q_out, k_out, v_out)."""
+    _need_gpu(q)
+    N, H, D = q.shape
+    HK = k.shape[1]
+    B = offsets.numel() - 1
+    if k_out is None and kv_begin is not None:
+        raise ValueError("k_out is required with kv_begin")
+    if q_out is None:
+        q_out = torch.empty((N, H, D), dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((N, HK, D), dtype=q.dtype, device=q.device)
+    if v is None:
+        v_out = None
+    elif v_out is None:
+        if kv_begin is not None:
+            raise ValueError("v_out is required with kv_begin")
+        v_out = torch.empty((N, HK, D), dtype=q.dtype, device=q.device)
+    rows = k_out.shape[0]
+    qp, qs = _head_view(q, H, D, q, "q")
+    kp, ks = _head_view(k, HK, D, q, "k")
+    qop, qos = _head_view(q_out, H, D, q, "q_out")
+    kop, kos = _head_view(k_out, HK, D, q, "k_out")
+    if k.shape[0] != N or q_out.shape[0] != N:
+        raise ValueError("q, k and q_out must have one row per token")
+    if v is not None:
+        vp, vs = _head_view(v, HK, D, q, "v")
+        vop, vos = _head_view(v_out, HK, D, q, "v_out")
+        if v.shape[0] != N or v_out.shape[0] != rows:
+            raise ValueError("v must have one row per token and v_out as many rows as k_out")
+    else:
+        vp, vs, vop, vos = None, (0, 0), None, (0, 0)
+    half = inv_freq.numel()
+    d = _abi.RopeDesc(B, N, H, HK, D, 2 * half, _code(q, "q"), _abi.ROPE_INTERLEAVED if interleaved else 0, eps, 0,
+                      rows, qs, ks, vs, qos, kos, vos)
+    st = lib().gdn_qk_norm_rope_varlen(
+        ctypes.byref(d), qp, kp, vp, _flat(inv_freq, half, torch.float32, q, "inv_freq"),
+        _flat(q_weight, D, torch.float32, q, "q_weight"), _flat(k_weight, D, torch.float32, q, "k_weight"),
+        _flat(offsets, B + 1, torch.int32, q, "offsets"), _flat(past, B, torch.int32, q, "past"),
+        _flat(positions, B, torch.int32, q, "positions"), _flat(kv_begin, B, torch.int64, q, "kv_begin"), qop, kop, vop,
+        _flat(dev_status, 1, torch.int32, q, "dev_status"), _stream(q.device))
+    _check(st, "gdn_qk_norm_rope_varlen")
+    return q_out, k_out, v_out
+
+
+def _attention(q, prefix_k, prefix_v, k, v, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse, workspace,
+               dev_status, where):
+    _need_gpu(q)
+    N, H, D = q.shape
+    HK = k.shape[1]
+    B = offsets.numel() - 1
+    if out is None:
+        out = torch.empty((N, H, D), dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((N, H), dtype=torch.float32, device=q.device)
+    qp, qs = _head_view(q, H, D, q, "q")
+    op, os_ = _head_view(out, H, D, q, "out")
+    kp, ks = _head_view(k, HK, D, q, "k")
+    vp, vs = _head_view(v, HK, D, q, "v")
+    rows = k.shape[0]
+    if v.shape[0] != rows or out.shape[0] != N:
+        raise ValueError("k and v must have the same rows, and out one row per token")
+    if prefix_k is not None:
+        pkp, pks = _head_view(prefix_k, HK, D, q, "prefix_k")
+        pvp, pvs = _head_view(prefix_v, HK, D, q, "prefix_v")
+        prefix = prefix_k.shape[0]
+        if prefix_v.shape[0] != prefix:
+            raise ValueError("prefix_k and prefix_v must have the same rows")
+    else:
+        pkp, pks, pvp, pvs, prefix = None, (0, 0), None, (0, 0), 0
+    d = _abi.AttnDesc(B, N, H, HK, D, N if max_q is None else max_q, _code(q, "q"), 0, scale, prefix, rows, qs, ks, vs,
+                      os_, pks, pvs)
+    ref = ctypes.byref(d)
+    L = lib()
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        _check(L.gdn_attention_workspace_bytes(ref, ctypes.byref(n)), "gdn_attention_workspace_bytes")
+        if n.value:
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+    ws, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace, "workspace"), workspace.nbytes)
+    tail = (_flat(offsets, B + 1, torch.int32, q, "offsets"), _flat(kv_begin, B, torch.int64, q, "kv_begin"),
+            _flat(kv_len, B, torch.int32, q, "kv_len"), op, _flat(lse, N * H, torch.float32, q, "lse"), ws, ws_bytes,
+            _flat(dev_status, 1, torch.int32, q, "dev_status"), _stream(q.device))
+    if prefix_k is None:
+        st = L.gdn_attention_varlen(ref, qp, kp, vp, *tail)
+    else:
+        st = L.gdn_attention_prefix_varlen(ref, qp, pkp, pvp, kp, vp, *tail)
+    _check(st, where)
+    return out, lse
+
+
+def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, *, kv_len=None,
+                     kv_begin=None, max_q: Optional[int] = None, scale: float = 0.0, out=None, lse=None,
+                     return_lse: bool = False, workspace=None, dev_status=None):
+    """Causal attention of packed sequences with grouped heads (gdn_attention_varlen).
+
+    q [N, H, D]; k, v [rows, HK, D], with contiguous heads and any row and head strides; offsets int32
+    [B+1].  The keys of sequence b are rows kv_begin[b] .. kv_begin[b] + kv_len[b] - 1 (int64 [B], int32
+    [B]), its own new tokens last; without them row t belongs to token t.  max_q is the longest
+    sequence's token count or any larger number (default N: correct, with idle blocks).  scale 0 is
+    1/sqrt(D).  Returns (out [N, H, D], lse [N, H] fp32, or None unless asked for)."""
+    return _attention(q, None, None, k, v, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse, workspace,
+                      dev_status, "gdn_attention_varlen")
+
+
+def attention_prefix_varlen(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor, k: torch.Tensor,
+                            v: torch.Tensor, offsets: torch.Tensor, *, kv_len=None, kv_begin=None,
+                            max_q: Optional[int] = None, scale: float = 0.0, out=None, lse=None,
+                            return_lse: bool = False, workspace=None, dev_status=None):
+    """attention_varlen where every sequence's keys start with the rows of prefix_k, prefix_v
+    [P, HK, D], read once for the whole batch (gdn_attention_prefix_varlen); kv_len counts a sequence's own
+    rows only."""
+    return _attention(q, prefix_k, prefix_v, k, v, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse,
+                      workspace, dev_status, "gdn_attention_prefix_varlen")
+
+
+def attention_workspace_bytes(q: torch.Tensor, B: int, *, HK: int, max_q: int, kv_rows: int, prefix_len: int = 0) -> int:
+    """Bytes of device scratch attention_varlen (prefix_len 0) or attention_prefix_varlen takes as
+    `workspace` for queries like q; it allocates them itself when the caller keeps none."""
+    N, H, D = q.shape
+    d = _abi.AttnDesc(B, N, H, HK, D, max_q, _code(q, "q"), 0, 0.0, prefix_len, kv_rows)
+    n = ctypes.c_size_t(0)
+    _check(lib().gdn_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)), "gdn_attention_workspace_bytes")
+    return int(n.value)

@@ -18,6 +18,7 @@ F32, BF16, F16 = 0, 1, 2
 # flags
 CONV_SILU = 1
 L2NORM, SOFTPLUS, SIGMOID, NO_RETRIEVE, GATE_PER_KEY = 1, 2, 4, 8, 16
+ROPE_INTERLEAVED = 1
 # gdn_path
 PATH_AUTO, PATH_DECODE, PATH_SEQ, PATH_CHUNK = 0, 1, 2, 3
 PATH_NAMES = {PATH_AUTO: "auto", PATH_DECODE: "decode", PATH_SEQ: "seq", PATH_CHUNK: "chunk"}
@@ -35,6 +36,10 @@ EXPORTS = (
     "gdn_scan_varlen_noalloc",
     "gdn_scan_workspace_bytes",
     "gdn_decode_step",
+    "gdn_qk_norm_rope_varlen",
+    "gdn_attention_varlen",
+    "gdn_attention_prefix_varlen",
+    "gdn_attention_workspace_bytes",
     "gdn_status_string",
     "gdn_abi_version",
 )
@@ -80,6 +85,50 @@ class QKVStreams(ctypes.Structure):
     ]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("HK", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("rot", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("cache_rows", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64 * 2),
+        ("k_stride", ctypes.c_int64 * 2),
+        ("v_stride", ctypes.c_int64 * 2),
+        ("q_out_stride", ctypes.c_int64 * 2),
+        ("k_out_stride", ctypes.c_int64 * 2),
+        ("v_out_stride", ctypes.c_int64 * 2),
+    ]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("HK", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("max_q", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("scale", ctypes.c_float),
+        ("prefix_len", ctypes.c_int32),
+        ("kv_rows", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64 * 2),
+        ("k_stride", ctypes.c_int64 * 2),
+        ("v_stride", ctypes.c_int64 * 2),
+        ("out_stride", ctypes.c_int64 * 2),
+        ("prefix_k_stride", ctypes.c_int64 * 2),
+        ("prefix_v_stride", ctypes.c_int64 * 2),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -119,6 +168,14 @@ def lib() -> ctypes.CDLL:
         L.gdn_decode_step.restype = st
         L.gdn_scan_workspace_bytes.argtypes = [ctypes.POINTER(ScanDesc), ctypes.POINTER(ctypes.c_size_t)]
         L.gdn_scan_workspace_bytes.restype = st
+        L.gdn_qk_norm_rope_varlen.argtypes = [ctypes.POINTER(RopeDesc)] + [vp] * 15
+        L.gdn_qk_norm_rope_varlen.restype = st
+        L.gdn_attention_varlen.argtypes = [ctypes.POINTER(AttnDesc)] + [vp] * 9 + [ctypes.c_size_t, vp, vp]
+        L.gdn_attention_varlen.restype = st
+        L.gdn_attention_prefix_varlen.argtypes = [ctypes.POINTER(AttnDesc)] + [vp] * 11 + [ctypes.c_size_t, vp, vp]
+        L.gdn_attention_prefix_varlen.restype = st
+        L.gdn_attention_workspace_bytes.argtypes = [ctypes.POINTER(AttnDesc), ctypes.POINTER(ctypes.c_size_t)]
+        L.gdn_attention_workspace_bytes.restype = st
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_abi_version.argtypes = []

@@ -119,6 +119,46 @@ gdn_status scan_varlen_scratch(const gdn_scan_desc* d, const void* qkv, const fl
                                ScratchFn scratch, size_t scratch_bytes, int32_t* dev_status, int32_t* path_used,
                                hipStream_t stream);
 
+// Rows of heads: element (row, head, e) at p + row*row + head*head + e (strides in elements).
+struct HeadRows {
+    void* p;
+    long long row, head;
+};
+
+struct RopeLaunch {
+    HeadRows q, k, v, q_out, k_out, v_out;
+    const float* inv_freq;
+    const float* q_weight;
+    const float* k_weight;
+    const int32_t* offsets;
+    const int32_t* past;
+    const int32_t* positions;
+    const int64_t* kv_begin;
+    int32_t* dev_status;
+    long long cache_rows;
+    int B, N, H, HK, D, rot;
+    int dtype;
+    bool interleaved;
+    float eps;
+};
+hipError_t launch_rope(const RopeLaunch& a, hipStream_t stream);
+
+struct AttnLaunch {
+    HeadRows q, k, v, pk, pv, out;
+    float* lse;
+    const int32_t* offsets;
+    const int64_t* kv_begin;  // NULL together with kv_len: keys packed like the queries
+    const int32_t* kv_len;
+    int32_t* dev_status;
+    void* workspace;
+    long long kv_rows;
+    int B, N, H, HK, D, max_q, prefix_len;
+    int dtype;
+    float scale;  // already resolved
+};
+hipError_t launch_attention(const AttnLaunch& a, hipStream_t stream);
+size_t attention_workspace_bytes(const AttnLaunch& a);
+
 // Longest sequence the DECODE kernel carries column by column with staged token operands; AUTO
 // takes DECODE while the average sequence is no longer than this.
 constexpr int kDecodeShortTokens = 8;

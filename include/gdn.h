@@ -15,7 +15,12 @@
  *                         streams with their own row strides
  *   gdn_scan_varlen_noalloc   gdn_scan_varlen with the library's own device scratch, for callers
  *                         that cannot allocate
- * plus gdn_scan_workspace_bytes, gdn_status_string and gdn_abi_version.
+ * The softmax-attention layers that stand between the recurrent ones, over the same packed batches:
+ *   gdn_qk_norm_rope_varlen   per-head RMS norm of q and k, rotary positions, and the write of the
+ *                         new keys and values into the cache
+ *   gdn_attention_varlen  causal grouped-head attention of each sequence over its rows of the cache
+ *   gdn_attention_prefix_varlen   the same for a batch whose sequences all start with one prefix
+ * plus gdn_scan_workspace_bytes, gdn_attention_workspace_bytes, gdn_status_string and gdn_abi_version.
  *
  * Sources (docs.rs source pages): "onnxruntime-ep-mlx 0.31.1 src/ops/paged_ssm.rs" -- kernel strings
  * CONV, DELTA_PREPARE and DELTA, the capture strings, host functions conv(), delta() and the claim
@@ -350,6 +355,109 @@ gdn_status gdn_scan_varlen_noalloc(const gdn_scan_desc *desc, const void *qkv, c
 /* Workspace bytes gdn_scan_varlen needs for `desc` (with its path resolved as AUTO would);
  * 0 when the resolved path needs none.  Returns the same argument errors as gdn_scan_varlen. */
 gdn_status gdn_scan_workspace_bytes(const gdn_scan_desc *desc, size_t *bytes);
+
+/* ------------------------------------------------------------------------------------------------
+ * gdn_qk_norm_rope_varlen -- what a softmax-attention layer does to its projections before the
+ * attention, in one launch.  For token t of sequence b (i = t - offsets[b]), every query and key
+ * head x (a D-vector) with its weight w:
+ *     y[e] = x[e] * w[e] / sqrt(mean(x^2) + eps)
+ *     angle_j = (positions[b] + i) * inv_freq[j],  j < rot/2
+ *     (y[lo], y[hi]) <- (y[lo]*cos - y[hi]*sin, y[lo]*sin + y[hi]*cos)  with lo = j, hi = j + rot/2,
+ *                       or lo = 2j, hi = 2j + 1 with GDN_ROPE_INTERLEAVED; elements from rot on stay
+ *     q_out[t] = the queries;  k_out[row], v_out[row] = the keys and the values as they are
+ *     row = kv_begin[b] + past[b] + i, or t where kv_begin is NULL
+ * Norms and rotations are fp32, the angle and its reduction to one turn are fp64 (an fp32 angle loses
+ * the fraction of a turn at far positions); each output is rounded once.
+ *
+ * Tensors (element (row, head, e) at row*stride[0] + head*stride[1] + e, strides in elements):
+ *   q [N, H, D], k, v [N, HK, D]  dtype      required unless N == 0; v NULL = values not written
+ *   inv_freq  [rot/2] fp32                   required when rot > 0
+ *   q_weight, k_weight [D] fp32              NULL = ones
+ *   q_out [N, H, D] dtype, may be q itself (same strides)   required unless N == 0
+ *   k_out, v_out [cache_rows, HK, D] dtype   required unless N == 0; v_out NULL iff v is
+ *   past, positions [B] int32                NULL = zeros; positions NULL = past
+ *   kv_begin  [B] int64                      NULL = rows are token indices (past moves positions only)
+ * Constraints: B >= 1, N >= 0, H, HK >= 1, 1 <= D <= 256, 0 <= rot <= D even, D, every stride and
+ * every base a multiple of 16 bytes (GDN_ERR_ALIGN), strides not negative.  q_out, k_out and v_out do
+ * not overlap each other or (q_out = q aside) the inputs, and no two tokens name one row.
+ * Malformed offsets, and rows outside [0, cache_rows) of a sequence with tokens, write nothing
+ * (GDN_ERR_OFFSETS in *dev_status).
+ * ---------------------------------------------------------------------------------------------- */
+#define GDN_ROPE_INTERLEAVED 1u
+
+typedef struct gdn_rope_desc {
+    int32_t B, N, H, HK, D, rot;
+    int32_t dtype;      /* gdn_dtype of q, k, v and the outputs */
+    uint32_t flags;     /* GDN_ROPE_INTERLEAVED */
+    float eps;          /* >= 0 */
+    int32_t reserved;   /* 0 */
+    int64_t cache_rows; /* rows of k_out and v_out */
+    int64_t q_stride[2], k_stride[2], v_stride[2];
+    int64_t q_out_stride[2], k_out_stride[2], v_out_stride[2];
+} gdn_rope_desc;
+
+gdn_status gdn_qk_norm_rope_varlen(const gdn_rope_desc *desc, const void *q, const void *k, const void *v,
+                                   const float *inv_freq, const float *q_weight, const float *k_weight,
+                                   const int32_t *offsets, const int32_t *past, const int32_t *positions,
+                                   const int64_t *kv_begin, void *q_out, void *k_out, void *v_out,
+                                   int32_t *dev_status, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * gdn_attention_varlen -- causal softmax attention of packed sequences with grouped heads.  Sequence
+ * b has T = offsets[b+1] - offsets[b] new tokens, whose keys and values are the last T of its
+ * n = kv_len[b] cache rows kv_begin[b] .. kv_begin[b] + n - 1.  Token i of it, query head h, reads
+ * key head h / (H/HK):
+ *     out = sum_j p_j v_j,  p = softmax_j(scale * q.k_j),  j <= n - T + i
+ *     lse = log sum_j exp(scale * q.k_j)
+ * A token that sees no key (n < T) gets out = 0 and lse = -inf.  Rows a token does not see
+ * contribute nothing, whatever they hold.
+ *
+ * gdn_attention_prefix_varlen -- the same where every sequence's keys start with one shared run of
+ * prefix_len rows, kept apart from the cache and read once for all: the sum runs over all of
+ * prefix_k, prefix_v and then over the sequence's own rows as above.
+ *
+ * Scores, softmax statistics and sums are fp32; with half-precision I/O the probabilities are rounded
+ * to that type as operands of the second product (the sum that divides them is of the unrounded ones).
+ *
+ * Tensors (strides as above):
+ *   q, out [N, H, D] dtype             required unless N == 0
+ *   k, v [kv_rows, HK, D] dtype        required unless kv_rows == 0
+ *   prefix_k, prefix_v [prefix_len, HK, D] dtype   required unless prefix_len == 0
+ *   lse [N, H] fp32                    NULL = not produced
+ *   kv_begin [B] int64, kv_len [B] int32   both NULL = the keys are packed like the queries (row t
+ *                                      belongs to token t)
+ *   workspace   device scratch of ws_bytes >= gdn_attention_workspace_bytes(desc)
+ * Constraints: B >= 1, N >= 0, H, HK >= 1, H % HK == 0, 1 <= D <= 256, D, every stride and every base a
+ * multiple of 16 bytes (GDN_ERR_ALIGN), strides not negative, rows of k and v at most 4 MiB apart
+ * (GDN_ERR_OVERFLOW), max_q >= 1 unless N == 0.  scale == 0 selects 1/sqrt(D); any other value is
+ * applied as given.  Malformed offsets, a sequence of more than max_q tokens and a key run outside
+ * [0, kv_rows) write nothing (GDN_ERR_OFFSETS in *dev_status).
+ * ---------------------------------------------------------------------------------------------- */
+typedef struct gdn_attn_desc {
+    int32_t B, N, H, HK, D;
+    int32_t max_q;      /* tokens of the longest sequence, or any larger number */
+    int32_t dtype;      /* gdn_dtype of q, k, v and out */
+    uint32_t flags;     /* 0 */
+    float scale;        /* 0 selects 1/sqrt(D) */
+    int32_t prefix_len; /* rows of prefix_k and prefix_v; 0 for gdn_attention_varlen */
+    int64_t kv_rows;    /* rows of k and v */
+    int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];
+    int64_t prefix_k_stride[2], prefix_v_stride[2];
+} gdn_attn_desc;
+
+gdn_status gdn_attention_varlen(const gdn_attn_desc *desc, const void *q, const void *k, const void *v,
+                                const int32_t *offsets, const int64_t *kv_begin, const int32_t *kv_len, void *out,
+                                float *lse, void *workspace, size_t ws_bytes, int32_t *dev_status,
+                                hipStream_t stream);
+
+gdn_status gdn_attention_prefix_varlen(const gdn_attn_desc *desc, const void *q, const void *prefix_k,
+                                       const void *prefix_v, const void *k, const void *v, const int32_t *offsets,
+                                       const int64_t *kv_begin, const int32_t *kv_len, void *out, float *lse,
+                                       void *workspace, size_t ws_bytes, int32_t *dev_status, hipStream_t stream);
+
+/* Workspace bytes the attention calls need for `desc`; 0 when none is needed.  Returns the same
+ * descriptor errors as the calls. */
+gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc *desc, size_t *bytes);
 
 /* Static description of a status code; never NULL. */
 const char *gdn_status_string(gdn_status status);

@@ -1,0 +1,328 @@
+"""GPU tests of gdn_attention_varlen and gdn_attention_prefix_varlen against a plain 64-bit attention:
+types, head widths and layouts, lengths around every tile edge, rows without keys, values in places
+that are masked, long runs cut in parts, malformed calls, streams and graphs."""
+import random
+
+import pytest
+
+from attn_util import DT, assert_within, attention_ref, layout
+from gpu_util import bits, ensure_built, require_gpu, sentinel
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    ensure_built()
+    return require_gpu()
+
+
+class Case:
+    """Seeded inputs on the CPU and the device: lengths are (new tokens, cache rows) per sequence."""
+
+    def __init__(self, torch, kind, HK, G, D, lengths, prefix=0, heads_major=False, seed=1, padded_q=False):
+        self.torch, self.kind, self.lengths = torch, kind, lengths
+        gen = torch.Generator().manual_seed(seed)
+        order = list(range(len(lengths)))
+        random.Random(seed).shuffle(order)
+        self.T, self.n = [t for t, _ in lengths], [n for _, n in lengths]
+        self.begin, rows = layout(lengths, order=order)
+        self.N, self.H = sum(self.T), HK * G
+
+        def normal(*shape, scale=1.0):
+            return (scale * torch.randn(shape, generator=gen)).to(DT[kind])
+
+        self.q = normal(self.N, self.H, D, scale=1.5)
+        self.kv = [normal(HK, rows, D).permute(1, 0, 2) if heads_major else normal(rows, HK, D) for _ in range(2)]
+        # rows of no sequence hold NaN
+        used = torch.zeros(rows, dtype=torch.bool)
+        for b, (_, n) in enumerate(lengths):
+            used[self.begin[b]:self.begin[b] + n] = True
+        for x in self.kv:
+            x[~used] = float("nan")
+        self.prefix = [normal(prefix, HK, D) for _ in range(2)] if prefix else None
+        self.padded_q = padded_q
+
+    def dev(self):
+        t, dev = self.torch, "cuda"
+
+        def move(x):  # keeps the strides
+            return x.permute(1, 0, 2).contiguous().to(dev).permute(1, 0, 2) if not x.is_contiguous() else x.to(dev)
+
+        off = [0]
+        for n in self.T:
+            off.append(off[-1] + n)
+        q = self.q.to(dev)
+        if self.padded_q:  # a part of a wider row
+            wide = t.full((self.N, self.H + 3, self.q.shape[2]), float("nan"), dtype=q.dtype, device=dev)
+            wide[:, 1:1 + self.H] = q
+            q = wide[:, 1:1 + self.H]
+        return dict(q=q, k=move(self.kv[0]), v=move(self.kv[1]), offsets=t.tensor(off, dtype=t.int32, device=dev),
+                    kv_begin=t.tensor(self.begin, dtype=t.int64, device=dev),
+                    kv_len=t.tensor(self.n, dtype=t.int32, device=dev), max_q=max(self.T + [1]), return_lse=True)
+
+    def call(self, x=None, **kw):
+        import gated_delta_rule_varlen_amd as gdn
+
+        x = {**(x or self.dev()), **kw}
+        q, k, v, off = (x.pop(n) for n in ("q", "k", "v", "offsets"))
+        if self.prefix is None:
+            return gdn.attention_varlen(q, k, v, off, **x)
+        return gdn.attention_prefix_varlen(q, *(p.cuda() for p in self.prefix), k, v, off, **x)
+
+    def ref(self, **kw):
+        p = self.prefix or (None, None)
+        return attention_ref(self.q, *self.kv, self.T, self.begin, self.n, kind=self.kind, prefix_k=p[0], prefix_v=p[1],
+                             **kw)
+
+    def check(self, what):
+        print(f"[case] {what} {self.kind} q {tuple(self.q.shape)} HK {self.kv[0].shape[1]} lengths {self.lengths[:12]}",
+              flush=True)
+        out, lse = self.call()
+        self.torch.cuda.synchronize()
+        o, l, o_tol, l_tol = self.ref()
+        assert out.dtype == DT[self.kind] and lse.dtype == self.torch.float32
+        assert_within(out, o, o_tol, what + " out")
+        assert_within(lse, l, l_tol, what + " lse")
+
+
+KINDS = ["bf16", "f16", "f32"]
+# new tokens and cache rows around the edges of 32-, 64-, 128- and 256-key tiles, empty ones among them
+DECODE = [(1, n) for n in (1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 300)] + [(0, 7), (0, 0), (1, 515)]
+BLOCKS = [(4, 4), (5, 36), (1, 1), (0, 0), (9, 200), (2, 130), (7, 64), (3, 65), (6, 512)]
+PROMPTS = [(130, 130), (1, 1), (0, 0), (64, 64), (65, 65), (300, 300), (31, 95), (33, 161), (128, 500)]
+NO_KEYS = [(3, 0), (4, 2), (1, 0), (40, 7), (1, 9), (2, 2), (0, 3)]
+SETS = {"decode": DECODE, "blocks": BLOCKS, "prompts": PROMPTS, "no_keys": NO_KEYS}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("HK,G,D", [(2, 4, 64), (2, 4, 128), (1, 8, 256), (2, 2, 32), (1, 3, 96), (3, 1, 72), (1, 5, 80),
+                                    (1, 16, 192), (2, 1, 8)])
+@pytest.mark.parametrize("name", SETS)
+def test_lengths_types_and_widths(torch, kind, HK, G, D, name):
+    Case(torch, kind, HK, G, D, SETS[name], seed=D + G).check(f"{name} D{D}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("HK,G,D,prefix", [(2, 4, 64, 1001), (2, 4, 128, 1), (1, 8, 256, 130), (1, 3, 72, 64), (1, 16, 96, 700)])
+@pytest.mark.parametrize("name", ["decode", "blocks", "prompts", "no_keys"])
+def test_shared_prefix(torch, kind, HK, G, D, prefix, name):
+    Case(torch, kind, HK, G, D, SETS[name], prefix=prefix, seed=prefix).check(f"prefix {prefix} {name} D{D}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("HK,G,D,lengths", [
+    (1, 4, 64, [(1, 5000)]),            # one sequence: its keys are cut in parts
+    (2, 8, 256, [(5, 3333), (2, 40)]),
+    (1, 2, 128, [(300, 4000)]),         # several row tiles over a long cache
+    (4, 16, 64, [(9, 700), (1, 900)]),  # more rows than one tile in a short call
+    (1, 1, 128, [(1, 64 * i + 3) for i in range(70)]),
+    (2, 1, 32, [(1, 1)] * 300),         # more sequences than a block has threads
+    (1, 7, 64, [(700, 700), (5, 1500)]),
+])
+def test_long_and_many(torch, kind, HK, G, D, lengths):
+    Case(torch, kind, HK, G, D, lengths, seed=5).check("long")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("prefix", [0, 77])
+def test_layouts(torch, kind, prefix):
+    """Heads-major caches and queries that are part of a wider row give the bits of the plain layout."""
+    for lengths in (DECODE, PROMPTS):
+        same = []
+        for heads_major in (False, True):
+            c = Case(torch, kind, 2, 4, 64, lengths, prefix=prefix, seed=3)
+            if heads_major:
+                c.kv = [x.permute(1, 0, 2).contiguous().permute(1, 0, 2) for x in c.kv]
+                c.padded_q = True
+            same.append(c.call())
+        torch.cuda.synchronize()
+        for a, b in zip(*same):
+            assert (bits(a) == bits(b)).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_packed_keys(torch, kind):
+    """Without kv_begin and kv_len the keys are packed like the queries."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    T = [5, 0, 130, 1, 64]
+    gen = torch.Generator().manual_seed(9)
+    q, k, v = (torch.randn((sum(T), h, 64), generator=gen).to(DT[kind]) for h in (8, 2, 2))
+    off = [0, 5, 5, 135, 136, 200]
+    out, lse = gdn.attention_varlen(q.cuda(), k.cuda(), v.cuda(), torch.tensor(off, dtype=torch.int32).cuda(),
+                                    return_lse=True)
+    o, l, ot, lt = attention_ref(q, k, v, T, off, T, kind=kind)
+    assert_within(out, o, ot, "packed out")
+    assert_within(lse, l, lt, "packed lse")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("HK,G,D,lengths,prefix", [
+    (1, 4, 64, [(6, 40), (3, 3)], 0),
+    (2, 2, 128, [(70, 170), (200, 200)], 0),
+    (1, 4, 256, [(40, 40)], 33),
+])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_masked_rows_hold_anything(torch, kind, HK, G, D, lengths, prefix, value):
+    """The last token's key and value reach no earlier token, even where they are not finite."""
+    c = Case(torch, kind, HK, G, D, lengths, prefix=prefix, seed=8)
+    for b, (_, n) in enumerate(lengths):
+        for x in c.kv:
+            x[c.begin[b] + n - 1] = value
+    out, lse = c.call()
+    o, l, ot, lt = c.ref()
+    keep = torch.ones(c.N, dtype=torch.bool)
+    end = 0
+    for t in c.T:
+        end += t
+        keep[end - 1] = False
+    assert_within(out[keep.cuda()], o[keep], ot[keep], "masked out")
+    assert_within(lse[keep.cuda()], l[keep], lt[keep], "masked lse")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lengths", [[(1, 900), (1, 3)], [(5, 300)], [(150, 400)]])
+def test_sharp_and_growing_scores(torch, kind, lengths):
+    """Scores that span hundreds and grow along the keys: the running maximum moves at every tile."""
+    c = Case(torch, kind, 1, 4, 64, lengths, seed=12)
+    for b, (_, n) in enumerate(lengths):
+        ramp = torch.linspace(0.2, 6.0, n)[:, None, None]
+        rows = slice(c.begin[b], c.begin[b] + n)
+        c.kv[0][rows] = (c.kv[0][rows].float() * ramp + ramp).to(DT[kind])
+    c.q = (c.q.float() * 2 + 1).to(DT[kind])
+    c.check("growing")
+
+
+@pytest.mark.parametrize("scale", [0.0, 0.03, -0.2])
+def test_scale(torch, scale):
+    c = Case(torch, "f32", 2, 2, 64, [(3, 50), (70, 90), (1, 200)], seed=14)
+    out, lse = c.call(scale=scale)
+    o, l, ot, lt = c.ref(scale=scale or None)
+    assert_within(out, o, ot, "scaled out")
+    assert_within(lse, l, lt, "scaled lse")
+
+
+def _expect_untouched(torch, c, status=-9, **kw):
+    x = c.dev()
+    out, lse = sentinel((c.N, c.H, c.q.shape[2]), c.kind), sentinel((c.N, c.H), "f32")
+    want = bits(out).copy(), bits(lse).copy()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for name, at, value in kw.pop("spoil", ()):
+        x[name][at] = value
+    c.call(x, out=out, lse=lse, dev_status=st, **kw)
+    torch.cuda.synchronize()
+    assert st.item() == status
+    assert ((bits(out) == want[0]).all() and (bits(lse) == want[1]).all()) == (status != 0)
+
+
+@pytest.mark.parametrize("prefix", [0, 40])
+@pytest.mark.parametrize("lengths", [[(1, 70), (1, 5), (1, 300)], [(100, 150), (0, 4), (230, 260)]])
+@pytest.mark.parametrize("what", ["ok", "start", "end", "falling", "longest", "begin", "run", "far", "length"])
+def test_malformed_calls_write_nothing(torch, lengths, prefix, what):
+    c = Case(torch, "bf16", 2, 4, 64, lengths, prefix=prefix, seed=2)
+    rows = c.kv[0].shape[0]
+    spoil = dict(ok=[], start=[("offsets", 0, 1)], end=[("offsets", 3, c.N + 1)], falling=[("offsets", 1, c.N + 5)],
+                 longest=[], begin=[("kv_begin", 1, -1)], run=[("kv_begin", 2, rows - c.n[2] + 1)],
+                 far=[("kv_begin", 0, 1 << 62)], length=[("kv_len", 0, -1)])[what]
+    kw = dict(max_q=max(c.T) - 1) if what == "longest" else {}
+    if what == "longest" and max(c.T) == 1:
+        pytest.skip("max_q 0 is refused on the host")
+    _expect_untouched(torch, c, status=0 if what == "ok" else -9, spoil=spoil, **kw)
+
+
+def test_calls_without_tokens(torch):
+    c = Case(torch, "bf16", 2, 2, 64, [(0, 5), (0, 0)], seed=2)
+    st = torch.ones(1, dtype=torch.int32, device="cuda")
+    out, lse = c.call(dev_status=st)
+    torch.cuda.synchronize()
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4) and st.item() == 0
+
+
+def test_binding_refuses_what_it_cannot_describe(torch):
+    c = Case(torch, "bf16", 2, 4, 64, [(1, 9), (2, 5)], seed=2)
+    x = c.dev()
+    half = x["k"].half()
+    for bad, err in ((dict(k=half), TypeError), (dict(k=x["k"][:, :, :32]), ValueError), (dict(k=x["k"][:5]), ValueError),
+                     (dict(kv_len=x["kv_len"].long()), TypeError), (dict(kv_begin=x["kv_begin"][:1]), ValueError),
+                     (dict(offsets=x["offsets"].cpu()), ValueError), (dict(v=x["v"].cpu()), ValueError),
+                     (dict(q=x["q"].transpose(1, 2)), ValueError), (dict(lse=x["kv_begin"]), TypeError),
+                     (dict(out=x["q"][:2]), ValueError)):
+        with pytest.raises(err):
+            c.call({**x, **bad})
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_offsets_past_32_bits(torch, kind):
+    """A run at the end of a cache of more than 2^32 bytes and 2^31 elements."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    HK, D, n = 4, 64, 700
+    rows = (1 << 31) // (HK * D) + 300  # the run starts below element 2^31 and ends past it
+    gen = torch.Generator().manual_seed(4)
+    q = torch.randn((3, 8, D), generator=gen).to(DT[kind])
+    k, v = (torch.randn((n, HK, D), generator=gen).to(DT[kind]) for _ in range(2))
+    cache = [torch.empty((rows, HK, D), dtype=DT[kind], device="cuda") for _ in range(2)]
+    for c, x in zip(cache, (k, v)):
+        c[rows - n:] = x.cuda()
+    out, lse = gdn.attention_varlen(q.cuda(), *cache, torch.tensor([0, 3], dtype=torch.int32).cuda(),
+                                    kv_begin=torch.tensor([rows - n]).cuda(),
+                                    kv_len=torch.tensor([n], dtype=torch.int32).cuda(), max_q=3, return_lse=True)
+    o, l, ot, lt = attention_ref(q, k, v, [3], [0], [n], kind=kind)
+    assert_within(out, o, ot, "far out")
+    assert_within(lse, l, lt, "far lse")
+
+
+@pytest.mark.parametrize("prefix", [0, 500])
+@pytest.mark.parametrize("lengths", [[(1, 3000), (1, 40)], [(200, 900), (3, 70)]])
+def test_repeats_streams_and_graphs(torch, prefix, lengths):
+    """The same bits on a second run, on another stream, and from replays of a captured graph whose
+    inputs change between them."""
+    c = Case(torch, "bf16", 2, 4, 128, lengths, prefix=prefix, seed=6)
+    x = c.dev()
+    first = c.call(x)
+    pre = [p.cuda() for p in c.prefix] if prefix else None
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        second = c.call(x)
+    torch.cuda.synchronize()
+    for a, b in zip(first, second):
+        assert (bits(a) == bits(b)).all()
+
+    import gated_delta_rule_varlen_amd as gdn
+
+    out, lse = torch.empty_like(first[0]), torch.empty_like(first[1])
+    args = [x["q"]] + (pre or []) + [x["k"], x["v"], x["offsets"]]
+    kw = {n: x[n] for n in ("kv_begin", "kv_len", "max_q")}
+    f = gdn.attention_prefix_varlen if prefix else gdn.attention_varlen
+    need = gdn.attention_workspace_bytes(x["q"], len(lengths), HK=2, max_q=kw["max_q"], kv_rows=len(x["k"]), prefix_len=prefix)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f(*args, **kw, out=out, lse=lse, workspace=ws)
+    for turn in range(4):
+        x["q"].copy_(c.q.cuda() * (1 + turn))
+        want = f(*args, **kw, return_lse=True)
+        torch.cuda.synchronize()
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (bits(out) == bits(want[0])).all() and (bits(lse) == bits(want[1])).all(), turn
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(torch, seed):
+    r = random.Random(1000 + seed)
+    kind = r.choice(KINDS)
+    HK, G = r.choice([1, 2, 3, 4]), r.choice([1, 2, 3, 4, 5, 8, 16])
+    D = r.choice([32, 64, 72, 80, 96, 128, 192, 256])
+    longest = r.choice([1, 2, 9, 60, 400])
+    B = r.randrange(1, 12)
+    lengths = []
+    for _ in range(B):
+        t = r.randrange(0, longest + 1)
+        lengths.append((t, max(0, t + r.choice([0, 0, -2, r.randrange(700)]))))
+    if sum(t for t, _ in lengths) == 0:
+        lengths[0] = (1, 5)
+    Case(torch, kind, HK, G, D, lengths, prefix=r.choice([0, 0, r.randrange(1, 600)]), seed=seed).check(f"random {seed}")
