@@ -1,120 +1,203 @@
-// gdn_attn.hip -- causal softmax attention of packed sequences with grouped heads, with or without a
-// prefix shared by all sequences (gdn_attention_varlen, gdn_attention_prefix_varlen).
+// gdn_attn.hip -- host side of the softmax attention: which form and tile a call takes, its workspace, and
+// the kernel that joins key parts.  The tile kernels are in gdn_attn.hpp.
 //
-// One wave computes one query row (token, head) in one pass over its keys: 64 keys at a time, one
-// per lane for the scores, then one element of the value row per lane for the products, with the
-// running maximum m and sum l of the softmax (out = sum_j exp(s_j - m) v_j / l, rescaled by
-// exp(m_old - m_new) whenever m grows).
+// Short form (max_q * G rows fit a tile of 32, 64 or 128): decode steps and short blocks, bound by the
+// cache's bytes.  Long form: prompts, bound by the matrix cores.  A shared prefix is one more run of
+// keys for the long form's tiles; for the short form a launch of its own first runs all tokens' rows
+// over the prefix, reading it once for the whole batch.
 #include <hip/hip_runtime.h>
 
-#include <climits>
+#include <algorithm>
 
-#include "gdn_device.hpp"
-#include "gdn_launch.hpp"
+#include "gdn_attn.hpp"
 
 namespace gdn {
 namespace {
 
-constexpr int NT = 64;
-constexpr int MAX_D = 256;
+using namespace attn;
 
-// Offsets, lengths and key runs of the whole call; also the sequence of token t.
-__device__ __forceinline__ bool attn_malformed(const AttnLaunch& a, int t, int& b) {
-    int bad = 0, at_or_below = 0;
-    for (int i = threadIdx.x; i <= a.B; i += NT) {
-        const int o = a.offsets[i];
-        if (i == 0) {
-            bad |= (o != 0);
-        } else {
-            const int n = o - a.offsets[i - 1];
-            bad |= (n < 0) | (n > a.max_q);
-            if (a.kv_len != nullptr) {
-                const long long len = a.kv_len[i - 1], begin = a.kv_begin[i - 1];
-                bad |= (len < 0) | (begin < 0) | (begin > a.kv_rows) | (begin + len > a.kv_rows);
-            } else {
-                bad |= (o > a.kv_rows);
-            }
-        }
-        if (i == a.B) bad |= (o != a.N);
-        at_or_below += (o <= t);
-    }
-    for (int m = 1; m < 64; m <<= 1) at_or_below += __shfl_xor(at_or_below, m);
-    b = at_or_below - 1;
-    return __syncthreads_or(bad) != 0;
-}
+constexpr int kCUs = 256;
+constexpr int kShortRows = 128;
 
-template <typename T>
-__global__ __launch_bounds__(NT) void attn_kernel(AttnLaunch a) {
+// Joins the parts of a row: pieces of a cut run (a chain of workers' slots) and sets [0, sets).  One block of
+// 1 or 4 waves a row (token, head); its waves share the parts.
+template <typename T, int NW>
+__global__ __launch_bounds__(64 * NW) void join_kernel(Args a, int bm, int local_set) {
     using TS = typename T::storage;
-    const int t = blockIdx.x / a.H, h = blockIdx.x - t * a.H, lane = threadIdx.x, hk = h / (a.H / a.HK);
-    int b;
-    const bool malformed = attn_malformed(a, t, b);
-    report_status(a.dev_status, malformed);
-    if (malformed || t >= a.N) return;
-    const int first = a.offsets[b], T_b = a.offsets[b + 1] - first;
-    const long long begin = a.kv_begin != nullptr ? a.kv_begin[b] : first;
-    const int own = (a.kv_len != nullptr ? a.kv_len[b] : T_b) - T_b + (t - first) + 1;  // keys this token sees
-
-    __shared__ float q[MAX_D];
-    for (int e = lane; e < a.D; e += NT)
-        q[e] = to_f32<T>(static_cast<const TS*>(a.q.p)[t * a.q.row + h * a.q.head + e]);
-    __syncthreads();
-
-    float m = -INFINITY, l = 0.0f, o[MAX_D / 64] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto run = [&](const HeadRows& K, const HeadRows& V, long long row0, int n) {
-        const TS* kp = static_cast<const TS*>(K.p) + row0 * K.row + hk * K.head;
-        const TS* vp = static_cast<const TS*>(V.p) + row0 * V.row + hk * V.head;
-        for (int j0 = 0; j0 < n; j0 += 64) {
-            float s = -INFINITY;
-            if (j0 + lane < n) {
-                const TS* row = kp + (j0 + lane) * K.row;
-                s = 0.0f;
-                for (int e = 0; e < a.D; e += 4) {
-                    const f32x4 x = load4<T>(row + e);
-                    for (int i = 0; i < 4; ++i) s = fmaf(q[e + i], x[i], s);
-                }
-                s *= a.scale;
-            }
-            float top = s;
-            for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-            const float m_new = fmaxf(m, top), ref = m_new == -INFINITY ? 0.0f : m_new;
-            const float p = expf(s - ref), w = expf(m - ref);
-            float sum = p;
-            for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
-            l = l * w + sum;
-            m = m_new;
-            for (int i = 0; i < MAX_D / 64; ++i) o[i] *= w;
-            for (int j = 0; j < 64 && j0 + j < n; ++j) {
-                const float pj = __shfl(p, j);
-                for (int i = 0; i < MAX_D / 64; ++i)
-                    if (lane + 64 * i < a.D) o[i] = fmaf(pj, to_f32<T>(vp[(j0 + j) * V.row + lane + 64 * i]), o[i]);
-            }
+    if (*a.status != 0) return;
+    const long long row = blockIdx.x;
+    const int t = (int)(row / a.c.H), h = (int)(row - (long long)t * a.c.H), hk = h / a.G;
+    int worker = -1, pieces = 0;
+    long long slot_row = 0;
+    if (a.row_info != nullptr) {
+        const int2 info = a.row_info[(long long)t * a.c.HK + hk];
+        worker = info.x;
+        if (worker >= 0) {
+            pieces = info.y >> 7;
+            slot_row = (info.y & 127) * a.G + (h - hk * a.G);
+        } else if (a.sets == 0) {
+            return;  // written whole
         }
-    };
-    run(a.pk, a.pv, 0, a.prefix_len);
-    run(a.k, a.v, begin, own);
-    TS* out = static_cast<TS*>(a.out.p) + t * a.out.row + h * a.out.head;
-    for (int i = 0; i < MAX_D / 64; ++i)
-        if (lane + 64 * i < a.D) out[lane + 64 * i] = from_f32<T>(l == 0.0f ? 0.0f : o[i] / l);
-    if (a.lse != nullptr && lane == 0) a.lse[t * a.H + h] = m + logf(l);
+    }
+    const int sets = a.sets - (worker >= 0 && local_set >= 0 ? 1 : 0);  // a cut run left its own set (the last) unused
+    const int parts = pieces + sets, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // the first piece is slot 1 of its worker, the others slot 0 of the following ones
+    auto slot = [&](int p) { return ((long long)(worker + p) * 2 + (p == 0 ? 1 : 0)) * bm + slot_row; };
+    auto ml_of = [&](int p) { return p < pieces ? a.slot_ml[slot(p)] : a.set_ml[(p - pieces) * a.set_rows + row]; };
+    float top = kNoMax;
+    for (int p = lane; p < parts; p += 64) top = fmaxf(top, ml_of(p).x);
+    for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
+    float l = 0.0f;
+    for (int p = lane; p < parts; p += 64) {
+        const float2 ml = ml_of(p);
+        l += ml.y * __builtin_amdgcn_exp2f(ml.x - top);
+    }
+    l = group_sum<64>(l);
+    f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int e = 4 * lane;
+    if (e < a.c.D) {
+#pragma unroll 4
+        for (int p = wave; p < parts; p += NW) {
+            const float w = __builtin_amdgcn_exp2f(ml_of(p).x - top);
+            const float* src = p < pieces ? a.slot_o + slot(p) * a.c.D : a.set_o + ((p - pieces) * a.set_rows + row) * a.c.D;
+            o += w * *reinterpret_cast<const f32x4*>(src + e);
+        }
+    }
+    if constexpr (NW > 1) {
+        __shared__ f32x4 xo[NW][64];
+        xo[wave][lane] = o;
+        __syncthreads();
+        if (wave != 0) return;
+        for (int w = 1; w < NW; ++w) o += xo[w][lane];
+    }
+    if (e < a.c.D) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        TS* out = static_cast<TS*>(a.c.out.p) + t * a.c.out.row + h * a.c.out.head;
+        for (int j = 0; j < 4; ++j) out[e + j] = from_f32<T>(o[j] * inv);
+    }
+    if (a.c.lse != nullptr && threadIdx.x == 0)
+        a.c.lse[row] = l == 0.0f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(l));
 }
 
 template <typename T>
-hipError_t launch(const AttnLaunch& a, hipStream_t stream) {
-    const long long blocks = a.N > 0 ? (long long)a.N * a.H : 1;
-    attn_kernel<T><<<(unsigned)blocks, NT, 0, stream>>>(a);
+Shape shape(int dp, int wr) {
+    return with_pick<T>(dp, wr, [](auto p) { return shape_of<typename decltype(p)::C>(); });
+}
+
+struct Plan {
+    Args a;
+    bool is_short, join;
+    int dp, wr, bm;
+    long long blocks, prefix_blocks;
+    size_t bytes;
+};
+
+template <typename T>
+Plan plan(const AttnLaunch& c) {
+    Plan p{};
+    Args& a = p.a;
+    a.c = c;
+    a.G = c.H / c.HK;
+    a.s2 = fabsf(c.scale) * kLog2e;
+    a.negate = c.scale < 0.0f;
+    a.splits = 1;
+    a.set_rows = (long long)c.N * c.H;
+    p.dp = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
+    const long long rows = (long long)c.max_q * a.G;
+    p.is_short = rows <= kShortRows;
+    p.wr = !p.is_short || rows > 64 ? 4 : rows > 32 ? 2 : 1;
+    const Shape s = shape<T>(p.dp, p.wr), whole = shape<T>(p.dp, 4);
+    p.bm = s.bm;
+    // key parts of the long form: enough blocks for two a CU, each with a few tiles at least
+    auto parts = [&](long long tiles, long long keys) {
+        const long long want = (2 * kCUs + tiles - 1) / std::max(1ll, tiles), most = keys / (4 * whole.bn);
+        return (int)std::max(1ll, std::min(std::min(want, most), 64ll));
+    };
+    const long long N = c.N, all_rows = N * a.G;
+    if (p.is_short) {
+        const long long units = c.HK * (c.kv_rows / s.bn + c.B);  // fewer blocks than that have work, bar overlapping runs
+        a.workers = (int)std::max(1ll, std::min((long long)kCUs * s.per_cu, units));
+        p.blocks = a.workers;
+        if (c.prefix_len > 0 && c.N > 0) {
+            const long long tiles = (all_rows + whole.bm - 1) / whole.bm;
+            a.splits = parts(tiles * c.HK, c.prefix_len);
+            p.prefix_blocks = tiles * c.HK * a.splits;
+            a.sets = a.splits + 1;
+            a.to_sets = true;
+            a.set0 = a.splits;
+        }
+        p.join = c.N > 0 && (a.workers > 1 || a.sets > 0);
+    } else {
+        const long long most = (rows + whole.bm - 1) / whole.bm;  // tiles of the longest sequence
+        a.splits = parts(std::min(most * c.B, all_rows / whole.bm + c.B) * c.HK, c.kv_rows + c.prefix_len);
+        p.blocks = most * c.B * c.HK * a.splits;
+        if (a.splits > 1) {
+            a.sets = a.splits;
+            a.to_sets = true;
+            p.join = true;
+        }
+    }
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        char* r = static_cast<char*>(c.workspace) + at;
+        at += (n + 255) / 256 * 256;
+        return r;
+    };
+    if (p.join) {
+        a.status = reinterpret_cast<int*>(take(4));
+        if (p.is_short) {
+            a.row_info = reinterpret_cast<int2*>(take(N * c.HK * 8));
+            a.slot_ml = reinterpret_cast<float2*>(take((size_t)a.workers * 2 * p.bm * 8));
+            a.slot_o = reinterpret_cast<float*>(take((size_t)a.workers * 2 * p.bm * c.D * 4));
+        }
+        if (a.sets > 0) {
+            a.set_ml = reinterpret_cast<float2*>(take((size_t)a.sets * a.set_rows * 8));
+            a.set_o = reinterpret_cast<float*>(take((size_t)a.sets * a.set_rows * c.D * 4));
+        }
+    }
+    p.bytes = at;
+    return p;
+}
+
+template <typename T>
+hipError_t launch(const AttnLaunch& c, hipStream_t stream) {
+    Plan p = plan<T>(c);
+    if (p.blocks > kMaxBlocks || p.prefix_blocks > kMaxBlocks || (p.join && p.a.set_rows > kMaxBlocks))
+        return hipErrorInvalidConfiguration;
+    hipError_t e;
+    if (p.is_short) {
+        if (p.prefix_blocks > 0) {
+            Args a = p.a;
+            a.prefix_rows = true;
+            a.set0 = 0;
+            if ((e = start_long<T>(a, p.dp, p.prefix_blocks, stream)) != hipSuccess) return e;
+        }
+        e = start_short<T>(p.a, p.dp, p.wr, p.blocks, stream);
+    } else {
+        e = start_long<T>(p.a, p.dp, p.blocks, stream);
+    }
+    if (e != hipSuccess || !p.join) return e;
+    const int local = p.is_short && p.a.sets > 0 ? p.a.set0 : -1;
+    if (p.a.set_rows <= 4 * kCUs) join_kernel<T, 4><<<(unsigned)p.a.set_rows, 256, 0, stream>>>(p.a, p.bm, local);
+    else join_kernel<T, 1><<<(unsigned)p.a.set_rows, 64, 0, stream>>>(p.a, p.bm, local);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(const AttnLaunch&) { return 0; }
+size_t attention_workspace_bytes(const AttnLaunch& c) {
+    switch (c.dtype) {
+        case GDN_F32: return plan<F32>(c).bytes;
+        case GDN_BF16: return plan<BF16>(c).bytes;
+        default: return plan<F16>(c).bytes;
+    }
+}
 
-hipError_t launch_attention(const AttnLaunch& a, hipStream_t stream) {
-    switch (a.dtype) {
-        case GDN_F32: return launch<F32>(a, stream);
-        case GDN_BF16: return launch<BF16>(a, stream);
-        default: return launch<F16>(a, stream);
+hipError_t launch_attention(const AttnLaunch& c, hipStream_t stream) {
+    switch (c.dtype) {
+        case GDN_F32: return launch<F32>(c, stream);
+        case GDN_BF16: return launch<BF16>(c, stream);
+        default: return launch<F16>(c, stream);
     }
 }
 
