@@ -521,7 +521,7 @@ def attention_workspace_bytes(q: torch.Tensor, B: int, *, HK: int, max_q: int, k
     """Bytes of device scratch attention_varlen (prefix_len 0) or attention_prefix_varlen takes as
     `workspace` for queries like q; it allocates them itself when the caller keeps none."""
     N, H, D = q.shape
-    d = _abi.AttnDesc(B, N, H, HK, D, max_q, _code(q, "q"), 0, 0.0, prefix_len, kv_rows)
+    d = _abi.AttnDesc(B, N, H, HK, D, max_q, _code(q, "q"), 0, 0.0, prefix_len, kv_rows, q.stride()[:2])
     n = ctypes.c_size_t(0)
     _check(lib().gdn_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)), "gdn_attention_workspace_bytes")
     return int(n.value)

@@ -19,14 +19,31 @@ using namespace attn;
 constexpr int kCUs = 256;
 constexpr int kShortRows = 128;
 
-// Joins the parts of a row: pieces of a cut run (a chain of workers' slots) and sets [0, sets).  One block of
-// 1 or 4 waves a row (token, head); its waves share the parts.
-template <typename T, int NW>
-__global__ __launch_bounds__(64 * NW) void join_kernel(Args a, int bm, int local_set) {
+// A row's result from its parts' sums: out and lse.
+template <typename T>
+__device__ __forceinline__ void finish(const Args& a, int t, int h, int e, f32x4 o, float top, float l, bool stats) {
     using TS = typename T::storage;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    union {
+        TS s[4];
+        f32x4 f;
+        u32x2 u;
+    } y;
+    for (int j = 0; j < 4; ++j) y.s[j] = from_f32<T>(o[j] * inv);
+    TS* out = static_cast<TS*>(a.c.out.p) + t * a.c.out.row + h * a.c.out.head + e;
+    if constexpr (sizeof(TS) == 2) *reinterpret_cast<u32x2*>(out) = y.u;
+    else *reinterpret_cast<f32x4*>(out) = y.f;
+    if (stats && a.c.lse != nullptr)
+        a.c.lse[(long long)t * a.c.H + h] = l == 0.0f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(l));
+}
+
+// Few rows or sets: a block a row (token, head) and 64 elements of it; 16 lanes hold the elements and the 16
+// groups of them share the parts -- the pieces of a cut run (a chain of workers' slots) and sets [0, sets).
+template <typename T>
+__global__ __launch_bounds__(256) void join_rows_kernel(Args a, int bm, int local_set) {
     if (*a.status != 0) return;
+    const int t = blockIdx.x / a.c.H, h = blockIdx.x - t * a.c.H, hk = h / a.G;
     const long long row = blockIdx.x;
-    const int t = (int)(row / a.c.H), h = (int)(row - (long long)t * a.c.H), hk = h / a.G;
     int worker = -1, pieces = 0;
     long long slot_row = 0;
     if (a.row_info != nullptr) {
@@ -40,54 +57,70 @@ __global__ __launch_bounds__(64 * NW) void join_kernel(Args a, int bm, int local
         }
     }
     const int sets = a.sets - (worker >= 0 && local_set >= 0 ? 1 : 0);  // a cut run left its own set (the last) unused
-    const int parts = pieces + sets, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int parts = pieces + sets, lane = threadIdx.x & 15, group = threadIdx.x >> 4;
     // the first piece is slot 1 of its worker, the others slot 0 of the following ones
     auto slot = [&](int p) { return ((long long)(worker + p) * 2 + (p == 0 ? 1 : 0)) * bm + slot_row; };
     auto ml_of = [&](int p) { return p < pieces ? a.slot_ml[slot(p)] : a.set_ml[(p - pieces) * a.set_rows + row]; };
-    float top = kNoMax;
-    for (int p = lane; p < parts; p += 64) top = fmaxf(top, ml_of(p).x);
-    for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
-    float l = 0.0f;
-    for (int p = lane; p < parts; p += 64) {
-        const float2 ml = ml_of(p);
-        l += ml.y * __builtin_amdgcn_exp2f(ml.x - top);
-    }
-    l = group_sum<64>(l);
+    const int e = blockIdx.y * 64 + 4 * lane;
+    float top = kNoMax, l = 0.0f;
     f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int e = 4 * lane;
-    if (e < a.c.D) {
 #pragma unroll 4
-        for (int p = wave; p < parts; p += NW) {
-            const float w = __builtin_amdgcn_exp2f(ml_of(p).x - top);
-            const float* src = p < pieces ? a.slot_o + slot(p) * a.c.D : a.set_o + ((p - pieces) * a.set_rows + row) * a.c.D;
-            o += w * *reinterpret_cast<const f32x4*>(src + e);
-        }
+    for (int p = group; p < parts; p += 16) {
+        const float2 ml = ml_of(p);
+        const float* src = p < pieces ? a.slot_o + slot(p) * a.c.D : a.set_o + ((p - pieces) * a.set_rows + row) * a.c.D;
+        const f32x4 x = *reinterpret_cast<const f32x4*>(src + (e < a.c.D ? e : 0));
+        const float to = fmaxf(top, ml.x), w = __builtin_amdgcn_exp2f(top - to), wx = __builtin_amdgcn_exp2f(ml.x - to);
+        top = to;
+        l = l * w + ml.y * wx;
+        o = o * w + x * wx;
     }
-    if constexpr (NW > 1) {
-        __shared__ f32x4 xo[NW][64];
-        xo[wave][lane] = o;
-        __syncthreads();
-        if (wave != 0) return;
-        for (int w = 1; w < NW; ++w) o += xo[w][lane];
+    __shared__ f32x4 xo[16][16];
+    __shared__ float2 xm[16];
+    xo[group][lane] = o;
+    if (lane == 0) xm[group] = make_float2(top, l);
+    __syncthreads();
+    if (group != 0) return;
+    const int some = min(parts, 16);
+    for (int g = 0; g < some; ++g) top = fmaxf(top, xm[g].x);
+    l = 0.0f;
+    o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g = 0; g < some; ++g) {
+        const float w = __builtin_amdgcn_exp2f(xm[g].x - top);
+        l += xm[g].y * w;
+        o += xo[g][lane] * w;
     }
-    if (e < a.c.D) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        TS* out = static_cast<TS*>(a.c.out.p) + t * a.c.out.row + h * a.c.out.head;
-        for (int j = 0; j < 4; ++j) out[e + j] = from_f32<T>(o[j] * inv);
-    }
-    if (a.c.lse != nullptr && threadIdx.x == 0)
-        a.c.lse[row] = l == 0.0f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(l));
+    if (e < a.c.D) finish<T>(a, t, h, e, o, top, l, e == 0);
 }
 
+// Many rows, of which few were cut: a block a worker, for the run that starts there and goes on; a wave a row.
 template <typename T>
-Shape shape(int dp, int wr) {
-    return with_pick<T>(dp, wr, [](auto p) { return shape_of<typename decltype(p)::C>(); });
+__global__ __launch_bounds__(256) void join_cut_kernel(Args a, int bm) {
+    if (*a.status != 0) return;
+    const int4 cut = a.cut[blockIdx.x];  // first token, tokens, key head, pieces
+    const int lane = threadIdx.x & 63, e = 4 * lane;
+    for (int r = threadIdx.x >> 6; r < cut.y * a.G; r += 4) {
+        float top = kNoMax, l = 0.0f;
+        f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+        for (int p = 0; p < cut.w; ++p) {
+            const long long at = ((long long)(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * bm + r;
+            const float2 ml = a.slot_ml[at];
+            const f32x4 x = *reinterpret_cast<const f32x4*>(a.slot_o + at * a.c.D + (e < a.c.D ? e : 0));
+            const float to = fmaxf(top, ml.x), w = __builtin_amdgcn_exp2f(top - to), wx = __builtin_amdgcn_exp2f(ml.x - to);
+            top = to;
+            l = l * w + ml.y * wx;
+            o = o * w + x * wx;
+        }
+        const int i = r / a.G;
+        if (e < a.c.D) finish<T>(a, cut.x + i, cut.z * a.G + r - i * a.G, e, o, top, l, lane == 0);
+    }
 }
 
 struct Plan {
     Args a;
     bool is_short, join;
     int dp, wr, bm;
+    int lds, long_lds;
     long long blocks, prefix_blocks;
     size_t bytes;
 };
@@ -103,20 +136,29 @@ Plan plan(const AttnLaunch& c) {
     a.splits = 1;
     a.set_rows = (long long)c.N * c.H;
     p.dp = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
-    const long long rows = (long long)c.max_q * a.G;
-    p.is_short = rows <= kShortRows;
-    p.wr = !p.is_short || rows > 64 ? 4 : rows > 32 ? 2 : 1;
-    const Shape s = shape<T>(p.dp, p.wr), whole = shape<T>(p.dp, 4);
-    p.bm = s.bm;
+    const long long rows = (long long)c.max_q * a.G, es = sizeof(typename T::storage);
+    p.wr = rows <= 64 ? (int)(rows + 15) / 16 : 8;
+    if (p.wr < 1) p.wr = 1;
+    const Shape s = with_short<T>(p.dp, p.wr, [](auto x) { return shape_of<typename decltype(x)::C>(); });
+    const Shape whole = with_long<T>(p.dp, [](auto x) { return shape_of<typename decltype(x)::C>(); });
+    // the short form's queries lie in LDS beside the ring, and a run's span a 32-bit range
+    const long long q_lds = (rows + 7) / 8 * 8 * s.row;
+    const long double q_span = ((long double)c.max_q * c.q.row + (long double)a.G * c.q.head) * es;
+    p.is_short = rows <= kShortRows && s.ring + q_lds <= kMaxLds && q_span < kOutside;
+    p.long_lds = whole.ring;
     // key parts of the long form: enough blocks for two a CU, each with a few tiles at least
     auto parts = [&](long long tiles, long long keys) {
         const long long want = (2 * kCUs + tiles - 1) / std::max(1ll, tiles), most = keys / (4 * whole.bn);
         return (int)std::max(1ll, std::min(std::min(want, most), 64ll));
     };
     const long long N = c.N, all_rows = N * a.G;
+    bool by_rows = true;
     if (p.is_short) {
+        p.bm = s.bm;
+        p.lds = (int)(s.ring + q_lds);
+        const int per_cu = std::min(8, (int)(160 * 1024 / (p.lds + 256)));
         const long long units = c.HK * (c.kv_rows / s.bn + c.B);  // fewer blocks than that have work, bar overlapping runs
-        a.workers = (int)std::max(1ll, std::min((long long)kCUs * s.per_cu, units));
+        a.workers = (int)std::max(1ll, std::min((long long)kCUs * per_cu, units));
         p.blocks = a.workers;
         if (c.prefix_len > 0 && c.N > 0) {
             const long long tiles = (all_rows + whole.bm - 1) / whole.bm;
@@ -127,6 +169,7 @@ Plan plan(const AttnLaunch& c) {
             a.set0 = a.splits;
         }
         p.join = c.N > 0 && (a.workers > 1 || a.sets > 0);
+        by_rows = a.sets > 0 || a.set_rows <= 8 * kCUs;
     } else {
         const long long most = (rows + whole.bm - 1) / whole.bm;  // tiles of the longest sequence
         a.splits = parts(std::min(most * c.B, all_rows / whole.bm + c.B) * c.HK, c.kv_rows + c.prefix_len);
@@ -146,7 +189,8 @@ Plan plan(const AttnLaunch& c) {
     if (p.join) {
         a.status = reinterpret_cast<int*>(take(4));
         if (p.is_short) {
-            a.row_info = reinterpret_cast<int2*>(take(N * c.HK * 8));
+            if (by_rows) a.row_info = reinterpret_cast<int2*>(take(N * c.HK * 8));
+            else a.cut = reinterpret_cast<int4*>(take((size_t)a.workers * 16));
             a.slot_ml = reinterpret_cast<float2*>(take((size_t)a.workers * 2 * p.bm * 8));
             a.slot_o = reinterpret_cast<float*>(take((size_t)a.workers * 2 * p.bm * c.D * 4));
         }
@@ -170,16 +214,19 @@ hipError_t launch(const AttnLaunch& c, hipStream_t stream) {
             Args a = p.a;
             a.prefix_rows = true;
             a.set0 = 0;
-            if ((e = start_long<T>(a, p.dp, p.prefix_blocks, stream)) != hipSuccess) return e;
+            if ((e = start_long<T>(a, p.dp, p.prefix_blocks, p.long_lds, stream)) != hipSuccess) return e;
         }
-        e = start_short<T>(p.a, p.dp, p.wr, p.blocks, stream);
+        e = start_short<T>(p.a, p.dp, p.wr, p.blocks, p.lds, stream);
     } else {
-        e = start_long<T>(p.a, p.dp, p.blocks, stream);
+        e = start_long<T>(p.a, p.dp, p.blocks, p.long_lds, stream);
     }
     if (e != hipSuccess || !p.join) return e;
-    const int local = p.is_short && p.a.sets > 0 ? p.a.set0 : -1;
-    if (p.a.set_rows <= 4 * kCUs) join_kernel<T, 4><<<(unsigned)p.a.set_rows, 256, 0, stream>>>(p.a, p.bm, local);
-    else join_kernel<T, 1><<<(unsigned)p.a.set_rows, 64, 0, stream>>>(p.a, p.bm, local);
+    if (p.a.cut != nullptr) {
+        join_cut_kernel<T><<<(unsigned)p.a.workers, 256, 0, stream>>>(p.a, p.bm);
+    } else {
+        const int local = p.is_short && p.a.sets > 0 ? p.a.set0 : -1;
+        join_rows_kernel<T><<<dim3((unsigned)p.a.set_rows, (c.D + 63) / 64), 256, 0, stream>>>(p.a, p.bm, local);
+    }
     return hipGetLastError();
 }
 

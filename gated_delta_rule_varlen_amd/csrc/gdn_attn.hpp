@@ -7,7 +7,7 @@
 // the keys.
 //
 // Products.  S^T = K Q^T and O^T = V^T P^T on 32x32 MFMA tiles: a lane's accumulators all belong to one
-// query row (column lane%32), so the softmax statistics are one number a lane and rescaling O
+// query row (column lane % M), so the softmax statistics are one number a lane and rescaling O
 // needs no exchange; the exponentials of S^T, rounded, are the second product's operand where they lie:
 // the 16 scores of a lane are keys 8(i/4) + 4(lane/32) + i%4, and V^T is read with its keys in that
 // order (a contraction may run in any order).
@@ -56,6 +56,7 @@ struct Args {
     // workspace
     int* status;
     int2* row_info;    // [N][HK]: x = worker a cut run starts in (-1: not cut), y = pieces * 128 + token in sequence
+    int4* cut;         // [workers]: first token, tokens, key head, pieces of the cut run that starts there (tokens 0: none)
     float* slot_o;     // [workers][2][BM][D]
     float2* slot_ml;   // [workers][2][BM]
     float* set_o;      // [sets][N*H][D]
@@ -64,36 +65,50 @@ struct Args {
     long long set_rows;  // N*H
 };
 
-template <typename T>
-struct Mma;
-template <>
-struct Mma<BF16> {
-    static __device__ __forceinline__ void mul(u32x4 a, u32x4 b, f32x16& c) {
-        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+// Accumulators of an M x M tile, and one step of its product: 16 bytes of each operand's rows a lane.
+template <int M>
+struct AccOf {
+    typedef float type __attribute__((ext_vector_type(M* M / 64)));
+};
+template <int M>
+using Acc = typename AccOf<M>::type;
+
+template <typename T, int M>
+__device__ __forceinline__ void multiply(u32x4 a, u32x4 b, Acc<M>& c) {
+    if constexpr (T::code == GDN_BF16) {
+        const bf16x8 x = __builtin_bit_cast(bf16x8, a), y = __builtin_bit_cast(bf16x8, b);
+        if constexpr (M == 32) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+        else c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+    } else if constexpr (T::code == GDN_F16) {
+        const f16x8 x = __builtin_bit_cast(f16x8, a), y = __builtin_bit_cast(f16x8, b);
+        if constexpr (M == 32) c = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, c, 0, 0, 0);
+        else c = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = __uint_as_float(a[j]), y = __uint_as_float(b[j]);
+            if constexpr (M == 32) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x, y, c, 0, 0, 0);
+            else c = __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, c, 0, 0, 0);
+        }
     }
-    static __device__ __forceinline__ uint32_t pack(float x, float y) {
+}
+template <int M>
+__device__ __forceinline__ void multiply1(float x, float y, Acc<M>& c) {
+    if constexpr (M == 32) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x, y, c, 0, 0, 0);
+    else c = __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, c, 0, 0, 0);
+}
+
+// Two values rounded to the half type T.
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    if constexpr (T::code == GDN_BF16) {
         typedef __bf16 v2 __attribute__((ext_vector_type(2)));
         return __builtin_bit_cast(uint32_t, v2{(__bf16)x, (__bf16)y});
-    }
-};
-template <>
-struct Mma<F16> {
-    static __device__ __forceinline__ void mul(u32x4 a, u32x4 b, f32x16& c) {
-        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-    }
-    static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    } else {
         typedef _Float16 v2 __attribute__((ext_vector_type(2)));
         return __builtin_bit_cast(uint32_t, v2{(_Float16)x, (_Float16)y});
     }
-};
-template <>
-struct Mma<F32> {
-    static __device__ __forceinline__ void mul(u32x4 a, u32x4 b, f32x16& c) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[j]), __uint_as_float(b[j]), c, 0, 0, 0);
-    }
-};
+}
 
 // The sign bits of the elements (one or two in 32 bits) whose exponent is all ones.
 template <typename T>
@@ -109,20 +124,48 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// The maximum and the sum of a lane's value and that of the lane 32 away.
-__device__ __forceinline__ float max_halves(float x) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+// Maximum and sum over the 64 / M lanes that share a query row.
+template <bool MAX>
+__device__ __forceinline__ float both(uint32_t x, uint32_t y) {
+    return MAX ? fmaxf(__uint_as_float(x), __uint_as_float(y)) : __uint_as_float(x) + __uint_as_float(y);
 }
-__device__ __forceinline__ float sum_halves(float x) {
+template <int M, bool MAX>
+__device__ __forceinline__ float over_row(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    x = both<MAX>(r[0], r[1]);
+    if constexpr (M == 16) {
+        const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = both<MAX>(q[0], q[1]);
+    }
+    return x;
 }
 
 // A value every lane holds, as a scalar.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ long long uniform(long long x) {
     return ((long long)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x);
+}
+
+// An entry of one of the call's small arrays (nothing writes them while it runs), through the scalar cache: a
+// vector load here would wait for every tile on its way.
+template <typename X>
+__device__ __forceinline__ X entry(const X* p, int i) {
+    return ((const __attribute__((address_space(4))) X*)p)[i];
+}
+
+// 64 x 16 bytes to LDS, at `at` + 16 * lane, from base + voff + soff of a range of `bytes`; zeros past it.  No register
+// waits for this load, and wait_and_meet() counts it.  (As a builtin the compiler would wait for all of them
+// before every transposing LDS read.)
+struct Range {
+    u32x4 r;
+    __device__ __forceinline__ Range(const void* base, int bytes) {
+        const uint64_t b = reinterpret_cast<uint64_t>(base);
+        r = u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)bytes, (uint32_t)kRsrc};
+    }
+};
+__device__ __forceinline__ void load_to_lds(const Range& s, uint32_t at, int voff, int soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 ::"s"(at), "v"(voff), "s"(s.r), "s"(soff) : "m0", "memory");
 }
 
 // Whole-call check (offsets, lengths, key runs) with a per-sequence sum: `units(T, n)` of every sequence.
@@ -201,24 +244,28 @@ __device__ __forceinline__ void find_unit(const AttnLaunch& c, F units, long lon
     }
 }
 
-template <typename T_, int DP_, int WR_, int WK_, int QT_, int KT_, int NS_, int WAVES_>
+template <typename T_, int M_, int DP_, int WR_, int KT_, int NS_, int WAVES_>
 struct Cfg {
     using T = T_;
     using TS = typename T::storage;
-    static constexpr int DP = DP_, WR = WR_, WK = WK_, QT = QT_, KT = KT_, NS = NS_, WAVES = WAVES_;
+    static constexpr int M = M_, DP = DP_, KT = KT_, NS = NS_, WAVES = WAVES_;
     static constexpr bool HALF = sizeof(TS) == 2;
-    static constexpr int ES = sizeof(TS), NW = WR * WK, NT = 64 * NW, BM = 32 * QT * WR, KW = 32 * KT, BN = KW * WK;
+    static constexpr int ES = sizeof(TS), NW = WR_, NT = 64 * NW, BM = M * NW, BN = 32 * KT;
+    static constexpr int NG = 64 / M;             // lanes that share a query row
+    static constexpr int EA = M * M / 64;         // accumulators a lane and tile
+    static constexpr int SUB = 32 / M;            // tiles that make up 32 keys
     static constexpr int RB = DP * ES;            // bytes of a row in LDS
     static constexpr int CPR = RB / 16;           // 16-byte pieces of a row
-    static constexpr int CS = RB / 32;            // operand steps of a score tile
-    static constexpr int DT = DP / 32;            // 32-wide parts of the head
+    static constexpr int CS = RB / (16 * NG);     // operand steps of a score tile
+    static constexpr int DT = DP / M;             // M-wide parts of the head
     static constexpr int TILE = BN * RB, STAGE = 2 * TILE;
-    static constexpr int JN = TILE / (NT * 16);   // loads a wave issues for one of K, V
-    static constexpr int RPI = NT / CPR;          // rows one load of the whole block covers
+    static constexpr int POW = NW >= 8 ? 8 : NW >= 4 ? 4 : NW >= 2 ? 2 : 1;
+    static constexpr int LW = POW * 1024 <= TILE ? POW : TILE / 1024;  // waves that load
+    static constexpr int JN = TILE / (LW * 1024);  // loads such a wave issues for one of K, V
+    static constexpr int RPI = LW * 64 / CPR;      // rows one load of all of them covers
     static constexpr int PRE = RPI >= 8 ? 1 : 8 / RPI;
-    static constexpr int XCH = (WK / 2) * WR * QT * DT * 16 * 64 * 4 + WK * WR * QT * 64 * 8;  // joining the key waves
-    static constexpr int LDS = NS * STAGE > XCH ? NS * STAGE : XCH;
-    static_assert(CPR >= 8 && TILE % (NT * 16) == 0 && RPI >= 1 && LDS <= 160 * 1024, "tile");
+    static constexpr int LDS = NS * STAGE;
+    static_assert(CPR >= 8 && TILE % (LW * 1024) == 0 && RPI >= 1 && LDS <= 160 * 1024 && JN % PRE == 0, "tile");
     // P of fp16 is kept 2^4 larger, away from the subnormals; with the 2^8 of lag it stays below 2^13
     static constexpr float BIAS = T::code == GDN_F16 ? 4.0f : 0.0f, LAG = 8.0f;
 };
@@ -234,28 +281,33 @@ template <typename C>
 struct Block {
     using T = typename C::T;
     using TS = typename C::TS;
-    static constexpr int QT = C::QT, KT = C::KT, DT = C::DT;
+    static constexpr int M = C::M, KT = C::KT, DT = C::DT;
 
     const Args& a;
     char* lds;
-    int lane, wave, wr, wk, col, half;
+    int lane, wave, col, grp;  // the lane's query row in the wave's tile, and its place among the lanes of that row
+    uint32_t lds_base;                      // LDS address of the ring
+    int row_bytes;                          // of a head
+    float c;                                // scores to base 2
     int kstride, vstride;                   // bytes between rows of this source
     int koff[C::PRE], voff[C::PRE];
-    u32x4 q[QT][C::CS];
-    int vis[QT];                            // keys the lane's row sees
+    u32x4 q[C::CS];
+    int vis;                                // keys the lane's row sees
     int vis_lo, vis_hi;                     // over the wave's rows
     int run_n;                              // keys of the run
     bool spoiled = false;                   // the wave met values only redo() can deal with
-    f32x16 o[QT][DT];
-    float ref[QT], l[QT];
+    Acc<M> o[DT];
+    float ref, l;
 
     __device__ __forceinline__ Block(const Args& a_, char* lds_) : a(a_), lds(lds_) {
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        wr = wave / C::WK;
-        wk = wave % C::WK;
-        col = lane & 31;
-        half = lane >> 5;
+        col = lane & (M - 1);
+        grp = lane / M;
+        lds_base = uniform((int)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
+        row_bytes = a.c.D * C::ES;
+        c = a.s2;
+        asm volatile("" : "+v"(c));  // a register: not read again for every tile
     }
 
     // byte offsets of the 16-byte pieces this lane loads, for rows `ks` and `vs` bytes apart
@@ -264,7 +316,7 @@ struct Block {
         vstride = (int)(vrow * C::ES);
 #pragma unroll
         for (int j = 0; j < C::PRE; ++j) {
-            const int p = (j * C::NW + wave) * 64 + lane, row = p / C::CPR, piece = (p % C::CPR) ^ (row & 7);
+            const int p = (j * C::LW + wave) * 64 + lane, row = p / C::CPR, piece = (p % C::CPR) ^ (row & 7);
             const bool in = piece * 16 < a.c.D * C::ES;
             koff[j] = in ? row * kstride + piece * 16 : kOutside;
             voff[j] = in ? row * vstride + piece * 16 : kOutside;
@@ -272,134 +324,162 @@ struct Block {
     }
 
     __device__ __forceinline__ void load_tile(const Keys& s, int tile, bool real, int stage) {
+        if (C::LW < C::NW && wave >= C::LW) return;
         const int k0 = tile * C::BN, left = s.n - k0, rows = left < C::BN ? left : C::BN, last = rows - 1;
         const bool any = real && rows > 0;
-        const __amdgpu_buffer_rsrc_t rk = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(s.k + (long long)k0 * kstride), 0, any ? last * kstride + a.c.D * C::ES : 0, kRsrc);
-        const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(s.v + (long long)k0 * vstride), 0, any ? last * vstride + a.c.D * C::ES : 0, kRsrc);
-        char* to = lds + stage * C::STAGE + wave * 1024;
+        const Range rk(s.k + (long long)k0 * kstride, any ? last * kstride + row_bytes : 0);
+        const Range rv(s.v + (long long)k0 * vstride, any ? last * vstride + row_bytes : 0);
+        const uint32_t to = lds_base + stage * C::STAGE + wave * 1024;
 #pragma unroll
         for (int j = 0; j < C::JN; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (__attribute__((address_space(3))) void*)(to + j * C::NW * 1024), 16,
-                                                     koff[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * kstride, 0, 0);
+            load_to_lds(rk, to + j * C::LW * 1024, koff[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * kstride);
 #pragma unroll
         for (int j = 0; j < C::JN; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rv, (__attribute__((address_space(3))) void*)(to + C::TILE + j * C::NW * 1024), 16,
-                voff[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * vstride, 0, 0);
+            load_to_lds(rv, to + C::TILE + j * C::LW * 1024, voff[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * vstride);
     }
 
     // Queries of the block's rows row0 .. (of `rows` in the list); rows past the list are zeros.
     __device__ __forceinline__ void load_rows(int row0, int rows, long long first, int hk) {
-        const int G = a.G;
+        const int G = a.G, r = row0 + wave * M + col, i = r / G, g = r - i * G;
+        const bool in = r < rows;
+        // lanes without an element read the row's first instead, so no load stands in a branch
+        const TS* p = static_cast<const TS*>(a.c.q.p) + (first + (in ? i : 0)) * a.c.q.row +
+                      (long long)(hk * G + (in ? g : 0)) * a.c.q.head;
+        const uint32_t flip = !a.negate ? 0u : C::HALF ? 0x80008000u : 0x80000000u;
 #pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            const int r = row0 + (wr * QT + t) * 32 + col, i = r / G, g = r - i * G;
-            const bool in = r < rows;
-            // lanes without an element read the row's first instead, so no load stands in a branch
-            const TS* p = static_cast<const TS*>(a.c.q.p) + (first + (in ? i : 0)) * a.c.q.row +
-                          (long long)(hk * G + (in ? g : 0)) * a.c.q.head;
-            const uint32_t flip = !a.negate ? 0u : C::HALF ? 0x80008000u : 0x80000000u;
-#pragma unroll
-            for (int s = 0; s < C::CS; ++s) {
-                const int e = (2 * s + half) * (16 / C::ES);
-                q[t][s] = *reinterpret_cast<const u32x4*>(p + (e < a.c.D ? e : 0));
-            }
-#pragma unroll
-            for (int s = 0; s < C::CS; ++s) {
-                const uint32_t keep = in && (2 * s + half) * (16 / C::ES) < a.c.D ? ~0u : 0u;
-                q[t][s] = (q[t][s] ^ flip) & keep;
-            }
-            ref[t] = kNoMax;
-            l[t] = 0.0f;
-            spoiled = false;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[t][d] = f32x16{};
+        for (int s = 0; s < C::CS; ++s) {
+            const int e = (C::NG * s + grp) * (16 / C::ES);
+            q[s] = *reinterpret_cast<const u32x4*>(p + (e < a.c.D ? e : 0));
         }
+#pragma unroll
+        for (int s = 0; s < C::CS; ++s) {
+            const uint32_t keep = in && (C::NG * s + grp) * (16 / C::ES) < a.c.D ? ~0u : 0u;
+            q[s] = (q[s] ^ flip) & keep;
+        }
+        clear();
+    }
+
+    __device__ __forceinline__ void clear() {
+        spoiled = false;
+        ref = kNoMax;
+        l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = Acc<M>{};
+    }
+
+    // The short form takes queries through LDS, as rows at `at` laid out like the keys': asked for with the run's
+    // first tile, long before they are needed, and read when the run begins.
+    __device__ __forceinline__ void ask_rows(int at, int T, long long first, int hk) {
+        if (C::LW < C::NW && wave >= C::LW) return;  // as for the tiles: only who loads those waits in order for these
+        const int G = a.G, rows = T * G;
+        const char* p = static_cast<const char*>(a.c.q.p) + (first * a.c.q.row + (long long)hk * G * a.c.q.head) * C::ES;
+        const int bytes = (int)(((T - 1) * a.c.q.row + (G - 1) * a.c.q.head + a.c.D) * C::ES);
+        const Range rq(p, bytes);
+        const int padded = (rows + 7) & ~7;
+        for (int x = wave * 64; x < padded * C::CPR; x += C::LW * 64) {
+            const int r = (x + lane) / C::CPR, piece = ((x + lane) % C::CPR) ^ (r & 7), i = r / G, g = r - i * G;
+            const int off = r < rows && piece * 16 < a.c.D * C::ES
+                                ? (int)((i * a.c.q.row + g * a.c.q.head) * C::ES) + piece * 16 : kOutside;
+            load_to_lds(rq, lds_base + at + x * 16, off, 0);
+        }
+    }
+    __device__ __forceinline__ void take_rows(const char* at, int rows) {
+        const uint32_t flip = !a.negate ? 0u : C::HALF ? 0x80008000u : 0x80000000u;
+        const int r = wave * M + col, have = r < rows ? r : 0;
+        const uint32_t keep = r < rows ? ~0u : 0u;  // rows past the list were not loaded
+        const char* p = at + have * C::RB;
+#pragma unroll
+        for (int s = 0; s < C::CS; ++s)
+            q[s] = (*reinterpret_cast<const u32x4*>(p + (((C::NG * s + grp) ^ (have & 7)) * 16)) ^ flip) & keep;
+        clear();
     }
 
     // The keys each row sees of a run of n: all, or (causal) seen0 + its token, at least 0 and at most n.
     __device__ __forceinline__ void see(int row0, int rows, bool causal, int seen0, int n) {
         run_n = n;
-        const int G = a.G, lo = row0 + wr * QT * 32, hi = min(lo + QT * 32, rows) - 1;
-        auto keys = [&](int r) { return causal ? min(max(seen0 + r / G, 0), n) : n; };
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            const int r = lo + t * 32 + col;
-            vis[t] = r < rows ? keys(r) : n;
-        }
-        vis_lo = __builtin_amdgcn_readfirstlane(keys(lo));
-        vis_hi = __builtin_amdgcn_readfirstlane(lo < rows ? keys(hi) : 0);
+        const int G = a.G, lo = row0 + wave * M, hi = min(lo + M, rows) - 1, r = lo + col;
+        auto keys = [&](int x) { return causal ? min(max(seen0 + x / G, 0), n) : n; };
+        vis = r < rows ? keys(r) : n;
+        vis_lo = uniform(keys(lo));
+        vis_hi = uniform(lo < rows ? keys(hi) : 0);
     }
 
-    // A stage's keys and values against the wave's rows; key0 = index of its first key in the run.
-    __device__ __forceinline__ void use_tile(int stage, int key0) {
-        const int base = key0 + wk * C::KW;
+    // A stage's keys and values against the wave's rows; base = index of its first key in the run.  Element i of a
+    // lane's scores of 32 keys is key 4 NG (i / 4) + 4 grp + i % 4.
+    __device__ __forceinline__ void use_tile(int stage, int base) {
         if (base >= vis_hi) return;
-        const char* kt_ = lds + stage * C::STAGE + (wk * C::KW + col) * C::RB;
-        f32x16 s[QT][KT];
+        constexpr int SN = C::SUB * C::EA;  // scores of 32 keys a lane
+        const char* kt_ = lds + stage * C::STAGE + col * C::RB;
+        Acc<M> acc[KT][C::SUB];
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
-            for (int t = 0; t < QT; ++t) s[t][k] = f32x16{};
+            for (int u = 0; u < C::SUB; ++u) acc[k][u] = Acc<M>{};
+        // operands are read in groups ahead of the products that use them
+        constexpr int KG = C::CS < 8 ? C::CS : C::CS > 8 && C::WAVES > 1 ? 4 : 8;
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
-            for (int x = 0; x < C::CS; ++x) {
-                const u32x4 f = *reinterpret_cast<const u32x4*>(kt_ + k * 32 * C::RB + (((2 * x + half) ^ (lane & 7)) * 16));
+            for (int x0 = 0; x0 < C::CS; x0 += KG) {
+                u32x4 f[KG][C::SUB];
 #pragma unroll
-                for (int t = 0; t < QT; ++t) Mma<T>::mul(f, q[t][x], s[t][k]);
+                for (int x = 0; x < KG; ++x)
+#pragma unroll
+                    for (int u = 0; u < C::SUB; ++u)
+                        f[x][u] = *reinterpret_cast<const u32x4*>(kt_ + (k * 32 + u * M) * C::RB +
+                                                                  (((C::NG * (x0 + x) + grp) ^ (lane & 7)) * 16));
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int x = 0; x < KG; ++x)
+#pragma unroll
+                    for (int u = 0; u < C::SUB; ++u) multiply<T, M>(f[x][u], q[x0 + x], acc[k][u]);
             }
-        if (base + C::KW > vis_lo) {
+        float s[KT][SN];
 #pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                const int room = vis[t] - base - 4 * half;
+        for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int k = 0; k < KT; ++k)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (32 * k + 8 * (i / 4) + i % 4 >= room) s[t][k][i] = -INFINITY;
-            }
-        }
-        float c = a.s2;
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            float top = s[t][0][0];
+            for (int i = 0; i < SN; ++i) s[k][i] = acc[k][i / C::EA][i % C::EA];
+        if (base + C::BN > vis_lo) {
+            const int room = vis - base - 4 * grp;
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][k][i]);
-            top = max_halves(top) * c;
-            if (__builtin_amdgcn_ballot_w64(top > ref[t] + (C::BIAS + C::LAG)) != 0) {
-                const float to = fmaxf(ref[t], top - C::BIAS), w = __builtin_amdgcn_exp2f(ref[t] - to);
-                ref[t] = to;
-                l[t] *= w;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[t][d] *= w;
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int k = 0; k < KT; ++k)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(fmaf(s[t][k][i], c, -ref[t]));
-                    s[t][k][i] = p;
-                    sum += p;
-                }
-            l[t] += sum;
+                for (int i = 0; i < SN; ++i)
+                    if (32 * k + 4 * C::NG * (i / 4) + i % 4 >= room) s[k][i] = -INFINITY;
         }
-        const char* vt = lds + stage * C::STAGE + C::TILE + wk * C::KW * C::RB;
+        float top = s[0][0];
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int i = 0; i < SN; ++i) top = fmaxf(top, s[k][i]);
+        top = over_row<M, true>(top) * c;
+        if (__builtin_amdgcn_ballot_w64(top > ref + (C::BIAS + C::LAG)) != 0) {
+            const float to = fmaxf(ref, top - C::BIAS), w = __builtin_amdgcn_exp2f(ref - to);
+            ref = to;
+            l *= w;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= w;
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int i = 0; i < SN; ++i) {
+                s[k][i] = __builtin_amdgcn_exp2f(fmaf(s[k][i], c, -ref));
+                sum += s[k][i];
+            }
+        l += sum;
+        const char* vt = lds + stage * C::STAGE + C::TILE;
         // 0 * infinity is NaN: where rows differ in what they see, a value that is not finite would reach the
-        // rows that must not see it.  Such a tile is found here and its block done again by redo().
-        if (vis_lo < min(base + C::KW, run_n)) spoiled |= any_not_finite(vt);
+        // rows that must not see it.  Such a tile is found here and the wave's rows are done again by redo().
+        if (vis_lo < min(base + C::BN, run_n)) spoiled |= any_not_finite(vt);
         product(vt, s);
     }
 
     __device__ __forceinline__ bool any_not_finite(const char* vt) {
         uint32_t acc = 0;
 #pragma unroll 1
-        for (int at = lane * 16; at < C::KW * C::RB; at += 1024) {
+        for (int at = lane * 16; at < C::BN * C::RB; at += 1024) {
             const u32x4 x = *reinterpret_cast<const u32x4*>(vt + at);
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc |= not_finite_sign<T>(x[j]);
@@ -408,56 +488,54 @@ struct Block {
     }
 
     // O^T += V^T P^T for the tile at vt.
-    __device__ __forceinline__ void product(const char* vt, const f32x16 (&s)[QT][KT]) {
+    template <int SN>
+    __device__ __forceinline__ void product(const char* vt, const float (&s)[KT][SN]) {
         if constexpr (C::HALF) {
-            // lane x of 16 names key x/4 and elements 4(x%4) .. of the 16-wide part (lane/16)%2
-            const int x = lane & 15, part = (lane >> 4) & 1, sw = 4 * half + (x >> 2);
-            const char* vp = vt + sw * C::RB + (x & 1) * 8;
+            // lane x of 16 names key x/4 of its four and elements 4(x%4) .. of a 16-wide part of the head
+            const int x = lane & 15, part = M == 32 ? (lane >> 4) & 1 : 0, key = 4 * grp + (x >> 2), sw = key & 7;
+            const char* vp = vt + key * C::RB + (x & 1) * 8;
 #pragma unroll
-            for (int k = 0; k < 2 * KT; ++k) {
-                u32x4 p[QT];
+            for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int t = 0; t < QT; ++t)
+                for (int z = 0; z < SN / 8; ++z) {  // eight scores a lane are one step: 8 NG keys
+                    u32x4 p;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        p[t][e] = Mma<T>::pack(s[t][k / 2][8 * (k % 2) + 2 * e], s[t][k / 2][8 * (k % 2) + 2 * e + 1]);
+                    for (int e = 0; e < 4; ++e) p[e] = pack<T>(s[k][8 * z + 2 * e], s[k][8 * z + 2 * e + 1]);
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const int piece = 4 * d + 2 * part + ((x >> 1) & 1);
-                    const char* at = vp + 16 * k * C::RB + ((piece ^ sw) * 16);
-                    union {
-                        v4i16 h[2];
-                        u32x4 v;
-                    } f;
-                    f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(at));
-                    f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(at + 8 * C::RB));
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) Mma<T>::mul(f.v, p[t], o[t][d]);
+                    for (int d = 0; d < DT; ++d) {
+                        const int piece = M / 8 * d + 2 * part + ((x >> 1) & 1);
+                        const char* at = vp + (32 * k + 8 * C::NG * z) * C::RB + ((piece ^ sw) * 16);
+                        union {
+                            v4i16 h[2];
+                            u32x4 v;
+                        } f;
+                        f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(at));
+                        f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) v4i16*)(at + 4 * C::NG * C::RB));
+                        multiply<T, M>(f.v, p, o[d]);
+                    }
                 }
-            }
         } else {
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int sw = 4 * half + i % 4;
-                    const char* row = vt + (32 * k + 8 * (i / 4) + sw) * C::RB + (col & 3) * 4;
+                for (int i = 0; i < SN; ++i) {
+                    const int key = 4 * grp + i % 4, sw = key & 7;
+                    const char* row = vt + (32 * k + 4 * C::NG * (i / 4) + key) * C::RB + (col & 3) * 4;
 #pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        const float v = *reinterpret_cast<const float*>(row + (((8 * d + (col >> 2)) ^ sw) * 16));
-#pragma unroll
-                        for (int t = 0; t < QT; ++t)
-                            o[t][d] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, s[t][k][i], o[t][d], 0, 0, 0);
-                    }
+                    for (int d = 0; d < DT; ++d)
+                        multiply1<M>(*reinterpret_cast<const float*>(row + (((M / 4 * d + (col >> 2)) ^ sw) * 16)), s[k][i], o[d]);
                 }
         }
     }
 
+    // LDS addresses are worth registers inside a loop over tiles, not across a block's runs.
+    __device__ __forceinline__ void fresh_addresses() { asm volatile("" : "+v"(lane), "+v"(col), "+v"(grp)); }
+
     // Tiles [t0, t1) of the run.  Loads run NS - 1 tiles ahead; the ones past the end are asked for with an
     // empty range, so the count of loads on their way is the same at every wait.
     __device__ __forceinline__ void run(const Keys& s, int t0, int t1) {
-        // LDS addresses are worth registers inside this loop, not across a block's runs
-        asm volatile("" : "+v"(lane), "+v"(col), "+v"(half));
+        fresh_addresses();
 #pragma unroll
         for (int i = 0; i < C::NS - 1; ++i) load_tile(s, t0 + i, t0 + i < t1, i);
         int stage = 0;
@@ -471,62 +549,10 @@ struct Block {
         wait_and_meet<0>();
     }
 
-    // Joins the key waves' parts into wave wk = 0 of each row group, and the two halves' sums.
-    __device__ __forceinline__ void join() {
-#pragma unroll
-        for (int t = 0; t < QT; ++t) l[t] = sum_halves(l[t]);
-        if constexpr (C::WK > 1) {
-            constexpr int OB = QT * DT * 16 * 64;  // floats of one wave's O
-            float* xo = reinterpret_cast<float*>(lds);
-            float2* xm = reinterpret_cast<float2*>(lds + (C::WK / 2) * C::WR * OB * 4);
-#pragma unroll
-            for (int step = C::WK / 2; step >= 1; step /= 2) {
-                if (wk >= step && wk < 2 * step) {
-                    float* to = xo + (wr * step + wk - step) * OB + lane;
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) {
-                        xm[((wr * step + wk - step) * QT + t) * 64 + lane] = make_float2(ref[t], l[t]);
-#pragma unroll
-                        for (int d = 0; d < DT; ++d)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) to[((t * DT + d) * 16 + i) * 64] = o[t][d][i];
-                    }
-                }
-                __syncthreads();
-                if (wk < step) {
-                    const float* from = xo + (wr * step + wk) * OB + lane;
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) {
-                        const float2 ml = xm[((wr * step + wk) * QT + t) * 64 + lane];
-                        const float top = fmaxf(ref[t], ml.x), w = __builtin_amdgcn_exp2f(ref[t] - top),
-                                    wo = __builtin_amdgcn_exp2f(ml.x - top);
-                        ref[t] = top;
-                        l[t] = l[t] * w + ml.y * wo;
-#pragma unroll
-                        for (int d = 0; d < DT; ++d)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[t][d][i] = o[t][d][i] * w + from[((t * DT + d) * 16 + i) * 64] * wo;
-                    }
-                }
-                __syncthreads();
-            }
-        }
-    }
+    // The lanes of a row summed their own keys.
+    __device__ __forceinline__ void sum_rows() { l = over_row<M, false>(l); }
 
-    // O of the lane's row, four elements at a time.
-    template <typename F>
-    __device__ __forceinline__ void each4(int t, F put) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = 32 * d + 8 * i + 4 * half;
-                if (e < a.c.D) put(e, f32x4{o[t][d][4 * i], o[t][d][4 * i + 1], o[t][d][4 * i + 2], o[t][d][4 * i + 3]});
-            }
-    }
-
-    // Where a row's result goes: its place in the list, and out or the workspace.
+    // Where rows' results go: their place in the list, and out or the workspace.
     struct To {
         int row0, rows;
         long long first;
@@ -534,58 +560,67 @@ struct Block {
         int set;          // >= 0: this set of the workspace
         long long slot;   // >= 0: this slot of the workspace
     };
-    // Unscaled elements e .. e+3 of row r (or, N = 1, one element), and once a row its ref and l.
-    template <int N>
-    __device__ __forceinline__ void put(const To& to, int r, int e, const float (&x)[N], float m, float sum, bool stats) {
+    // Row r of them: the destination of its elements (fp32 sums, or the finished row), and its statistics there.
+    struct Row {
+        float* sums;
+        TS* out;
+        float inv;
+    };
+    __device__ __forceinline__ Row row_at(const To& to, int r, float m, float sum, bool stats) {
         const int i = r / a.G, h = to.hk * a.G + r - i * a.G;
-        const long long at = to.slot >= 0 ? to.slot * C::BM + r : (to.set >= 0 ? to.set * a.set_rows : 0) + (to.first + i) * a.c.H + h;
+        const long long token_row = (to.first + i) * a.c.H + h;
+        Row y{nullptr, nullptr, 1.0f};
         if (to.slot >= 0 || to.set >= 0) {
-            float* p = (to.slot >= 0 ? a.slot_o : a.set_o) + at * a.c.D + e;
+            const long long at = to.slot >= 0 ? to.slot * C::BM + r : to.set * a.set_rows + token_row;
+            y.sums = (to.slot >= 0 ? a.slot_o : a.set_o) + at * a.c.D;
             if (stats) (to.slot >= 0 ? a.slot_ml : a.set_ml)[at] = make_float2(m, sum);
-            if constexpr (N == 4) *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
-            else *p = x[0];
         } else {
-            TS* out = static_cast<TS*>(a.c.out.p) + (to.first + i) * a.c.out.row + h * a.c.out.head + e;
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            union {
-                TS s[4];
-                f32x4 f;
-                u32x2 u;
-            } y;
-#pragma unroll
-            for (int j = 0; j < N; ++j) y.s[j] = from_f32<T>(x[j] * inv);
-            if constexpr (N == 1) *out = y.s[0];
-            else if constexpr (C::HALF) *reinterpret_cast<u32x2*>(out) = y.u;
-            else *reinterpret_cast<f32x4*>(out) = y.f;
+            y.out = static_cast<TS*>(a.c.out.p) + (to.first + i) * a.c.out.row + h * a.c.out.head;
+            y.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             if (stats && a.c.lse != nullptr)
-                a.c.lse[at] = sum == 0.0f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(sum));
+                a.c.lse[token_row] = sum == 0.0f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(sum));
         }
+        return y;
     }
 
-    // The accumulators of the block's rows.
+    // The accumulators of the wave's rows.
     __device__ __forceinline__ void store(const To& to) {
-        if (wk != 0) return;
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            const int r = to.row0 + (wr * QT + t) * 32 + col;
-            if (r >= to.rows) continue;
+        const int r = to.row0 + wave * M + col;
+        if (r >= to.rows) return;
+        const Row y = row_at(to, r, ref, l, grp == 0);
+        if (y.sums != nullptr) {
+            float* p = y.sums + 4 * grp;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = 32 * d + 8 * i + 4 * half;
-                    const float x[4] = {o[t][d][4 * i], o[t][d][4 * i + 1], o[t][d][4 * i + 2], o[t][d][4 * i + 3]};
-                    if (e < a.c.D) put(to, r, e, x, ref[t], l[t], d == 0 && i == 0 && half == 0);
+                for (int i = 0; i < C::EA / 4; ++i) {
+                    const int e = M * d + 4 * C::NG * i;
+                    if (e + 4 * grp < a.c.D)
+                        *reinterpret_cast<f32x4*>(p + e) = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+                }
+        } else {
+            TS* p = y.out + 4 * grp;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < C::EA / 4; ++i) {
+                    const int e = M * d + 4 * C::NG * i;
+                    if (e + 4 * grp >= a.c.D) continue;
+                    const f32x4 x = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]} * y.inv;
+                    if constexpr (C::HALF) *reinterpret_cast<u32x2*>(p + e) = u32x2{pack<T>(x[0], x[1]), pack<T>(x[2], x[3])};
+                    else *reinterpret_cast<f32x4*>(p + e) = x;
                 }
         }
     }
 
-    // The block's rows again, plainly: a wave a row, 64 keys at a time, over the keys p0 .. p1 - 1 of the prefix
+    // The wave's rows again, plainly: one after the other, 64 keys at a time, over the keys p0 .. p1 - 1 of the prefix
     // and k0 .. k1 - 1 of the run (seen0 + token of them seen).
     __device__ __forceinline__ void redo(const To& to, const Keys& prefix, int p0, int p1, const Keys& own, int k0, int k1,
                                          int seen0) {
 #pragma unroll 1
-        for (int r = to.row0 + wave; r < min(to.row0 + C::BM, to.rows); r += C::NW) {
+        for (int x0 = 0; x0 < M; ++x0) {
+            const int r = to.row0 + wave * M + x0;
+            if (r >= to.rows) break;
             const int i = r / a.G, g = r - i * a.G;
             const TS* qp = static_cast<const TS*>(a.c.q.p) + (to.first + i) * a.c.q.row + (long long)(to.hk * a.G + g) * a.c.q.head;
             float m = kNoMax, sum = 0.0f, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -622,9 +657,12 @@ struct Block {
                     }
                 }
             }
+            const Row y = row_at(to, r, m, sum, lane == 0);
             for (int z = 0; z < 4; ++z) {
-                const float one[1] = {x[z]};
-                if (lane + 64 * z < a.c.D) put(to, r, lane + 64 * z, one, m, sum, z == 0 && lane == 0);
+                const int e = lane + 64 * z;
+                if (e >= a.c.D) break;
+                if (y.sums != nullptr) y.sums[e] = x[z];
+                else y.out[e] = from_f32<T>(x[z] * y.inv);
             }
         }
     }
@@ -654,15 +692,15 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
     const int B = a.prefix_rows ? 1 : a.c.B, b = x % B;
     x /= B;
     const int part = x % a.splits, back = x / a.splits;
-    const int first = uniform(a.prefix_rows ? 0 : a.c.offsets[b]);
-    const int T = uniform(a.prefix_rows ? a.c.N : a.c.offsets[b + 1]) - first;
+    const int first = uniform(a.prefix_rows ? 0 : entry(a.c.offsets, b));
+    const int T = uniform(a.prefix_rows ? a.c.N : entry(a.c.offsets, b + 1)) - first;
     const int rows = T * a.G, tiles = (rows + C::BM - 1) / C::BM, row0 = (tiles - 1 - back) * C::BM;
     if (row0 < 0 || rows == 0) return;
     int n = 0;
     long long begin = 0;
     if (!a.prefix_rows) {
-        n = a.c.kv_len != nullptr ? uniform(a.c.kv_len[b]) : T;
-        begin = a.c.kv_begin != nullptr ? uniform((long long)a.c.kv_begin[b]) : first;
+        n = a.c.kv_len != nullptr ? uniform(entry(a.c.kv_len, b)) : T;
+        begin = a.c.kv_begin != nullptr ? uniform((long long)entry(a.c.kv_begin, b)) : first;
     }
     const int seen0 = n - T + 1;
     const int last_token = min(row0 + C::BM, rows) - 1;
@@ -687,16 +725,23 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
         blk.set_source(a.c.k.row, a.c.v.row);
         blk.run(own, k0, k1);
     }
-    blk.join();
+    blk.sum_rows();
     const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? a.set0 + part : -1, -1};
     blk.store(to);
-    if (__syncthreads_or(blk.spoiled))
+    if (blk.spoiled)
         blk.redo(to, prefix, t0 * C::BN, min(p1 * C::BN, a.c.prefix_len), own, k0 * C::BN, max(0, min(k1 * C::BN, n)), seen0);
 }
 
 // The short form (a sequence's rows fit one tile): all (sequence, key head) runs laid end to end, counted
 // in key tiles, and cut into equal parts, one a block.  A run inside one block is finished there; pieces of
-// a cut run go to the workspace for the joining kernel.
+// a cut run go to the workspace for the joining kernel.  Loads follow the part's tiles across the ends of
+// runs, so a block's stream never dries up where a new run starts.
+struct Run {
+    int b, hk, first, T, n, tiles;  // the run
+    int t0, t1;                     // this block's tiles of it
+    long long begin;
+};
+
 template <typename C>
 __global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
     extern __shared__ __align__(1024) char lds[];
@@ -707,150 +752,197 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
     long long total;
     const bool malformed = check_and_find<C::NT>(a.c, units, &total);
     report(a, malformed);
-    if (malformed || total == 0) return;
-    const long long W = total < a.workers ? total : a.workers;
-    if (blockIdx.x >= W) return;
     const int w = blockIdx.x;
-    long long u = w * total / W;
+    const long long W = total < a.workers ? total : a.workers;
+    if (malformed || w >= W) {
+        if (a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    long long u = w * total / W;  // first unit of the consumer's run
     const long long u1 = (w + 1ll) * total / W;
-    int b;
     long long base;
-    find_unit<C::NT>(a.c, units, u, &b, &base);
-
-    Block<C> blk(a, lds);
-    blk.set_source(a.c.k.row, a.c.v.row);
-    int first = 0, T = 0, n = 0, nt = 0;
-    long long begin = 0;
+    Run ld;  // the run whose tiles are being asked for
+    find_unit<C::NT>(a.c, units, u, &ld.b, &base);
     auto open = [&] {
-        first = uniform(a.c.offsets[b]);
-        T = uniform(a.c.offsets[b + 1]) - first;
-        n = a.c.kv_len != nullptr ? uniform(a.c.kv_len[b]) : T;
-        begin = a.c.kv_begin != nullptr ? uniform((long long)a.c.kv_begin[b]) : first;
-        nt = tiles_of(T, n);
+        ld.first = uniform(entry(a.c.offsets, ld.b));
+        ld.T = uniform(entry(a.c.offsets, ld.b + 1)) - ld.first;
+        ld.n = a.c.kv_len != nullptr ? uniform(entry(a.c.kv_len, ld.b)) : ld.T;
+        ld.begin = a.c.kv_begin != nullptr ? uniform((long long)entry(a.c.kv_begin, ld.b)) : ld.first;
+        ld.tiles = tiles_of(ld.T, ld.n);
     };
     open();
+    Block<C> blk(a, lds);
+    blk.set_source(a.c.k.row, a.c.v.row);
+    const int q_at = C::NS * C::STAGE;
+
+    int left = (int)(u1 - u);  // tiles not asked for yet
     const int within = (int)(u - base);
-    int hk = within / nt, tile = within - hk * nt;
+    ld.hk = within / ld.tiles;
+    ld.t0 = within - ld.hk * ld.tiles;
+    Keys keys;
+    auto enter = [&] {  // the loads go on in run ld
+        ld.t1 = min(ld.tiles, ld.t0 + left);
+        keys = Keys{static_cast<const char*>(a.c.k.p) + (ld.begin * a.c.k.row + ld.hk * a.c.k.head) * C::ES,
+                    static_cast<const char*>(a.c.v.p) + (ld.begin * a.c.v.row + ld.hk * a.c.v.head) * C::ES, ld.n};
+        blk.ask_rows(q_at, ld.T, ld.first, ld.hk);
+    };
+    enter();
+    Run run = ld;  // the run being computed; the loads are in it or in the next one
+    bool crossed = false, fresh = true;  // fresh: the run's queries are still in LDS only
+    int ask = ld.t0, ahead = 0, ask_stage = 0, stage = 0, t = run.t0;
+    auto fill = [&] {
+        while (ahead < C::NS - 1 && left > 0) {
+            if (ask == ld.t1) {
+                if (crossed || fresh) return;  // the queries' place in LDS holds one run's
+                if (++ld.hk == HK) {
+                    ld.hk = 0;
+                    do {
+                        ++ld.b;
+                        open();
+                    } while (ld.tiles == 0);
+                }
+                ld.t0 = ask = 0;
+                enter();
+                crossed = true;
+            }
+            blk.load_tile(keys, ask, true, ask_stage);
+            ask_stage = ask_stage == C::NS - 1 ? 0 : ask_stage + 1;
+            ++ask;
+            ++ahead;
+            --left;
+        }
+    };
+    fill();
     while (true) {
-        const int count = (int)min((long long)(nt - tile), u1 - u), rows = T * a.G;
-        blk.load_rows(0, rows, first, hk);
-        blk.see(0, rows, true, n - T + 1, n);
-        const Keys s{static_cast<const char*>(a.c.k.p) + (begin * a.c.k.row + hk * a.c.k.head) * C::ES,
-                     static_cast<const char*>(a.c.v.p) + (begin * a.c.v.row + hk * a.c.v.head) * C::ES, n};
-        blk.run(s, tile, tile + count);
-        blk.join();
-        // a worker's slot 0: its first run, cut at the front; slot 1: a run that goes on in the next worker
-        const bool whole = count == nt;
-        const typename Block<C>::To to{0, rows, first, hk, whole && a.to_sets ? a.set0 : -1,
-                                       whole ? -1 : w * 2ll + (tile == 0 ? 1 : 0)};
-        blk.store(to);
-        if (T > 1 && __syncthreads_or(blk.spoiled))
-            blk.redo(to, s, 0, 0, s, tile * C::BN, min((tile + count) * C::BN, n), n - T + 1);
-        if (tile == 0 && a.row_info != nullptr) {
-            // the worker that holds the run's last unit
-            const long long last = u + nt - 1, w_last = ((last + 1) * W - 1) / total;
-            for (int i = threadIdx.x; i < T; i += C::NT)
-                a.row_info[(long long)(first + i) * HK + hk] = make_int2(whole ? -1 : w, (int)(w_last - w + 1) * 128 + i);
+        // the next tile (and what was asked for before it) is there; with the ring full, NS - 2 newer ones may
+        // be on their way
+        if (ahead == C::NS - 1) wait_and_meet<(C::NS - 2) * 2 * C::JN>();
+        else wait_and_meet<0>();
+        if (t == run.t1) {
+            // Results are stored here, behind the wait, so that no later wait for tiles has to sit out the stores.
+            blk.sum_rows();
+            const int rows = run.T * a.G;
+            const bool whole = run.t1 - run.t0 == run.tiles;
+            // a worker's slot 0: a run cut at the front; slot 1: a run that starts here and goes on in the next worker
+            const typename Block<C>::To to{0, rows, run.first, run.hk, whole && a.to_sets ? a.set0 : -1,
+                                           whole ? -1 : w * 2ll + (run.t0 == 0 ? 1 : 0)};
+            blk.store(to);
+            if (blk.spoiled) {
+                const Keys own{static_cast<const char*>(a.c.k.p) + (run.begin * a.c.k.row + run.hk * a.c.k.head) * C::ES,
+                               static_cast<const char*>(a.c.v.p) + (run.begin * a.c.v.row + run.hk * a.c.v.head) * C::ES,
+                               run.n};
+                blk.redo(to, own, 0, 0, own, run.t0 * C::BN, min(run.t1 * C::BN, run.n), run.n - run.T + 1);
+            }
+            if (run.t0 == 0) {
+                // the worker that holds the run's last unit
+                const long long last = u + run.tiles - 1;
+                const int pieces = whole ? 1 : (int)(((last + 1) * W - 1) / total) - w + 1;
+                if (a.row_info != nullptr)
+                    for (int i = threadIdx.x; i < run.T; i += C::NT)
+                        a.row_info[(long long)(run.first + i) * HK + run.hk] = make_int2(whole ? -1 : w, pieces * 128 + i);
+                if (!whole && a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(run.first, run.T, run.hk, pieces);
+            }
+            u += run.t1 - run.t0;
+            if (u >= u1) {
+                if ((whole || run.t0 != 0) && a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(0, 0, 0, 0);
+                return;
+            }
+            run = ld;
+            t = run.t0;
+            crossed = false;
+            fresh = true;
         }
-        u += count;
-        if (u >= u1) break;
-        tile = 0;
-        if (++hk == HK) {
-            hk = 0;
-            do {
-                ++b;
-                open();
-            } while (nt == 0);
+        if (fresh) {
+            blk.fresh_addresses();
+            blk.see(0, run.T * a.G, true, run.n - run.T + 1, run.n);
+            blk.take_rows(lds + q_at, run.T * a.G);
+            wait_and_meet<63>();  // all waves have read the queries: their place may be written again
+            fresh = false;
         }
+        --ahead;
+        fill();
+        blk.use_tile(stage, t * C::BN);
+        stage = stage == C::NS - 1 ? 0 : stage + 1;
+        ++t;
     }
 }
 
 // ---- which tile for which call -------------------------------------------------------------------
-// Head widths are compiled for 64, 128 and 256.  A stage holds about 32 KB of keys and values, so two
-// blocks of two stages fit a CU.
+// Head widths are compiled for 64, 128 and 256.
+//
+// Short form, 16 x 16 tiles, one wave for every 16 rows (1, 2, 3, 4 or 8 waves): what counts is bytes on their way,
+// 64 to 96 KB a CU over its blocks.
 template <typename T, int DP, int WR>
-struct Pick;
-#define GDN_ATTN_PICK(T, DP, WR, WK, KT, NS, WAVES) \
-    template <>                                     \
-    struct Pick<T, DP, WR> {                        \
-        using C = Cfg<T, DP, WR, WK, 1, KT, NS, WAVES>; \
-    };
-#define GDN_ATTN_PICK_HALF(T)              \
-    GDN_ATTN_PICK(T, 64, 1, 4, 1, 2, 2)    \
-    GDN_ATTN_PICK(T, 64, 2, 2, 2, 2, 2)    \
-    GDN_ATTN_PICK(T, 64, 4, 1, 2, 2, 2)    \
-    GDN_ATTN_PICK(T, 128, 1, 2, 1, 2, 1)   \
-    GDN_ATTN_PICK(T, 128, 2, 2, 1, 2, 2)   \
-    GDN_ATTN_PICK(T, 128, 4, 1, 2, 2, 2)   \
-    GDN_ATTN_PICK(T, 256, 1, 1, 1, 2, 1)   \
-    GDN_ATTN_PICK(T, 256, 2, 1, 1, 2, 1)   \
-    GDN_ATTN_PICK(T, 256, 4, 1, 1, 2, 2)
-GDN_ATTN_PICK_HALF(BF16)
-GDN_ATTN_PICK_HALF(F16)
-GDN_ATTN_PICK(F32, 64, 1, 2, 1, 2, 1)
-GDN_ATTN_PICK(F32, 64, 2, 2, 1, 2, 2)
-GDN_ATTN_PICK(F32, 64, 4, 1, 2, 2, 2)
-GDN_ATTN_PICK(F32, 128, 1, 1, 1, 2, 1)
-GDN_ATTN_PICK(F32, 128, 2, 1, 1, 2, 1)
-GDN_ATTN_PICK(F32, 128, 4, 1, 1, 2, 2)
-GDN_ATTN_PICK(F32, 256, 1, 1, 1, 2, 1)
-GDN_ATTN_PICK(F32, 256, 2, 1, 1, 2, 1)
-GDN_ATTN_PICK(F32, 256, 4, 1, 1, 2, 1)
+struct Short {
+    static constexpr int RB = DP * (int)sizeof(typename T::storage);
+    static constexpr int NS = RB <= 256 ? 4 : RB <= 512 && WR == 3 ? 4 : RB <= 512 && WR == 4 ? 3 : 2;
+    using C = Cfg<T, 16, DP, WR, 1, NS, 1>;
+};
+// Long form, 32 x 32 tiles, four waves.
+template <typename T, int DP>
+struct Long {
+    static constexpr int RB = DP * (int)sizeof(typename T::storage);
+    using C = Cfg<T, 32, DP, 4, RB <= 256 ? 2 : 1, 2, RB <= 512 ? 2 : 1>;
+};
 
-// What the host needs to know of a configuration.
+// What the host needs to know of a configuration: tile sizes, bytes of the ring and of a row in LDS.
 struct Shape {
-    int bm, bn, per_cu;
+    int bm, bn, ring, row;
 };
 template <typename C>
 constexpr Shape shape_of() {
-    return Shape{C::BM, C::BN, 2 * C::LDS <= 156 * 1024 ? 2 : 1};
+    return Shape{C::BM, C::BN, C::LDS, C::RB};
 }
 
+constexpr int kMaxLds = 159 * 1024;  // of the 160 KB, less the kernels' own few words
+
 template <typename C, bool LONG>
-hipError_t start(const Args& a, long long blocks, hipStream_t stream) {
-    if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
+hipError_t start(const Args& a, long long blocks, int lds, hipStream_t stream) {
+    if (blocks > kMaxBlocks || lds > kMaxLds) return hipErrorInvalidConfiguration;
     void (*f)(Args);
     if constexpr (LONG) f = &long_kernel<C>;
     else f = &short_kernel<C>;
     // more than 64 KB of LDS has to be asked for; the attribute belongs to the current device
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
     if (e != hipSuccess) return e;
-    f<<<(unsigned)blocks, C::NT, C::LDS, stream>>>(a);
+    f<<<(unsigned)blocks, C::NT, lds, stream>>>(a);
     return hipGetLastError();
 }
 
-// dp 64, 128 or 256; wr 1, 2 or 4.  The long form runs at wr = 4.
-template <typename T, typename F>
-auto with_pick(int dp, int wr, F f) {
-    switch (dp * 8 + wr) {
-        case 64 * 8 + 1: return f(Pick<T, 64, 1>{});
-        case 64 * 8 + 2: return f(Pick<T, 64, 2>{});
-        case 64 * 8 + 4: return f(Pick<T, 64, 4>{});
-        case 128 * 8 + 1: return f(Pick<T, 128, 1>{});
-        case 128 * 8 + 2: return f(Pick<T, 128, 2>{});
-        case 128 * 8 + 4: return f(Pick<T, 128, 4>{});
-        case 256 * 8 + 1: return f(Pick<T, 256, 1>{});
-        case 256 * 8 + 2: return f(Pick<T, 256, 2>{});
-        default: return f(Pick<T, 256, 4>{});
+// dp 64, 128 or 256; wr 1, 2, 3, 4 or 8.
+template <typename T, int DP, typename F>
+auto with_waves(int wr, F f) {
+    switch (wr) {
+        case 1: return f(Short<T, DP, 1>{});
+        case 2: return f(Short<T, DP, 2>{});
+        case 3: return f(Short<T, DP, 3>{});
+        case 4: return f(Short<T, DP, 4>{});
+        default: return f(Short<T, DP, 8>{});
     }
+}
+template <typename T, typename F>
+auto with_short(int dp, int wr, F f) {
+    return dp == 64 ? with_waves<T, 64>(wr, f) : dp == 128 ? with_waves<T, 128>(wr, f) : with_waves<T, 256>(wr, f);
+}
+template <typename T, typename F>
+auto with_long(int dp, F f) {
+    return dp == 64 ? f(Long<T, 64>{}) : dp == 128 ? f(Long<T, 128>{}) : f(Long<T, 256>{});
 }
 
 // One translation unit per type holds its kernels.
 template <typename T>
-hipError_t start_short(const Args& a, int dp, int wr, long long blocks, hipStream_t stream);
+hipError_t start_short(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream);
 template <typename T>
-hipError_t start_long(const Args& a, int dp, long long blocks, hipStream_t stream);
+hipError_t start_long(const Args& a, int dp, long long blocks, int lds, hipStream_t stream);
 
-#define GDN_ATTN_INSTANCES(T)                                                                                     \
-    template <>                                                                                                   \
-    hipError_t start_short<T>(const Args& a, int dp, int wr, long long blocks, hipStream_t stream) {              \
-        return with_pick<T>(dp, wr, [&](auto p) { return start<typename decltype(p)::C, false>(a, blocks, stream); }); \
-    }                                                                                                             \
-    template <>                                                                                                   \
-    hipError_t start_long<T>(const Args& a, int dp, long long blocks, hipStream_t stream) {                       \
-        if (dp == 64) return start<typename Pick<T, 64, 4>::C, true>(a, blocks, stream);                          \
-        if (dp == 128) return start<typename Pick<T, 128, 4>::C, true>(a, blocks, stream);                        \
-        return start<typename Pick<T, 256, 4>::C, true>(a, blocks, stream);                                       \
+#define GDN_ATTN_INSTANCES(T)                                                                                           \
+    template <>                                                                                                         \
+    hipError_t start_short<T>(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream) {           \
+        return with_short<T>(dp, wr, [&](auto p) { return start<typename decltype(p)::C, false>(a, blocks, lds, stream); }); \
+    }                                                                                                                   \
+    template <>                                                                                                         \
+    hipError_t start_long<T>(const Args& a, int dp, long long blocks, int lds, hipStream_t stream) {                    \
+        return with_long<T>(dp, [&](auto p) { return start<typename decltype(p)::C, true>(a, blocks, lds, stream); });   \
     }
 
 }  // namespace attn

@@ -60,6 +60,8 @@ gdn_status check_attn_desc(const gdn_attn_desc* d, gdn::AttnLaunch* a) {
     const int64_t* rows[4] = {d->k_stride, d->v_stride, d->prefix_k_stride, d->prefix_v_stride};
     for (int i = 0; i < (d->prefix_len > 0 ? 4 : 2); ++i)
         if (rows[i][0] > kMaxRowBytes / dsize(d->dtype)) return GDN_ERR_OVERFLOW;
+    // the plan of a call also looks at how far apart the queries lie
+    a->q = gdn::HeadRows{nullptr, d->q_stride[0], d->q_stride[1]};
     a->B = d->B;
     a->N = d->N;
     a->H = d->H;
@@ -76,7 +78,7 @@ gdn_status check_attn_desc(const gdn_attn_desc* d, gdn::AttnLaunch* a) {
 gdn_status attention(const gdn_attn_desc* d, const void* q, const void* pk, const void* pv, const void* k,
                      const void* v, const int32_t* offsets, const int64_t* kv_begin, const int32_t* kv_len, void* out,
                      float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status, hipStream_t stream) {
-    gdn::AttnLaunch a;
+    gdn::AttnLaunch a{};
     gdn_status st = check_attn_desc(d, &a);
     if (st != GDN_OK) return st;
     if (offsets == nullptr || (kv_begin == nullptr) != (kv_len == nullptr)) return GDN_ERR_NULL;
@@ -184,7 +186,7 @@ gdn_status gdn_attention_prefix_varlen(const gdn_attn_desc* d, const void* q, co
 
 gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc* d, size_t* bytes) {
     if (bytes == nullptr) return GDN_ERR_NULL;
-    gdn::AttnLaunch a;
+    gdn::AttnLaunch a{};
     const gdn_status st = check_attn_desc(d, &a);
     if (st == GDN_OK) *bytes = gdn::attention_workspace_bytes(a);
     return st;
