@@ -8,6 +8,7 @@ library.  Every step of the computation runs in the library's HIP kernels; there
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -354,40 +355,54 @@ def decode_step(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, *,
     return out, state_out, conv_state_out
 
 
-def _head_view(t: torch.Tensor, heads: int, D: int, like: torch.Tensor, what: str):
-    """(device address, row and head strides) of a [rows, heads, D] tensor with contiguous heads."""
-    if t.dtype != like.dtype:
-        raise TypeError(f"{what}: dtype {t.dtype} differs from {like.dtype}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{what} must be on {like.device}")
-    shape = t.shape
+# The operators below are called once a layer and token, so their host side is kept short: descriptors are
+# packed straight to bytes (gdn_rope_desc and gdn_attn_desc have one layout), and addresses and streams
+# passed as plain integers.
+_DESC = struct.Struct("=7iIfi13q")
+_NO_ROWS = (None, 0, 0, 0)
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _head_rows(t: torch.Tensor, heads: int, D: int, dtype, dev: int, what: str):
+    """(device address, row stride, head stride, rows) of a [rows, heads, D] tensor with contiguous heads."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: dtype {t.dtype} differs from {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on cuda:{dev}")
+    shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != D:
         raise ValueError(f"{what} must be [rows, {heads}, {D}], got {tuple(shape)}")
-    row, head, elem = t.stride()
-    if elem != 1 and D != 1:
+    if stride[2] != 1 and D != 1:
         raise ValueError(f"{what}: the elements of a head must be contiguous")
     # the stride of an axis of one entry names nothing
-    return t.data_ptr(), (row if shape[0] > 1 else D * heads, head if heads > 1 else D)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * D, stride[1] if heads > 1 else D, shape[0]
 
 
-def _flat(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, like: torch.Tensor, what: str):
+def _flat(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, dev: int, what: str):
     """Device address of a contiguous vector of n entries (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{what} must be on {like.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on cuda:{dev}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous with {n} entries")
     return t.data_ptr()
 
 
-def _need_gpu(q: torch.Tensor):
+def _query_shape(q: torch.Tensor):
+    """(N, H, D, device index) of the queries."""
     if q.dim() != 3:
         raise ValueError(f"q must be [N, heads, D], got {tuple(q.shape)}")
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("q must be a device tensor")
+    N, H, D = q.shape
+    return N, H, D, dev
 
 
 def qk_norm_rope_varlen(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], offsets: torch.Tensor, *,
@@ -403,91 +418,93 @@ def qk_norm_rope_varlen(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
     (int64 [B]), goes to row kv_begin[b] + past[b] + i of k_out and v_out [rows, HK, D]; without
     kv_begin to the row of its own index.  q_out may be q; outputs not given are allocated (k_out and
     v_out only without kv_begin).  Returns (q_out, k_out, v_out)."""
-    _need_gpu(q)
-    N, H, D = q.shape
+    N, H, D, dev = _query_shape(q)
     HK = k.shape[1]
     B = offsets.numel() - 1
-    if k_out is None and kv_begin is not None:
-        raise ValueError("k_out is required with kv_begin")
+    dtype = q.dtype
+    if kv_begin is not None and (k_out is None or (v is not None and v_out is None)):
+        raise ValueError("k_out and v_out are required with kv_begin")
     if q_out is None:
-        q_out = torch.empty((N, H, D), dtype=q.dtype, device=q.device)
+        q_out = q.new_empty((N, H, D))
     if k_out is None:
-        k_out = torch.empty((N, HK, D), dtype=q.dtype, device=q.device)
+        k_out = q.new_empty((N, HK, D))
+    qp, qr, qh, _ = _head_rows(q, H, D, dtype, dev, "q")
+    kp, kr, kh, nk = _head_rows(k, HK, D, dtype, dev, "k")
+    qop, qor, qoh, nqo = _head_rows(q_out, H, D, dtype, dev, "q_out")
+    kop, kor, koh, rows = _head_rows(k_out, HK, D, dtype, dev, "k_out")
+    if nk != N or nqo != N:
+        raise ValueError("q, k and q_out must have one row per token")
     if v is None:
         v_out = None
-    elif v_out is None:
-        if kv_begin is not None:
-            raise ValueError("v_out is required with kv_begin")
-        v_out = torch.empty((N, HK, D), dtype=q.dtype, device=q.device)
-    rows = k_out.shape[0]
-    qp, qs = _head_view(q, H, D, q, "q")
-    kp, ks = _head_view(k, HK, D, q, "k")
-    qop, qos = _head_view(q_out, H, D, q, "q_out")
-    kop, kos = _head_view(k_out, HK, D, q, "k_out")
-    if k.shape[0] != N or q_out.shape[0] != N:
-        raise ValueError("q, k and q_out must have one row per token")
-    if v is not None:
-        vp, vs = _head_view(v, HK, D, q, "v")
-        vop, vos = _head_view(v_out, HK, D, q, "v_out")
-        if v.shape[0] != N or v_out.shape[0] != rows:
-            raise ValueError("v must have one row per token and v_out as many rows as k_out")
+        vp, vr, vh, _ = vop, vor, voh, _ = _NO_ROWS
     else:
-        vp, vs, vop, vos = None, (0, 0), None, (0, 0)
+        if v_out is None:
+            v_out = q.new_empty((N, HK, D))
+        vp, vr, vh, nv = _head_rows(v, HK, D, dtype, dev, "v")
+        vop, vor, voh, nvo = _head_rows(v_out, HK, D, dtype, dev, "v_out")
+        if nv != N or nvo != rows:
+            raise ValueError("v must have one row per token and v_out as many rows as k_out")
     half = inv_freq.numel()
-    d = _abi.RopeDesc(B, N, H, HK, D, 2 * half, _code(q, "q"), _abi.ROPE_INTERLEAVED if interleaved else 0, eps, 0,
-                      rows, qs, ks, vs, qos, kos, vos)
+    desc = _DESC.pack(B, N, H, HK, D, 2 * half, _code(q, "q"), _abi.ROPE_INTERLEAVED if interleaved else 0, eps, 0, rows,
+                      qr, qh, kr, kh, vr, vh, qor, qoh, kor, koh, vor, voh)
     st = lib().gdn_qk_norm_rope_varlen(
-        ctypes.byref(d), qp, kp, vp, _flat(inv_freq, half, torch.float32, q, "inv_freq"),
-        _flat(q_weight, D, torch.float32, q, "q_weight"), _flat(k_weight, D, torch.float32, q, "k_weight"),
-        _flat(offsets, B + 1, torch.int32, q, "offsets"), _flat(past, B, torch.int32, q, "past"),
-        _flat(positions, B, torch.int32, q, "positions"), _flat(kv_begin, B, torch.int64, q, "kv_begin"), qop, kop, vop,
-        _flat(dev_status, 1, torch.int32, q, "dev_status"), _stream(q.device))
+        desc, qp, kp, vp, _flat(inv_freq, half, torch.float32, dev, "inv_freq"),
+        _flat(q_weight, D, torch.float32, dev, "q_weight"), _flat(k_weight, D, torch.float32, dev, "k_weight"),
+        _flat(offsets, B + 1, torch.int32, dev, "offsets"), _flat(past, B, torch.int32, dev, "past"),
+        _flat(positions, B, torch.int32, dev, "positions"), _flat(kv_begin, B, torch.int64, dev, "kv_begin"), qop, kop,
+        vop, _flat(dev_status, 1, torch.int32, dev, "dev_status"), _raw_stream(dev))
     _check(st, "gdn_qk_norm_rope_varlen")
     return q_out, k_out, v_out
 
 
 def _attention(q, prefix_k, prefix_v, k, v, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse, workspace,
                dev_status, where):
-    _need_gpu(q)
-    N, H, D = q.shape
+    N, H, D, dev = _query_shape(q)
     HK = k.shape[1]
     B = offsets.numel() - 1
+    dtype = q.dtype
+    qp, qr, qh, _ = _head_rows(q, H, D, dtype, dev, "q")
+    kp, kr, kh, rows = _head_rows(k, HK, D, dtype, dev, "k")
+    vp, vr, vh, nv = _head_rows(v, HK, D, dtype, dev, "v")
+    if nv != rows:
+        raise ValueError("k and v must have the same rows")
     if out is None:
-        out = torch.empty((N, H, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty((N, H, D))
+        op, orow, oh = out.data_ptr(), H * D, D
+    else:
+        op, orow, oh, no = _head_rows(out, H, D, dtype, dev, "out")
+        if no != N:
+            raise ValueError("out must have one row per token")
+    if prefix_k is None:
+        pkp, pkr, pkh, prefix = pvp, pvr, pvh, _ = _NO_ROWS
+    else:
+        pkp, pkr, pkh, prefix = _head_rows(prefix_k, HK, D, dtype, dev, "prefix_k")
+        pvp, pvr, pvh, npv = _head_rows(prefix_v, HK, D, dtype, dev, "prefix_v")
+        if npv != prefix:
+            raise ValueError("prefix_k and prefix_v must have the same rows")
     if lse is None and return_lse:
         lse = torch.empty((N, H), dtype=torch.float32, device=q.device)
-    qp, qs = _head_view(q, H, D, q, "q")
-    op, os_ = _head_view(out, H, D, q, "out")
-    kp, ks = _head_view(k, HK, D, q, "k")
-    vp, vs = _head_view(v, HK, D, q, "v")
-    rows = k.shape[0]
-    if v.shape[0] != rows or out.shape[0] != N:
-        raise ValueError("k and v must have the same rows, and out one row per token")
-    if prefix_k is not None:
-        pkp, pks = _head_view(prefix_k, HK, D, q, "prefix_k")
-        pvp, pvs = _head_view(prefix_v, HK, D, q, "prefix_v")
-        prefix = prefix_k.shape[0]
-        if prefix_v.shape[0] != prefix:
-            raise ValueError("prefix_k and prefix_v must have the same rows")
-    else:
-        pkp, pks, pvp, pvs, prefix = None, (0, 0), None, (0, 0), 0
-    d = _abi.AttnDesc(B, N, H, HK, D, N if max_q is None else max_q, _code(q, "q"), 0, scale, prefix, rows, qs, ks, vs,
-                      os_, pks, pvs)
-    ref = ctypes.byref(d)
+    desc = _DESC.pack(B, N, H, HK, D, N if max_q is None else min(max_q, N), _code(q, "q"), 0, scale, prefix, rows,
+                      qr, qh, kr, kh, vr, vh, orow, oh, pkr, pkh, pvr, pvh)
     L = lib()
     if workspace is None:
-        n = ctypes.c_size_t(0)
-        _check(L.gdn_attention_workspace_bytes(ref, ctypes.byref(n)), "gdn_attention_workspace_bytes")
-        if n.value:
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
-    ws, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace, "workspace"), workspace.nbytes)
-    tail = (_flat(offsets, B + 1, torch.int32, q, "offsets"), _flat(kv_begin, B, torch.int64, q, "kv_begin"),
-            _flat(kv_len, B, torch.int32, q, "kv_len"), op, _flat(lse, N * H, torch.float32, q, "lse"), ws, ws_bytes,
-            _flat(dev_status, 1, torch.int32, q, "dev_status"), _stream(q.device))
-    if prefix_k is None:
-        st = L.gdn_attention_varlen(ref, qp, kp, vp, *tail)
+        n = ctypes.c_size_t()
+        _check(L.gdn_attention_workspace_bytes(desc, ctypes.byref(n)), "gdn_attention_workspace_bytes")
+        ws_bytes = n.value
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
+        else:
+            ws = None
     else:
-        st = L.gdn_attention_prefix_varlen(ref, qp, pkp, pvp, kp, vp, *tail)
+        ws, ws_bytes = _ptr(workspace, "workspace"), workspace.nbytes
+    tail = (_flat(offsets, B + 1, torch.int32, dev, "offsets"), _flat(kv_begin, B, torch.int64, dev, "kv_begin"),
+            _flat(kv_len, B, torch.int32, dev, "kv_len"), op, _flat(lse, N * H, torch.float32, dev, "lse"), ws, ws_bytes,
+            _flat(dev_status, 1, torch.int32, dev, "dev_status"), _raw_stream(dev))
+    if prefix_k is None:
+        st = L.gdn_attention_varlen(desc, qp, kp, vp, *tail)
+    else:
+        st = L.gdn_attention_prefix_varlen(desc, qp, pkp, pvp, kp, vp, *tail)
     _check(st, where)
     return out, lse
 
@@ -521,7 +538,9 @@ def attention_workspace_bytes(q: torch.Tensor, B: int, *, HK: int, max_q: int, k
     """Bytes of device scratch attention_varlen (prefix_len 0) or attention_prefix_varlen takes as
     `workspace` for queries like q; it allocates them itself when the caller keeps none."""
     N, H, D = q.shape
-    d = _abi.AttnDesc(B, N, H, HK, D, max_q, _code(q, "q"), 0, 0.0, prefix_len, kv_rows, q.stride()[:2])
-    n = ctypes.c_size_t(0)
-    _check(lib().gdn_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)), "gdn_attention_workspace_bytes")
-    return int(n.value)
+    qr, qh, _ = q.stride()
+    desc = _DESC.pack(B, N, H, HK, D, min(max_q, N), _code(q, "q"), 0, 0.0, prefix_len, kv_rows, qr if N > 1 else H * D,
+                      qh if H > 1 else D, *([0] * 10))
+    n = ctypes.c_size_t()
+    _check(lib().gdn_attention_workspace_bytes(desc, ctypes.byref(n)), "gdn_attention_workspace_bytes")
+    return n.value

@@ -168,13 +168,14 @@ def lib() -> ctypes.CDLL:
         L.gdn_decode_step.restype = st
         L.gdn_scan_workspace_bytes.argtypes = [ctypes.POINTER(ScanDesc), ctypes.POINTER(ctypes.c_size_t)]
         L.gdn_scan_workspace_bytes.restype = st
-        L.gdn_qk_norm_rope_varlen.argtypes = [ctypes.POINTER(RopeDesc)] + [vp] * 15
+        # descriptors as addresses: a structure by reference, or its bytes
+        L.gdn_qk_norm_rope_varlen.argtypes = [vp] + [vp] * 15
         L.gdn_qk_norm_rope_varlen.restype = st
-        L.gdn_attention_varlen.argtypes = [ctypes.POINTER(AttnDesc)] + [vp] * 9 + [ctypes.c_size_t, vp, vp]
+        L.gdn_attention_varlen.argtypes = [vp] + [vp] * 9 + [ctypes.c_size_t, vp, vp]
         L.gdn_attention_varlen.restype = st
-        L.gdn_attention_prefix_varlen.argtypes = [ctypes.POINTER(AttnDesc)] + [vp] * 11 + [ctypes.c_size_t, vp, vp]
+        L.gdn_attention_prefix_varlen.argtypes = [vp] + [vp] * 11 + [ctypes.c_size_t, vp, vp]
         L.gdn_attention_prefix_varlen.restype = st
-        L.gdn_attention_workspace_bytes.argtypes = [ctypes.POINTER(AttnDesc), ctypes.POINTER(ctypes.c_size_t)]
+        L.gdn_attention_workspace_bytes.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
         L.gdn_attention_workspace_bytes.restype = st
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p

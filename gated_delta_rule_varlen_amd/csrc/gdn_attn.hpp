@@ -24,6 +24,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <climits>
 
 #include "gdn_device.hpp"
@@ -902,9 +903,18 @@ hipError_t start(const Args& a, long long blocks, int lds, hipStream_t stream) {
     void (*f)(Args);
     if constexpr (LONG) f = &long_kernel<C>;
     else f = &short_kernel<C>;
-    // more than 64 KB of LDS has to be asked for; the attribute belongs to the current device
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
-    if (e != hipSuccess) return e;
+    if (lds > 64 * 1024) {
+        // has to be asked for, once on each device (asking twice does no harm)
+        static std::atomic<uint64_t> asked{0};
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        const uint64_t bit = 1ull << (dev & 63);
+        if (e == hipSuccess && (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit))) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
+            if (e == hipSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
+        }
+        if (e != hipSuccess) return e;
+    }
     f<<<(unsigned)blocks, C::NT, lds, stream>>>(a);
     return hipGetLastError();
 }

@@ -22,40 +22,34 @@ namespace gdn {
 namespace {
 
 constexpr int NT = 256;        // threads per block
-constexpr int MAX_TPB = 8;     // tokens per block at most
+constexpr int MAX_TPB = 16;    // tokens per block at most
 constexpr int MAX_HALF = 128;  // rotated pairs at most
 
-// Whole-call check: the offsets, and for every sequence with tokens the rows it writes.  Also counts
-// the offsets at or below token t0, which gives its sequence (the last one starting there, so empty
-// sequences are passed over).  Reached by all threads of the block.
-__device__ __forceinline__ bool rope_malformed(const RopeLaunch& a, int t0, int& b0) {
-    int bad = 0, at_or_below = 0;
-    for (int i = threadIdx.x; i <= a.B; i += NT) {
-        const int o = a.offsets[i];
-        if (i == 0) {
-            bad |= (o != 0);
-        } else {
-            const int prev = a.offsets[i - 1];
-            bad |= (prev > o);
-            if (prev < o) {
-                const long long past = a.past != nullptr ? a.past[i - 1] : 0;
-                bad |= (past < 0);
-                if (a.kv_begin != nullptr) {
-                    const long long begin = a.kv_begin[i - 1];
-                    bad |= (begin < 0) | (begin > a.cache_rows) | (begin + past + ((long long)o - prev) > a.cache_rows);
-                }
-            }
+// What the block's tokens need of their sequences.
+struct Token {
+    long long pos, row;
+};
+
+// Whole-call check: the offsets, and for every sequence with tokens the rows it writes.  The thread that holds a
+// sequence of the block's tokens t0 .. t1 - 1 leaves their positions and rows in `tok`, so nothing of the call's
+// small arrays is read a second time.  Reached by all threads of the block.
+__device__ __forceinline__ bool rope_malformed(const RopeLaunch& a, int t0, int t1, Token* tok) {
+    int bad = 0;
+    for (int i = threadIdx.x; i < a.B; i += NT) {
+        const int o = a.offsets[i], e = a.offsets[i + 1];
+        const long long past = a.past != nullptr ? a.past[i] : 0;
+        const long long first = a.positions != nullptr ? a.positions[i] : past;
+        const long long begin = a.kv_begin != nullptr ? a.kv_begin[i] : 0;
+        bad |= (i == 0 && o != 0) | (o > e) | (i == a.B - 1 && e != a.N);
+        if (o < e) {
+            bad |= (past < 0);
+            if (a.kv_begin != nullptr)
+                bad |= (begin < 0) | (begin > a.cache_rows) | (begin + past + ((long long)e - o) > a.cache_rows);
         }
-        if (i == a.B) bad |= (o != a.N);
-        at_or_below += (o <= t0);
+        for (int t = max(o, t0); t < min(e, t1); ++t)
+            tok[t - t0] = Token{first + (t - o), a.kv_begin != nullptr ? begin + past + (t - o) : t};
     }
-    __shared__ int count;
-    if (threadIdx.x == 0) count = 0;
-    const bool malformed = __syncthreads_or(bad) != 0;
-    if (at_or_below != 0) atomicAdd(&count, at_or_below);
-    __syncthreads();
-    b0 = count - 1;
-    return malformed;
+    return __syncthreads_or(bad) != 0;
 }
 
 // (cos, sin) of pair j at position pos.
@@ -68,19 +62,19 @@ __device__ __forceinline__ float2 turn_of(long long pos, float freq) {
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ long long uniform(long long x) {
+    return ((long long)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x);
+}
 
 // wpt waves share a token's rows; a block takes tpb tokens.  LOG2_L: log2 of the lanes of a row.
 template <typename T, int LOG2_L, bool NEIGHBOURS>
 __global__ __launch_bounds__(NT) void rope_rows_kernel(RopeLaunch a, int tpb, int wpt) {
     using TS = typename T::storage;
-    constexpr int VEC = 16 / sizeof(TS), L = 1 << LOG2_L, R = 64 / L, UNROLL = 4;
+    constexpr int VEC = 16 / sizeof(TS), L = 1 << LOG2_L, R = 64 / L;
     __shared__ float2 turn[NT / 64][MAX_HALF];
-    const int t0 = blockIdx.x * tpb, half = a.rot / 2, lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    int b;
-    const bool malformed = rope_malformed(a, t0, b);
-    report_status(a.dev_status, malformed);
-    if (malformed) return;
-    b = uniform(b);
+    __shared__ Token tok[MAX_TPB];
+    const int t0 = blockIdx.x * tpb, t1 = min(t0 + tpb, a.N), half = a.rot / 2;
+    const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), share = wave % wpt;
 
     // the lane's two pieces
     const int j = lane & (L - 1), pairs = half / VEC;
@@ -95,87 +89,100 @@ __global__ __launch_bounds__(NT) void rope_rows_kernel(RopeLaunch a, int tpb, in
         e0 = a.rot + 2 * (j - pairs) * VEC;
         e1 = e0 + VEC;
     }
-    const bool in0 = e0 < a.D, in1 = e1 < a.D, turns = NEIGHBOURS ? e0 < a.rot : j < pairs;
+    const bool in0 = e0 < a.D, in1 = e1 < a.D;
+    // lanes without a piece read the row's first (and count it as zero below): no load stands in a branch
+    const int r0 = in0 ? e0 : 0, r1 = in1 ? e1 : 0;
+
+    // A pass is R rows (heads) of the queries, the keys or the values of a token.
+    const int pq = (a.H + R - 1) / R, pk = (a.HK + R - 1) / R, passes = pq + pk + (a.v.p != nullptr ? pk : 0);
+    union Piece {
+        u32x4 v;
+        TS e[VEC];
+    };
+    struct Rows {
+        Piece x[2];
+    };
+    auto fetch = [&](int t, int p) {
+        const HeadRows& s = p < pq ? a.q : p < pq + pk ? a.k : a.v;
+        const int heads = p < pq ? a.H : a.HK, h = (p < pq ? p : p < pq + pk ? p - pq : p - pq - pk) * R + lane / L;
+        const TS* src = static_cast<const TS*>(s.p) + t * s.row + min(h, heads - 1) * s.head;
+        Rows y;
+        y.x[0].v = *reinterpret_cast<const u32x4*>(src + r0);
+        y.x[1].v = *reinterpret_cast<const u32x4*>(src + r1);
+        return y;
+    };
+    // the first rows, the weights and the frequencies are on their way while the call is checked
+    int t = t0 + wave / wpt;
+    Rows next;
+    if (t < t1 && share < passes) next = fetch(t, share);
+    float freq[MAX_HALF / 64];
+#pragma unroll
+    for (int i = 0; i < MAX_HALF / 64; ++i) freq[i] = lane + 64 * i < half ? a.inv_freq[lane + 64 * i] : 0.0f;
     float wq[2 * VEC], wk[2 * VEC];
 #pragma unroll
     for (int i = 0; i < 2 * VEC; ++i) {
-        const int e = i < VEC ? e0 + i : e1 + i - VEC;
-        wq[i] = a.q_weight != nullptr && e < a.D ? a.q_weight[e] : 1.0f;
-        wk[i] = a.k_weight != nullptr && e < a.D ? a.k_weight[e] : 1.0f;
+        const int e = i < VEC ? r0 + i : r1 + i - VEC;
+        wq[i] = a.q_weight != nullptr ? a.q_weight[e] : 1.0f;
+        wk[i] = a.k_weight != nullptr ? a.k_weight[e] : 1.0f;
     }
-    const int heads = a.H + a.HK + (a.v.p != nullptr ? a.HK : 0), share = wave % wpt;
+    const bool malformed = rope_malformed(a, t0, t1, tok);
+    report_status(a.dev_status, malformed);
+    if (malformed) return;
 
-    for (int t = t0 + wave / wpt; t < min(t0 + tpb, a.N); t += NT / 64 / wpt) {
-        while (b + 1 < a.B && a.offsets[b + 1] <= t) ++b;
-        const int i_tok = t - a.offsets[b];
-        const long long past = a.past != nullptr ? a.past[b] : 0;
-        const long long pos = (a.positions != nullptr ? a.positions[b] : past) + i_tok;
-        const long long row = a.kv_begin != nullptr ? a.kv_begin[b] + past + i_tok : t;
-        union Piece {
-            u32x4 v;
-            TS e[VEC];
-        };
-        auto place = [&](const HeadRows& r, long long at, int h) { return static_cast<TS*>(r.p) + at * r.row + h * r.head; };
-        auto source = [&](int h) {
-            return h < a.H ? place(a.q, t, h) : h < a.H + a.HK ? place(a.k, t, h - a.H) : place(a.v, t, h - a.H - a.HK);
-        };
-        auto target = [&](int h) {
-            return h < a.H ? place(a.q_out, t, h)
-                           : h < a.H + a.HK ? place(a.k_out, row, h - a.H) : place(a.v_out, row, h - a.H - a.HK);
-        };
-        // the first rows are on their way while the table is computed
-        const int h0 = share * R + lane / L, step = wpt * R;
-        Piece x[UNROLL][2];
-        auto fetch = [&](int hb) {
+    const float inv_d = 1.0f / (float)a.D;
+    for (; t < t1; t += NT / 64 / wpt) {
+        const long long pos = uniform(tok[t - t0].pos), row = uniform(tok[t - t0].row);
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int h = hb + u * step;
-                // lanes without a piece read the row's first (and count it as zero below): no load in a branch
-                const TS* p = source(min(h, heads - 1));
-                x[u][0].v = *reinterpret_cast<const u32x4*>(p + (in0 ? e0 : 0));
-                x[u][1].v = *reinterpret_cast<const u32x4*>(p + (in1 ? e1 : 0));
-            }
-        };
-        fetch(h0);
-        for (int i = lane; i < half; i += 64) turn[wave][i] = turn_of(pos, a.inv_freq[i]);
+        for (int i = 0; i < MAX_HALF / 64; ++i)
+            if (lane + 64 * i < half) turn[wave][lane + 64 * i] = turn_of(pos, freq[i]);
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         float2 cs[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            cs[i] = turns && e0 / (NEIGHBOURS ? 2 : 1) + i < half ? turn[wave][e0 / (NEIGHBOURS ? 2 : 1) + i] : make_float2(1.0f, 0.0f);
-        for (int hb = h0; hb - lane / L < heads; hb += UNROLL * step) {
-            if (hb != h0) fetch(hb);
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int h = hb + u * step;
+        for (int i = 0; i < VEC; ++i) {
+            const int pair = (NEIGHBOURS ? e0 / 2 : e0) + i;  // the tail's lanes lie past the pairs
+            const float2 c = turn[wave][min(pair, MAX_HALF - 1)];
+            cs[i] = pair < half ? c : make_float2(1.0f, 0.0f);
+        }
+        __builtin_amdgcn_wave_barrier();
+        for (int p = share; p < passes; p += wpt) {
+            Rows now = next;
+            // the next rows of this token, or the first of the wave's next one
+            if (p + wpt < passes) next = fetch(t, p + wpt);
+            else if (t + NT / 64 / wpt < t1) next = fetch(t + NT / 64 / wpt, share);
+            const bool is_q = p < pq, is_v = p >= pq + pk;
+            const int h = (is_q ? p : is_v ? p - pq - pk : p - pq) * R + lane / L;
+            if (!is_v) {
                 float y[2 * VEC], ss = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2 * VEC; ++i) {
-                    y[i] = to_f32<T>(x[u][i / VEC].e[i % VEC]);
+                    y[i] = to_f32<T>(now.x[i / VEC].e[i % VEC]);
                     ss = fmaf(y[i], (i < VEC ? in0 : in1) ? y[i] : 0.0f, ss);
                 }
-                ss = group_sum<L>(ss);
-                if (h >= heads) continue;
-                if (h < a.H + a.HK) {
-                    const float inv = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-                    const bool is_q = h < a.H;
+                const float inv = __builtin_amdgcn_rsqf(fmaf(group_sum<L>(ss), inv_d, a.eps));
+                if (is_q) {
 #pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) y[i] = y[i] * inv * (is_q ? wq[i] : wk[i]);
+                    for (int i = 0; i < 2 * VEC; ++i) y[i] = y[i] * inv * wq[i];
+                } else {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const int lo = NEIGHBOURS ? 2 * i : i, hi = NEIGHBOURS ? 2 * i + 1 : VEC + i;
-                        const float p = y[lo], q = y[hi];
-                        y[lo] = p * cs[i].x - q * cs[i].y;
-                        y[hi] = p * cs[i].y + q * cs[i].x;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) x[u][i / VEC].e[i % VEC] = from_f32<T>(y[i]);
+                    for (int i = 0; i < 2 * VEC; ++i) y[i] = y[i] * inv * wk[i];
                 }
-                TS* p = target(h);
-                if (in0) *reinterpret_cast<u32x4*>(p + e0) = x[u][0].v;
-                if (in1) *reinterpret_cast<u32x4*>(p + e1) = x[u][1].v;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int lo = NEIGHBOURS ? 2 * i : i, hi = NEIGHBOURS ? 2 * i + 1 : VEC + i;
+                    const float u = y[lo], w = y[hi];
+                    y[lo] = u * cs[i].x - w * cs[i].y;
+                    y[hi] = u * cs[i].y + w * cs[i].x;
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * VEC; ++i) now.x[i / VEC].e[i % VEC] = from_f32<T>(y[i]);
+            }
+            const HeadRows& d = is_q ? a.q_out : is_v ? a.v_out : a.k_out;
+            TS* dst = static_cast<TS*>(d.p) + (is_q ? t : row) * d.row + h * d.head;
+            if (h < (is_q ? a.H : a.HK)) {
+                if (in0) *reinterpret_cast<u32x4*>(dst + e0) = now.x[0].v;
+                if (in1) *reinterpret_cast<u32x4*>(dst + e1) = now.x[1].v;
             }
         }
     }
@@ -187,23 +194,14 @@ __global__ __launch_bounds__(NT) void rope_kernel(RopeLaunch a, int tpb, int log
     using TS = typename T::storage;
     constexpr int VEC = 16 / sizeof(TS);
     __shared__ float2 turn[MAX_TPB * MAX_HALF];
-    __shared__ int seq[MAX_TPB];
+    __shared__ Token tok[MAX_TPB];
     const int t0 = blockIdx.x * tpb, nt = min(tpb, a.N - t0), half = a.rot / 2;
-    int b0;
-    const bool malformed = rope_malformed(a, t0, b0);
+    const bool malformed = rope_malformed(a, t0, t0 + nt, tok);
     report_status(a.dev_status, malformed);
     if (malformed || nt <= 0) return;
-    if (threadIdx.x < nt) {
-        int b = b0;
-        while (b + 1 < a.B && a.offsets[b + 1] <= t0 + (int)threadIdx.x) ++b;
-        seq[threadIdx.x] = b;
-    }
-    __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += NT) {
-        const int tk = i / half, j = i - tk * half, b = seq[tk];
-        const int* first = a.positions != nullptr ? a.positions : a.past;
-        const long long pos = (long long)(first != nullptr ? first[b] : 0) + (t0 + tk - a.offsets[b]);
-        turn[i] = turn_of(pos, a.inv_freq[j]);
+        const int tk = i / half;
+        turn[i] = turn_of(tok[tk].pos, a.inv_freq[i - tk * half]);
     }
     __syncthreads();
 
@@ -213,13 +211,11 @@ __global__ __launch_bounds__(NT) void rope_kernel(RopeLaunch a, int tpb, int log
     const int rows = nt * heads, step = NT >> log2_lanes;
     // every lane of a group stays in the loop for the group sum
     for (int r = threadIdx.x >> log2_lanes; r < rows; r += step) {
-        const int tk = r / heads, h = r - tk * heads, t = t0 + tk, b = seq[tk];
+        const int tk = r / heads, h = r - tk * heads, t = t0 + tk;
         const bool is_q = h < a.H, is_v = h >= a.H + a.HK;
         const int hh = is_q ? h : is_v ? h - a.H - a.HK : h - a.H;
         const HeadRows &src = is_q ? a.q : is_v ? a.v : a.k, &dst = is_q ? a.q_out : is_v ? a.v_out : a.k_out;
-        long long row = t;
-        if (!is_q && a.kv_begin != nullptr)
-            row = a.kv_begin[b] + (a.past != nullptr ? a.past[b] : 0) + (t - a.offsets[b]);
+        const long long row = is_q ? t : tok[tk].row;
         const TS* x = static_cast<const TS*>(src.p) + t * src.row + hh * src.head;
         TS* y = static_cast<TS*>(dst.p) + row * dst.row + hh * dst.head;
         union Chunk {
@@ -273,7 +269,7 @@ hipError_t launch(const RopeLaunch& a, hipStream_t stream) {
         return hipGetLastError();
     }
     // a block's four waves share a token while that still leaves idle CUs, else take four tokens each
-    const int wpt = a.N <= 1024 ? 4 : 1, tpb = a.N <= 1024 ? 1 : a.N <= 8192 ? 4 : 16;
+    const int wpt = a.N <= 1024 ? 4 : 1, tpb = a.N <= 1024 ? 1 : a.N <= 16384 ? 4 : 8;
     const int blocks = a.N > 0 ? (a.N + tpb - 1) / tpb : 1;
     auto go = [&](auto kernel) {
         kernel<<<blocks, NT, 0, stream>>>(a, tpb, wpt);
