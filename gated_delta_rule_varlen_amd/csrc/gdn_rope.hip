@@ -268,8 +268,11 @@ hipError_t launch(const RopeLaunch& a, hipStream_t stream) {
         rope_kernel<T><<<blocks, NT, 0, stream>>>(a, tpb, log2_pieces);
         return hipGetLastError();
     }
-    // a block's four waves share a token while that still leaves idle CUs, else take four tokens each
-    const int wpt = a.N <= 1024 ? 4 : 1, tpb = a.N <= 1024 ? 1 : a.N <= 16384 ? 4 : 8;
+    // A block's four waves share a token while that leaves CUs idle.  Else a wave takes tokens of its own: as many
+    // as let all blocks run at once (10277 tokens, D = 64: 23 us at three, 28 at one), and where there are too
+    // many for that, one, which evens out the last round (24748 tokens, D = 128: 130 us at one, 141 at three).
+    const bool few = a.N <= 1024;
+    const int wpt = few ? 4 : 1, tpb = few ? 1 : a.N <= 12288 ? 4 * ((a.N + 4095) / 4096) : 4;
     const int blocks = a.N > 0 ? (a.N + tpb - 1) / tpb : 1;
     auto go = [&](auto kernel) {
         kernel<<<blocks, NT, 0, stream>>>(a, tpb, wpt);
