@@ -13,8 +13,9 @@
 // order (a contraction may run in any order).
 //
 // Keys and values reach LDS by 16-byte asynchronous loads that write it directly, NS stages deep, with
-// the 16-byte pieces of row r stored at place piece ^ (r % 8), which spreads a column read (K) and a
-// transposing read (V) over the banks.  The buffer's range check returns zeros for rows past the
+// the 16-byte pieces of a row stored at place piece ^ f(row): an LDS read serves 16 rows of one piece (K) or 4
+// to 8 rows of neighbouring pieces (V) at a time, and f differs between those (without it, two thirds of the
+// LDS cycles were conflicts).  The buffer's range check returns zeros for rows past the
 // sequence's keys and pieces past D, so nothing outside a run is read, and nothing unwritten is used.
 //
 // Softmax in base 2: p = 2^(s*c - ref), c = scale*log2(e).  ref follows the running maximum only when
@@ -264,9 +265,15 @@ struct Cfg {
     static constexpr int LW = POW * 1024 <= TILE ? POW : TILE / 1024;  // waves that load
     static constexpr int JN = TILE / (LW * 1024);  // loads such a wave issues for one of K, V
     static constexpr int RPI = LW * 64 / CPR;      // rows one load of all of them covers
-    static constexpr int PRE = RPI >= 8 ? 1 : 8 / RPI;
+    static constexpr int PRE = RPI >= 16 ? 1 : 16 / RPI;  // after which the places of a row's pieces repeat
     static constexpr int LDS = NS * STAGE;
     static_assert(CPR >= 8 && TILE % (LW * 1024) == 0 && RPI >= 1 && LDS <= 160 * 1024 && JN % PRE == 0, "tile");
+    // Where the pieces of row r are stored: at place piece ^ this.  16 places are the 256 bytes the banks span.
+    static __device__ __forceinline__ int place_k(int r) { return RB == 128 ? (r >> 1) & 7 : r & 15; }
+    static __device__ __forceinline__ int place_v(int r) {
+        const int b0 = r & 1, b1 = (r >> 1) & 1, b2 = (r >> 2) & 1;
+        return RB == 128 ? b1 << 2 | b2 << 1 : b1 << 3 | b0 << 2 | b2 << 1;
+    }
     // P of fp16 is kept 2^4 larger, away from the subnormals; with the 2^8 of lag it stays below 2^13
     static constexpr float BIAS = T::code == GDN_F16 ? 4.0f : 0.0f, LAG = 8.0f;
 };
@@ -317,10 +324,10 @@ struct Block {
         vstride = (int)(vrow * C::ES);
 #pragma unroll
         for (int j = 0; j < C::PRE; ++j) {
-            const int p = (j * C::LW + wave) * 64 + lane, row = p / C::CPR, piece = (p % C::CPR) ^ (row & 7);
-            const bool in = piece * 16 < a.c.D * C::ES;
-            koff[j] = in ? row * kstride + piece * 16 : kOutside;
-            voff[j] = in ? row * vstride + piece * 16 : kOutside;
+            const int p = (j * C::LW + wave) * 64 + lane, row = p / C::CPR, place = p % C::CPR;
+            const int kp = (place ^ C::place_k(row)) * 16, vp = (place ^ C::place_v(row)) * 16;
+            koff[j] = kp < row_bytes ? row * kstride + kp : kOutside;
+            voff[j] = vp < row_bytes ? row * vstride + vp : kOutside;
         }
     }
 
@@ -378,7 +385,7 @@ struct Block {
         const Range rq(p, bytes);
         const int padded = (rows + 7) & ~7;
         for (int x = wave * 64; x < padded * C::CPR; x += C::LW * 64) {
-            const int r = (x + lane) / C::CPR, piece = ((x + lane) % C::CPR) ^ (r & 7), i = r / G, g = r - i * G;
+            const int r = (x + lane) / C::CPR, piece = ((x + lane) % C::CPR) ^ C::place_k(r), i = r / G, g = r - i * G;
             const int off = r < rows && piece * 16 < a.c.D * C::ES
                                 ? (int)((i * a.c.q.row + g * a.c.q.head) * C::ES) + piece * 16 : kOutside;
             load_to_lds(rq, lds_base + at + x * 16, off, 0);
@@ -391,7 +398,7 @@ struct Block {
         const char* p = at + have * C::RB;
 #pragma unroll
         for (int s = 0; s < C::CS; ++s)
-            q[s] = (*reinterpret_cast<const u32x4*>(p + (((C::NG * s + grp) ^ (have & 7)) * 16)) ^ flip) & keep;
+            q[s] = (*reinterpret_cast<const u32x4*>(p + (((C::NG * s + grp) ^ C::place_k(have)) * 16)) ^ flip) & keep;
         clear();
     }
 
@@ -428,7 +435,7 @@ struct Block {
 #pragma unroll
                     for (int u = 0; u < C::SUB; ++u)
                         f[x][u] = *reinterpret_cast<const u32x4*>(kt_ + (k * 32 + u * M) * C::RB +
-                                                                  (((C::NG * (x0 + x) + grp) ^ (lane & 7)) * 16));
+                                                                  (((C::NG * (x0 + x) + grp) ^ C::place_k(col)) * 16));
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int x = 0; x < KG; ++x)
@@ -493,7 +500,7 @@ struct Block {
     __device__ __forceinline__ void product(const char* vt, const float (&s)[KT][SN]) {
         if constexpr (C::HALF) {
             // lane x of 16 names key x/4 of its four and elements 4(x%4) .. of a 16-wide part of the head
-            const int x = lane & 15, part = M == 32 ? (lane >> 4) & 1 : 0, key = 4 * grp + (x >> 2), sw = key & 7;
+            const int x = lane & 15, part = M == 32 ? (lane >> 4) & 1 : 0, key = 4 * grp + (x >> 2), sw = C::place_v(key);
             const char* vp = vt + key * C::RB + (x & 1) * 8;
 #pragma unroll
             for (int k = 0; k < KT; ++k)
@@ -521,7 +528,7 @@ struct Block {
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int i = 0; i < SN; ++i) {
-                    const int key = 4 * grp + i % 4, sw = key & 7;
+                    const int key = 4 * grp + i % 4, sw = C::place_v(key);
                     const char* row = vt + (32 * k + 4 * C::NG * (i / 4) + key) * C::RB + (col & 3) * 4;
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
