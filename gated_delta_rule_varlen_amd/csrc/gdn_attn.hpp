@@ -27,6 +27,7 @@
 
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "gdn_device.hpp"
 #include "gdn_launch.hpp"
@@ -260,19 +261,31 @@ struct Cfg {
     static constexpr int CPR = RB / 16;           // 16-byte pieces of a row
     static constexpr int CS = RB / (16 * NG);     // operand steps of a score tile
     static constexpr int DT = DP / M;             // M-wide parts of the head
-    static constexpr int TILE = BN * RB, STAGE = 2 * TILE;
+    static constexpr int TILE = BN * RB;
+    // Rows in LDS: 1024 bytes after 1024 bytes as they are loaded, those of the widest half-precision rows of the
+    // long form PAD apart: with that the places of a row's pieces depend on one bit of its index only, and the reads
+    // of a tile are a register or two and a constant each, where eight registers were spilled.
+    static constexpr bool PADDED = M == 32 && RB == 512 && HALF;
+    static constexpr int KB = TILE / 1024, KSTEP = 1024 + (PADDED ? 32 : 0), VSTEP = 1024 + (PADDED ? 128 : 0);
+    static constexpr int KTILE = KB * KSTEP, STAGE = KTILE + KB * VSTEP;
+    template <int STEP>
+    static __device__ __forceinline__ constexpr int row_at(int r) {
+        return STEP == 1024 ? r * RB : r / (1024 / RB) * STEP + r % (1024 / RB) * RB;
+    }
     static constexpr int POW = NW >= 8 ? 8 : NW >= 4 ? 4 : NW >= 2 ? 2 : 1;
     static constexpr int LW = POW * 1024 <= TILE ? POW : TILE / 1024;  // waves that load
     static constexpr int JN = TILE / (LW * 1024);  // loads such a wave issues for one of K, V
     static constexpr int RPI = LW * 64 / CPR;      // rows one load of all of them covers
     static constexpr int PRE = RPI >= 16 ? 1 : 16 / RPI;  // after which the places of a row's pieces repeat
-    static constexpr int LDS = NS * STAGE;
-    static_assert(CPR >= 8 && TILE % (LW * 1024) == 0 && RPI >= 1 && LDS <= 160 * 1024 && JN % PRE == 0, "tile");
+    static constexpr int QL = PADDED ? 2 : 0;  // operand steps of the queries that lie in LDS, behind the ring
+    static constexpr int RING = NS * STAGE, LDS = RING + QL * NW * 1024;
+    static constexpr bool PIPE = RB <= 256;       // the registers hold two tiles' scores (long form)
+    static_assert(CPR >= 8 && TILE % (LW * 1024) == 0 && RPI >= 1 && LDS <= 159 * 1024 && JN % PRE == 0, "tile");
     // Where the pieces of row r are stored: at place piece ^ this.  16 places are the 256 bytes the banks span.
-    static __device__ __forceinline__ int place_k(int r) { return RB == 128 ? (r >> 1) & 7 : r & 15; }
+    static __device__ __forceinline__ int place_k(int r) { return PADDED ? r & 1 : RB == 128 ? (r >> 1) & 7 : r & 15; }
     static __device__ __forceinline__ int place_v(int r) {
         const int b0 = r & 1, b1 = (r >> 1) & 1, b2 = (r >> 2) & 1;
-        return RB == 128 ? b1 << 2 | b2 << 1 : b1 << 3 | b0 << 2 | b2 << 1;
+        return PADDED ? b0 << 2 : RB == 128 ? b1 << 2 | b2 << 1 : b1 << 3 | b0 << 2 | b2 << 1;
     }
     // P of fp16 is kept 2^4 larger, away from the subnormals; with the 2^8 of lag it stays below 2^13
     static constexpr float BIAS = T::code == GDN_F16 ? 4.0f : 0.0f, LAG = 8.0f;
@@ -299,7 +312,7 @@ struct Block {
     float c;                                // scores to base 2
     int kstride, vstride;                   // bytes between rows of this source
     int koff[C::PRE], voff[C::PRE];
-    u32x4 q[C::CS];
+    u32x4 q[C::CS - C::QL];
     int vis;                                // keys the lane's row sees
     int vis_lo, vis_hi;                     // over the wave's rows
     int run_n;                              // keys of the run
@@ -315,7 +328,7 @@ struct Block {
         lds_base = uniform((int)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
         row_bytes = a.c.D * C::ES;
         c = a.s2;
-        asm volatile("" : "+v"(c));  // a register: not read again for every tile
+        asm volatile("" : "+s"(c));  // a register: not read again for every tile
     }
 
     // byte offsets of the 16-byte pieces this lane loads, for rows `ks` and `vs` bytes apart
@@ -331,19 +344,20 @@ struct Block {
         }
     }
 
-    __device__ __forceinline__ void load_tile(const Keys& s, int tile, bool real, int stage) {
+    template <bool V>
+    __device__ __forceinline__ void load_half(const Keys& s, int tile, bool real, int stage) {
         if (C::LW < C::NW && wave >= C::LW) return;
-        const int k0 = tile * C::BN, left = s.n - k0, rows = left < C::BN ? left : C::BN, last = rows - 1;
-        const bool any = real && rows > 0;
-        const Range rk(s.k + (long long)k0 * kstride, any ? last * kstride + row_bytes : 0);
-        const Range rv(s.v + (long long)k0 * vstride, any ? last * vstride + row_bytes : 0);
-        const uint32_t to = lds_base + stage * C::STAGE + wave * 1024;
+        const int k0 = tile * C::BN, left = s.n - k0, rows = left < C::BN ? left : C::BN, stride = V ? vstride : kstride;
+        const Range r((V ? s.v : s.k) + (long long)k0 * stride, real && rows > 0 ? (rows - 1) * stride + row_bytes : 0);
+        constexpr int STEP = V ? C::VSTEP : C::KSTEP;
+        const uint32_t to = lds_base + stage * C::STAGE + (V ? C::KTILE : 0) + wave * STEP;
 #pragma unroll
         for (int j = 0; j < C::JN; ++j)
-            load_to_lds(rk, to + j * C::LW * 1024, koff[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * kstride);
-#pragma unroll
-        for (int j = 0; j < C::JN; ++j)
-            load_to_lds(rv, to + C::TILE + j * C::LW * 1024, voff[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * vstride);
+            load_to_lds(r, to + j * C::LW * STEP, (V ? voff : koff)[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * stride);
+    }
+    __device__ __forceinline__ void load_tile(const Keys& s, int tile, bool real, int stage) {
+        load_half<false>(s, tile, real, stage);
+        load_half<true>(s, tile, real, stage);
     }
 
     // Queries of the block's rows row0 .. (of `rows` in the list); rows past the list are zeros.
@@ -354,15 +368,18 @@ struct Block {
         const TS* p = static_cast<const TS*>(a.c.q.p) + (first + (in ? i : 0)) * a.c.q.row +
                       (long long)(hk * G + (in ? g : 0)) * a.c.q.head;
         const uint32_t flip = !a.negate ? 0u : C::HALF ? 0x80008000u : 0x80000000u;
+        u32x4 x[C::CS];
 #pragma unroll
         for (int s = 0; s < C::CS; ++s) {
             const int e = (C::NG * s + grp) * (16 / C::ES);
-            q[s] = *reinterpret_cast<const u32x4*>(p + (e < a.c.D ? e : 0));
+            x[s] = *reinterpret_cast<const u32x4*>(p + (e < a.c.D ? e : 0));
         }
 #pragma unroll
         for (int s = 0; s < C::CS; ++s) {
             const uint32_t keep = in && (C::NG * s + grp) * (16 / C::ES) < a.c.D ? ~0u : 0u;
-            q[s] = (q[s] ^ flip) & keep;
+            x[s] = (x[s] ^ flip) & keep;
+            if (s < C::CS - C::QL) q[s] = x[s];
+            else *query_at(s) = x[s];
         }
         clear();
     }
@@ -373,6 +390,11 @@ struct Block {
         l = 0.0f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] = Acc<M>{};
+    }
+
+    // Where this lane keeps operand step s of its queries in LDS, for the last QL of them.
+    __device__ __forceinline__ u32x4* query_at(int s) {
+        return reinterpret_cast<u32x4*>(lds + C::RING + (wave * C::QL + s - (C::CS - C::QL)) * 1024 + lane * 16);
     }
 
     // The short form takes queries through LDS, as rows at `at` laid out like the keys': asked for with the run's
@@ -397,7 +419,7 @@ struct Block {
         const uint32_t keep = r < rows ? ~0u : 0u;  // rows past the list were not loaded
         const char* p = at + have * C::RB;
 #pragma unroll
-        for (int s = 0; s < C::CS; ++s)
+        for (int s = 0; s < C::CS - C::QL; ++s)
             q[s] = (*reinterpret_cast<const u32x4*>(p + (((C::NG * s + grp) ^ C::place_k(have)) * 16)) ^ flip) & keep;
         clear();
     }
@@ -412,13 +434,13 @@ struct Block {
         vis_hi = uniform(lo < rows ? keys(hi) : 0);
     }
 
-    // A stage's keys and values against the wave's rows; base = index of its first key in the run.  Element i of a
-    // lane's scores of 32 keys is key 4 NG (i / 4) + 4 grp + i % 4.
-    __device__ __forceinline__ void use_tile(int stage, int base) {
-        if (base >= vis_hi) return;
-        constexpr int SN = C::SUB * C::EA;  // scores of 32 keys a lane
-        const char* kt_ = lds + stage * C::STAGE + col * C::RB;
-        Acc<M> acc[KT][C::SUB];
+    static constexpr int SN = C::SUB * C::EA;  // scores of 32 keys a lane
+    using Scores = Acc<M>[KT][C::SUB];
+
+    // Scores of a stage's keys: element i of a lane's scores of 32 keys is key 4 NG (i / 4) + 4 grp + i % 4.
+    template <bool GROUPED>
+    __device__ __forceinline__ void scores(int stage, Scores& acc) {
+        const char* kt_ = lds + stage * C::STAGE + C::template row_at<C::KSTEP>(col);
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
@@ -434,33 +456,36 @@ struct Block {
                 for (int x = 0; x < KG; ++x)
 #pragma unroll
                     for (int u = 0; u < C::SUB; ++u)
-                        f[x][u] = *reinterpret_cast<const u32x4*>(kt_ + (k * 32 + u * M) * C::RB +
+                        f[x][u] = *reinterpret_cast<const u32x4*>(kt_ + C::template row_at<C::KSTEP>(k * 32 + u * M) +
                                                                   (((C::NG * (x0 + x) + grp) ^ C::place_k(col)) * 16));
-                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (GROUPED) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int x = 0; x < KG; ++x)
+                for (int x = 0; x < KG; ++x) {
+                    const u32x4 y = x0 + x < C::CS - C::QL ? q[x0 + x] : *query_at(x0 + x);
 #pragma unroll
-                    for (int u = 0; u < C::SUB; ++u) multiply<T, M>(f[x][u], q[x0 + x], acc[k][u]);
+                    for (int u = 0; u < C::SUB; ++u) multiply<T, M>(f[x][u], y, acc[k][u]);
+                }
             }
-        float s[KT][SN];
+    }
+    // Hides the keys a row does not see; base = index of the tile's first key in the run.
+    __device__ __forceinline__ void hide(Scores& s, int base) {
+        const int room = vis - base - 4 * grp;
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
-            for (int i = 0; i < SN; ++i) s[k][i] = acc[k][i / C::EA][i % C::EA];
-        if (base + C::BN > vis_lo) {
-            const int room = vis - base - 4 * grp;
-#pragma unroll
-            for (int k = 0; k < KT; ++k)
-#pragma unroll
-                for (int i = 0; i < SN; ++i)
-                    if (32 * k + 4 * C::NG * (i / 4) + i % 4 >= room) s[k][i] = -INFINITY;
-        }
-        float top = s[0][0];
+            for (int i = 0; i < SN; ++i)
+                s[k][i / C::EA][i % C::EA] = 32 * k + 4 * C::NG * (i / 4) + i % 4 >= room ? -INFINITY : s[k][i / C::EA][i % C::EA];
+    }
+    // The largest score of each row, to base 2.
+    __device__ __forceinline__ float largest(const Scores& s) {
+        float top = s[0][0][0];
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
-            for (int i = 0; i < SN; ++i) top = fmaxf(top, s[k][i]);
-        top = over_row<M, true>(top) * c;
+            for (int i = 0; i < SN; ++i) top = fmaxf(top, s[k][i / C::EA][i % C::EA]);
+        return over_row<M, true>(top) * c;
+    }
+    __device__ __forceinline__ void follow(float top) {
         if (__builtin_amdgcn_ballot_w64(top > ref + (C::BIAS + C::LAG)) != 0) {
             const float to = fmaxf(ref, top - C::BIAS), w = __builtin_amdgcn_exp2f(ref - to);
             ref = to;
@@ -468,27 +493,46 @@ struct Block {
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= w;
         }
+    }
+    __device__ __forceinline__ void exponentials(Scores& s) {
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int i = 0; i < SN; ++i) {
-                s[k][i] = __builtin_amdgcn_exp2f(fmaf(s[k][i], c, -ref));
-                sum += s[k][i];
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[k][i / C::EA][i % C::EA], c, -ref));
+                s[k][i / C::EA][i % C::EA] = p;
+                sum += p;
             }
         l += sum;
-        const char* vt = lds + stage * C::STAGE + C::TILE;
-        // 0 * infinity is NaN: where rows differ in what they see, a value that is not finite would reach the
-        // rows that must not see it.  Such a tile is found here and the wave's rows are done again by redo().
+    }
+    // 0 * infinity is NaN: where rows differ in what they see, a value that is not finite would reach the
+    // rows that must not see it.  Such a tile is found here and the wave's rows are done again by redo().
+    __device__ __forceinline__ void look(const char* vt, int base) {
         if (vis_lo < min(base + C::BN, run_n)) spoiled |= any_not_finite(vt);
+    }
+
+    // A stage's keys and values against the wave's rows.
+    __device__ __forceinline__ void use_tile(int stage, int base) {
+        if (base >= vis_hi) return;
+        Scores s;
+        scores<true>(stage, s);
+        if (base + C::BN > vis_lo) {
+            hide(s, base);
+            asm volatile("");  // keeps this a branch: most tiles hide nothing
+        }
+        follow(largest(s));
+        exponentials(s);
+        const char* vt = lds + stage * C::STAGE + C::KTILE;
+        look(vt, base);
         product(vt, s);
     }
 
     __device__ __forceinline__ bool any_not_finite(const char* vt) {
         uint32_t acc = 0;
 #pragma unroll 1
-        for (int at = lane * 16; at < C::BN * C::RB; at += 1024) {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(vt + at);
+        for (int i = 0; i < C::KB; ++i) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(vt + i * C::VSTEP + lane * 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc |= not_finite_sign<T>(x[j]);
         }
@@ -496,30 +540,32 @@ struct Block {
     }
 
     // O^T += V^T P^T for the tile at vt.
-    template <int SN>
-    __device__ __forceinline__ void product(const char* vt, const float (&s)[KT][SN]) {
+    __device__ __forceinline__ void product(const char* vt, const Scores& s) {
         if constexpr (C::HALF) {
             // lane x of 16 names key x/4 of its four and elements 4(x%4) .. of a 16-wide part of the head
             const int x = lane & 15, part = M == 32 ? (lane >> 4) & 1 : 0, key = 4 * grp + (x >> 2), sw = C::place_v(key);
-            const char* vp = vt + key * C::RB + (x & 1) * 8;
+            const char* vp = vt + C::template row_at<C::VSTEP>(key) + (x & 1) * 8;
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int z = 0; z < SN / 8; ++z) {  // eight scores a lane are one step: 8 NG keys
                     u32x4 p;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = pack<T>(s[k][8 * z + 2 * e], s[k][8 * z + 2 * e + 1]);
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = 8 * z + 2 * e;
+                        p[e] = pack<T>(s[k][i / C::EA][i % C::EA], s[k][(i + 1) / C::EA][(i + 1) % C::EA]);
+                    }
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
                         const int piece = M / 8 * d + 2 * part + ((x >> 1) & 1);
-                        const char* at = vp + (32 * k + 8 * C::NG * z) * C::RB + ((piece ^ sw) * 16);
+                        const char* at = vp + C::template row_at<C::VSTEP>(32 * k + 8 * C::NG * z) + ((piece ^ sw) * 16);
                         union {
                             v4i16 h[2];
                             u32x4 v;
                         } f;
                         f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(at));
                         f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) v4i16*)(at + 4 * C::NG * C::RB));
+                            (__attribute__((address_space(3))) v4i16*)(at + C::template row_at<C::VSTEP>(4 * C::NG)));
                         multiply<T, M>(f.v, p, o[d]);
                     }
                 }
@@ -532,27 +578,130 @@ struct Block {
                     const char* row = vt + (32 * k + 4 * C::NG * (i / 4) + key) * C::RB + (col & 3) * 4;
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
-                        multiply1<M>(*reinterpret_cast<const float*>(row + (((M / 4 * d + (col >> 2)) ^ sw) * 16)), s[k][i], o[d]);
+                        multiply1<M>(*reinterpret_cast<const float*>(row + (((M / 4 * d + (col >> 2)) ^ sw) * 16)), s[k][i / C::EA][i % C::EA], o[d]);
                 }
         }
     }
 
     // LDS addresses are worth registers inside a loop over tiles, not across a block's runs.
-    __device__ __forceinline__ void fresh_addresses() { asm volatile("" : "+v"(lane), "+v"(col), "+v"(grp)); }
+    __device__ __forceinline__ void fresh_addresses() {
+        asm volatile("" : "+v"(lane));
+        col = lane & (M - 1);
+        grp = lane / M;
+    }
 
-    // Tiles [t0, t1) of the run.  Loads run NS - 1 tiles ahead; the ones past the end are asked for with an
-    // empty range, so the count of loads on their way is the same at every wait.
-    __device__ __forceinline__ void run(const Keys& s, int t0, int t1) {
+    // One tile of the long form's pipeline.  While the matrix cores form the next tile's scores, the vector unit
+    // takes this one's exponentials, and while they multiply those with the values, the next tile's maximum: a
+    // wave has work for both at any time.  HIDE: the next tile has keys that some rows must not see.
+    template <bool HIDE, bool LAST>
+    __device__ __forceinline__ void step(int stage, int t, Scores& cur, Scores& next, float& top) {
+        follow(top);
+        const char* vt = lds + stage * C::STAGE + C::KTILE;
+        if constexpr (!LAST) scores<false>(stage ^ 1, next);
+        exponentials(cur);
+        product(vt, cur);
+        if constexpr (!LAST) {
+            if constexpr (HIDE) hide(next, (t + 1) * C::BN);
+            top = largest(next);
+            order<QK, KREADS, KREADS + AHEAD_V, PV, VREADS, 5 * KT * SN / 2, KT * SN, KT * SN>();
+        }
+    }
+    // The same where the registers do not hold two tiles' scores: one tile after the other, and the other wave
+    // of the SIMD fills the matrix cores meanwhile.
+    template <bool HIDE>
+    __device__ __forceinline__ void plain_step(int stage, int t, Scores& cur) {
+        scores<false>(stage, cur);
+        if constexpr (HIDE) hide(cur, t * C::BN);
+        const float top = largest(cur);
+        order<QK, KREADS, KREADS, 0, 0, 0, 0, 0>();
+        follow(top);
+        exponentials(cur);
+        product(lds + stage * C::STAGE + C::KTILE, cur);
+        order<0, 0, 0, PV, VREADS, 0, 0, 5 * KT * SN / 2>();
+    }
+    static constexpr int QK = KT * C::SUB * C::CS * (C::HALF ? 1 : 4), PV = KT * DT * (C::HALF ? SN / 8 : SN);  // matrix instructions
+    static constexpr int KREADS = KT * (C::SUB * C::CS + C::QL), VREADS = KT * DT * (C::HALF ? SN / 4 : SN);           // LDS reads
+    static constexpr int AHEAD_V = C::PIPE ? (C::HALF ? 8 : 4) : 4;  // reads of values before the products with them begin
+    // The order of a step's instructions: reads run ahead of the products that use them, and vector work stands
+    // between the products.  M1, M2: products of either kind, with D1, D2 reads (E1 of them during the first kind) and
+    // V1, X1 vector instructions and exponentials during the first kind, V2 vector ones during the second.
+    template <int M1, int D1, int E1, int M2, int D2, int V1, int X1, int V2>
+    static __device__ __forceinline__ void order() {
+        constexpr int AHEAD = 4, FIRST = M1 > 0 ? AHEAD : AHEAD_V;
+        __builtin_amdgcn_sched_group_barrier(0x100, FIRST, 0);
+        if constexpr (M1 > 0) spread<M1, 0, E1 - FIRST, (E1 - FIRST + M1 - 1) / M1, V1, X1>();
+        if constexpr (M2 > 0) spread<M2, 0, D1 + D2 - (M1 > 0 ? E1 : FIRST), (D2 + M2 - 1) / M2, V2, 0>();
+    }
+    // Products I .. M - 1, with `RATE` of the D reads each while there are any, and their even share of V vector
+    // instructions and X exponentials.
+    template <int M_, int I, int D, int RATE, int V, int X>
+    static __device__ __forceinline__ void spread() {
+        if constexpr (I < M_) {
+            constexpr int done = I * RATE < D ? I * RATE : D, d = D - done < RATE ? D - done : RATE, v = V * (I + 1) / M_ - V * I / M_, x = X * (I + 1) / M_ - X * I / M_;
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
+            if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
+            if constexpr (x > 0) __builtin_amdgcn_sched_group_barrier(0x400, x, 0);
+            spread<M_, I + 1, D, RATE, V, X>();
+        }
+    }
+
+    // Tiles [t0, t1) of the run; those before `full` are seen whole by all rows of the block.  Values run a tile
+    // ahead, keys two; the loads past the end are asked for with an empty range.
+    __device__ __forceinline__ void run(const Keys& s, int t0, int t1, int full) {
         fresh_addresses();
+        int stage = 0, t = t0;
+        if constexpr (!C::PIPE) {
+            Scores cur;
+            load_tile(s, t0, true, 0);
+            auto one = [&](auto hidden, int at) {
+                wait_and_meet<0>();
+                load_tile(s, t + 1, t + 1 < t1, at ^ 1);
+                if (hidden.value) look(lds + at * C::STAGE + C::KTILE, t * C::BN);
+                plain_step<hidden.value>(at, t, cur);
+                ++t;
+            };
+            while (t + 1 < min(full, t1)) {
+                one(std::false_type{}, 0);
+                one(std::false_type{}, 1);
+            }
+            for (; t < t1; stage ^= 1) one(std::true_type{}, stage);
+        } else {
+            Scores now, next;
+            float top;
+            load_half<false>(s, t0, true, 0);
+            load_half<true>(s, t0, true, 0);
+            load_half<false>(s, t0 + 1, t0 + 1 < t1, 1);
+            wait_and_meet<2 * C::JN>();
+            scores<true>(0, now);
+            if (t0 >= full) hide(now, t0 * C::BN);
+            top = largest(now);
+            auto ahead = [&](int at) {
+                wait_and_meet<0>();
+                load_half<true>(s, t + 1, t + 1 < t1, at ^ 1);
+                load_half<false>(s, t + 2, t + 2 < t1, at);
+            };
+            while (t + 2 < min(full, t1 - 1)) {
+                ahead(0);
+                step<false, false>(0, t, now, next, top);
+                ++t;
+                ahead(1);
+                step<false, false>(1, t, next, now, top);
+                ++t;
+            }
+            for (; t < t1 - 1; ++t) {
+                ahead(stage);
+                if (t >= full) look(lds + stage * C::STAGE + C::KTILE, t * C::BN);
+                step<true, false>(stage, t, now, next, top);
 #pragma unroll
-        for (int i = 0; i < C::NS - 1; ++i) load_tile(s, t0 + i, t0 + i < t1, i);
-        int stage = 0;
-        for (int t = t0; t < t1; ++t) {
-            wait_and_meet<(C::NS - 2) * 2 * C::JN>();
-            const int next = stage == 0 ? C::NS - 1 : stage - 1;
-            load_tile(s, t + C::NS - 1, t + C::NS - 1 < t1, next);
-            use_tile(stage, t * C::BN);
-            stage = stage == C::NS - 1 ? 0 : stage + 1;
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int u = 0; u < C::SUB; ++u) now[k][u] = next[k][u];
+                stage ^= 1;
+            }
+            wait_and_meet<0>();
+            if (t >= full) look(lds + stage * C::STAGE + C::KTILE, t * C::BN);
+            step<false, true>(stage, t, now, next, top);
         }
         wait_and_meet<0>();
     }
@@ -712,9 +861,9 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
     }
     const int seen0 = n - T + 1;
     const int last_token = min(row0 + C::BM, rows) - 1;
-    const int reach = max(0, min(n, seen0 + last_token / a.G));  // keys the last row sees
+    const int reach = uniform(max(0, min(n, seen0 + last_token / a.G)));  // keys the last row sees
     const int ptiles = (a.c.prefix_len + C::BN - 1) / C::BN, all = ptiles + (reach + C::BN - 1) / C::BN;
-    const int t0 = (int)((long long)all * part / a.splits), t1 = (int)((long long)all * (part + 1) / a.splits);
+    const int t0 = uniform((int)((long long)all * part / a.splits)), t1 = uniform((int)((long long)all * (part + 1) / a.splits));
 
     Block<C> blk(a, lds);
     blk.load_rows(row0, rows, first, hk);
@@ -726,12 +875,12 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
     if (t0 < p1) {
         blk.see(row0, rows, false, 0, a.c.prefix_len);
         blk.set_source(a.c.pk.row, a.c.pv.row);
-        blk.run(prefix, t0, p1);
+        blk.run(prefix, t0, p1, a.c.prefix_len / C::BN);
     }
     if (k0 < k1) {
         blk.see(row0, rows, true, seen0, n);
         blk.set_source(a.c.k.row, a.c.v.row);
-        blk.run(own, k0, k1);
+        blk.run(own, k0, k1, uniform(max(0, min(n, seen0 + row0 / a.G)) / C::BN));
     }
     blk.sum_rows();
     const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? a.set0 + part : -1, -1};
