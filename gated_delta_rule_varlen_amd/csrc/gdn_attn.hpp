@@ -52,6 +52,7 @@ struct Args {
     float s2;       // |scale| * log2(e); the sign goes to the queries
     bool negate;
     int splits;     // key parts of the long form
+    int chunk;      // row tiles of a sequence that follow one another
     int workers;    // blocks of the short form
     bool prefix_rows;  // the long form runs all tokens' rows over the prefix alone
     bool to_sets;   // results go to the workspace, for the joining kernel
@@ -171,7 +172,49 @@ __device__ __forceinline__ void load_to_lds(const Range& s, uint32_t at, int vof
                  ::"s"(at), "v"(voff), "s"(s.r), "s"(soff) : "m0", "memory");
 }
 
-// Whole-call check (offsets, lengths, key runs) with a per-sequence sum: `units(T, n)` of every sequence.
+// Sequence i of the call as its arrays give it, in bounds whatever they hold: what a block asks for before the
+// whole call is checked lies inside the tensors.
+struct Sequence {
+    int first, T, n;
+    long long begin;
+};
+__device__ __forceinline__ Sequence sequence(const AttnLaunch& c, int i) {
+    Sequence s;
+    s.first = min(max(uniform(entry(c.offsets, i)), 0), c.N);
+    s.T = min(max(uniform(entry(c.offsets, i + 1)) - s.first, 0), min(c.max_q, c.N - s.first));
+    if (c.kv_len != nullptr) {
+        const long long n = max(uniform(entry(c.kv_len, i)), 0), begin = uniform((long long)entry(c.kv_begin, i));
+        s.n = (int)min(n, c.kv_rows);
+        s.begin = min(max(begin, 0ll), c.kv_rows - s.n);
+    } else {
+        s.begin = min((long long)s.first, c.kv_rows);
+        s.n = (int)min((long long)s.T, c.kv_rows - s.begin);
+    }
+    return s;
+}
+
+// Whether sequence i is malformed; T and n as the arrays have them.
+__device__ __forceinline__ bool bad_sequence(const AttnLaunch& c, int i, int* T, int* n) {
+    const int o = c.offsets[i], e = c.offsets[i + 1], t = e - o;
+    bool bad = (t < 0) | (t > c.max_q) | (i == 0 && o != 0) | (i == c.B - 1 && e != c.N);
+    *T = *n = t;
+    if (c.kv_len != nullptr) {
+        *n = c.kv_len[i];
+        const long long begin = c.kv_begin[i];
+        bad |= (*n < 0) | (begin < 0) | (begin > c.kv_rows) | (begin + *n > c.kv_rows);
+    } else {
+        bad |= (e > c.kv_rows);
+    }
+    return bad;
+}
+// Whole-call check.  Reached by all threads.
+template <int NT>
+__device__ __forceinline__ bool check(const AttnLaunch& c) {
+    int bad = 0, T, n;
+    for (int i = threadIdx.x; i < c.B; i += NT) bad |= bad_sequence(c, i, &T, &n);
+    return __syncthreads_or(bad) != 0;
+}
+// The same with a per-sequence sum: `units(T, n)` of every sequence.
 // Returns whether the call is malformed; total = the sum over all sequences, and for the sequence that
 // holds unit `want` (want < total) seq = its index and base = the sum before it.  Reached by all threads.
 template <int NT, typename F>
@@ -180,18 +223,9 @@ __device__ __forceinline__ bool check_and_find(const AttnLaunch& c, F units, lon
     int bad = 0;
     long long sum = 0;
     for (int i = threadIdx.x; i < c.B; i += NT) {
-        const int o = c.offsets[i], e = c.offsets[i + 1], t = e - o;
-        bad |= (t < 0) | (t > c.max_q) | (i == 0 && o != 0) | (i == c.B - 1 && e != c.N);
-        long long n;
-        if (c.kv_len != nullptr) {
-            n = c.kv_len[i];
-            const long long begin = c.kv_begin[i];
-            bad |= (n < 0) | (begin < 0) | (begin > c.kv_rows) | (begin + n > c.kv_rows);
-        } else {
-            n = t;
-            bad |= (e > c.kv_rows);
-        }
-        sum += units(t, (int)n);
+        int T, n;
+        bad |= bad_sequence(c, i, &T, &n);
+        sum += units(T, n);
     }
     const bool malformed = __syncthreads_or(bad) != 0;
     for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
@@ -277,7 +311,9 @@ struct Cfg {
     static constexpr int JN = TILE / (LW * 1024);  // loads such a wave issues for one of K, V
     static constexpr int RPI = LW * 64 / CPR;      // rows one load of all of them covers
     static constexpr int PRE = RPI >= 16 ? 1 : 16 / RPI;  // after which the places of a row's pieces repeat
-    static constexpr int QL = PADDED ? 2 : 0;  // operand steps of the queries that lie in LDS, behind the ring
+    // Operand steps of the queries that lie in LDS, behind the ring: at width 256 eight waves' share of the CU's
+    // registers holds six (with ten in LDS a 16384-token prompt takes 1757 us, with seven and spills 2170)
+    static constexpr int QL = PADDED ? 10 : 0;
     static constexpr int RING = NS * STAGE, LDS = RING + QL * NW * 1024;
     static constexpr bool PIPE = RB <= 256;       // the registers hold two tiles' scores (long form)
     static_assert(CPR >= 8 && TILE % (LW * 1024) == 0 && RPI >= 1 && LDS <= 159 * 1024 && JN % PRE == 0, "tile");
@@ -539,35 +575,42 @@ struct Block {
         return __builtin_amdgcn_ballot_w64((acc & (C::HALF ? 0x80008000u : 0x80000000u)) != 0) != 0;
     }
 
+    // Operands of the second product: eight probabilities a lane, and the values of the same keys.
+    static __device__ __forceinline__ u32x4 packed(const Scores& s, int k, int z) {
+        u32x4 p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = 8 * z + 2 * e;
+            p[e] = pack<T>(s[k][i / C::EA][i % C::EA], s[k][(i + 1) / C::EA][(i + 1) % C::EA]);
+        }
+        return p;
+    }
+    __device__ __forceinline__ u32x4 values(const char* vt, int k, int z, int d) {
+        // lane x of 16 names key x/4 of its four and elements 4(x%4) .. of a 16-wide part of the head
+        const int x = lane & 15, part = M == 32 ? (lane >> 4) & 1 : 0, key = 4 * grp + (x >> 2), sw = C::place_v(key);
+        const int piece = M / 8 * d + 2 * part + ((x >> 1) & 1);
+        const char* at = vt + C::template row_at<C::VSTEP>(key) + (x & 1) * 8 +
+                         C::template row_at<C::VSTEP>(32 * k + 8 * C::NG * z) + ((piece ^ sw) * 16);
+        union {
+            v4i16 h[2];
+            u32x4 v;
+        } f;
+        f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(at));
+        f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) v4i16*)(at + C::template row_at<C::VSTEP>(4 * C::NG)));
+        return f.v;
+    }
+
     // O^T += V^T P^T for the tile at vt.
     __device__ __forceinline__ void product(const char* vt, const Scores& s) {
         if constexpr (C::HALF) {
-            // lane x of 16 names key x/4 of its four and elements 4(x%4) .. of a 16-wide part of the head
-            const int x = lane & 15, part = M == 32 ? (lane >> 4) & 1 : 0, key = 4 * grp + (x >> 2), sw = C::place_v(key);
-            const char* vp = vt + C::template row_at<C::VSTEP>(key) + (x & 1) * 8;
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int z = 0; z < SN / 8; ++z) {  // eight scores a lane are one step: 8 NG keys
-                    u32x4 p;
+                    const u32x4 p = packed(s, k, z);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = 8 * z + 2 * e;
-                        p[e] = pack<T>(s[k][i / C::EA][i % C::EA], s[k][(i + 1) / C::EA][(i + 1) % C::EA]);
-                    }
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        const int piece = M / 8 * d + 2 * part + ((x >> 1) & 1);
-                        const char* at = vp + C::template row_at<C::VSTEP>(32 * k + 8 * C::NG * z) + ((piece ^ sw) * 16);
-                        union {
-                            v4i16 h[2];
-                            u32x4 v;
-                        } f;
-                        f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(at));
-                        f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) v4i16*)(at + C::template row_at<C::VSTEP>(4 * C::NG)));
-                        multiply<T, M>(f.v, p, o[d]);
-                    }
+                    for (int d = 0; d < DT; ++d) multiply<T, M>(values(vt, k, z, d), p, o[d]);
                 }
         } else {
 #pragma unroll
@@ -607,21 +650,63 @@ struct Block {
         }
     }
     // The same where the registers do not hold two tiles' scores: one tile after the other, and the other wave
-    // of the SIMD fills the matrix cores meanwhile.
+    // of the SIMD fills the matrix cores meanwhile.  The order is written out, as the compiler's own gives up
+    // the reads ahead when registers are short.
     template <bool HIDE>
     __device__ __forceinline__ void plain_step(int stage, int t, Scores& cur) {
-        scores<false>(stage, cur);
-        if constexpr (HIDE) hide(cur, t * C::BN);
-        const float top = largest(cur);
-        order<QK, KREADS, KREADS, 0, 0, 0, 0, 0>();
-        follow(top);
-        exponentials(cur);
-        product(lds + stage * C::STAGE + C::KTILE, cur);
-        order<0, 0, 0, PV, VREADS, 0, 0, 5 * KT * SN / 2>();
+        const char* vt = lds + stage * C::STAGE + C::KTILE;
+        if constexpr (C::HALF) {
+            static_assert(KT == 1 && C::SUB == 1, "one tile of 32 keys");
+            constexpr int AK = 4, AV = 4, Z = SN / 8;
+            const char* kt_ = lds + stage * C::STAGE + C::template row_at<C::KSTEP>(col);
+            auto key = [&](int x) { return *reinterpret_cast<const u32x4*>(kt_ + (((C::NG * x + grp) ^ C::place_k(col)) * 16)); };
+            auto query = [&](int x) { return x < C::CS - C::QL ? q[x] : *query_at(x); };
+            u32x4 f[C::CS], g[C::CS], v[DT * Z];
+#pragma unroll
+            for (int x = 0; x < AK; ++x) f[x] = key(x), g[x] = query(x);
+            cur[0][0] = Acc<M>{};
+#pragma unroll
+            for (int x = 0; x < C::CS; ++x) {
+                if (x + AK < C::CS) f[x + AK] = key(x + AK), g[x + AK] = query(x + AK);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply<T, M>(f[x], g[x], cur[0][0]);
+            }
+#pragma unroll
+            for (int x = 0; x < AV; ++x) v[x] = values(vt, 0, x / DT, x % DT);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (HIDE) hide(cur, t * C::BN);
+            follow(largest(cur));
+            float sum = 0.0f;
+            auto exponential = [&](int i) {
+                cur[0][0][i] = __builtin_amdgcn_exp2f(fmaf(cur[0][0][i], c, -ref));
+                sum += cur[0][0][i];
+            };
+#pragma unroll
+            for (int i = 0; i < 8; ++i) exponential(i);
+            u32x4 p = packed(cur, 0, 0);
+#pragma unroll
+            for (int x = 0; x < DT * Z; ++x) {
+                if (x + AV < DT * Z) v[x + AV] = values(vt, 0, (x + AV) / DT, (x + AV) % DT);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply<T, M>(v[x], p, o[x % DT]);
+                if (x < 8 * (Z - 1)) exponential(8 + x);
+                if (x % DT == DT - 1 && x + 1 < DT * Z) p = packed(cur, 0, x / DT + 1);
+            }
+            l += sum;
+        } else {
+            scores<false>(stage, cur);
+            if constexpr (HIDE) hide(cur, t * C::BN);
+            const float top = largest(cur);
+            order<QK, KREADS, KREADS, 0, 0, 0, 0, 0>();
+            follow(top);
+            exponentials(cur);
+            product(vt, cur);
+            order<0, 0, 0, PV, VREADS, 0, 0, 5 * KT * SN / 2>();
+        }
     }
     static constexpr int QK = KT * C::SUB * C::CS * (C::HALF ? 1 : 4), PV = KT * DT * (C::HALF ? SN / 8 : SN);  // matrix instructions
     static constexpr int KREADS = KT * (C::SUB * C::CS + C::QL), VREADS = KT * DT * (C::HALF ? SN / 4 : SN);           // LDS reads
-    static constexpr int AHEAD_V = C::PIPE ? (C::HALF ? 8 : 4) : 4;  // reads of values before the products with them begin
+    static constexpr int AHEAD_V = C::HALF ? 8 : 4;  // reads of values before the products with them begin
     // The order of a step's instructions: reads run ahead of the products that use them, and vector work stands
     // between the products.  M1, M2: products of either kind, with D1, D2 reads (E1 of them during the first kind) and
     // V1, X1 vector instructions and exponentials during the first kind, V2 vector ones during the second.
@@ -648,12 +733,15 @@ struct Block {
 
     // Tiles [t0, t1) of the run; those before `full` are seen whole by all rows of the block.  Values run a tile
     // ahead, keys two; the loads past the end are asked for with an empty range.
-    __device__ __forceinline__ void run(const Keys& s, int t0, int t1, int full) {
+    // `stop` is asked once they are on their way.
+    template <typename F>
+    __device__ __forceinline__ bool run(const Keys& s, int t0, int t1, int full, F stop) {
         fresh_addresses();
         int stage = 0, t = t0;
         if constexpr (!C::PIPE) {
             Scores cur;
             load_tile(s, t0, true, 0);
+            if (stop()) return false;
             auto one = [&](auto hidden, int at) {
                 wait_and_meet<0>();
                 load_tile(s, t + 1, t + 1 < t1, at ^ 1);
@@ -672,6 +760,7 @@ struct Block {
             load_half<false>(s, t0, true, 0);
             load_half<true>(s, t0, true, 0);
             load_half<false>(s, t0 + 1, t0 + 1 < t1, 1);
+            if (stop()) return false;
             wait_and_meet<2 * C::JN>();
             scores<true>(0, now);
             if (t0 >= full) hide(now, t0 * C::BN);
@@ -704,6 +793,7 @@ struct Block {
             step<false, true>(stage, t, now, next, top);
         }
         wait_and_meet<0>();
+        return true;
     }
 
     // The lanes of a row summed their own keys.
@@ -833,31 +923,34 @@ __device__ __forceinline__ void report(const Args& a, bool malformed) {
 }
 
 // The long form: one block per key head, sequence, tile of BM rows and key part; the last tiles of a
-// sequence (which see most keys) come first.  Key heads are the fastest index, so the blocks that read
-// one head's keys at a time lie on few XCDs.  With prefix_rows the rows are all tokens' and the keys
-// the prefix alone.
+// sequence (which see most keys) come first, `chunk` of them before the next sequence's.  Key heads are the
+// fastest index, so the blocks that read one head's keys at a time lie on few XCDs.  With prefix_rows the rows
+// are all tokens' and the keys the prefix alone.
 template <typename C>
 __global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
     extern __shared__ __align__(1024) char lds[];
-    long long total;
-    const bool malformed = check_and_find<C::NT>(a.c, [](int, int) { return 0ll; }, &total);
-    report(a, malformed);
-    if (malformed) return;
     unsigned x = blockIdx.x;
     const int hk = x % a.c.HK;
     x /= a.c.HK;
+    const int lo = x % a.chunk;
+    x /= a.chunk;
     const int B = a.prefix_rows ? 1 : a.c.B, b = x % B;
     x /= B;
-    const int part = x % a.splits, back = x / a.splits;
-    const int first = uniform(a.prefix_rows ? 0 : entry(a.c.offsets, b));
-    const int T = uniform(a.prefix_rows ? a.c.N : entry(a.c.offsets, b + 1)) - first;
+    const int part = x % a.splits, back = x / a.splits * a.chunk + lo;
+    // Queries and the first keys are on their way while the call is checked.
+    const Sequence seq = a.prefix_rows ? Sequence{0, a.c.N, 0, 0} : sequence(a.c, b);
+    const int first = seq.first, T = seq.T, n = seq.n;
+    const long long begin = seq.begin;
+    auto stop = [&] {
+        const bool malformed = check<C::NT>(a.c);
+        report(a, malformed);
+        if (malformed) wait_and_meet<0>();
+        return malformed;
+    };
     const int rows = T * a.G, tiles = (rows + C::BM - 1) / C::BM, row0 = (tiles - 1 - back) * C::BM;
-    if (row0 < 0 || rows == 0) return;
-    int n = 0;
-    long long begin = 0;
-    if (!a.prefix_rows) {
-        n = a.c.kv_len != nullptr ? uniform(entry(a.c.kv_len, b)) : T;
-        begin = a.c.kv_begin != nullptr ? uniform((long long)entry(a.c.kv_begin, b)) : first;
+    if (row0 < 0 || rows == 0) {
+        if (blockIdx.x == 0) stop();  // the block that reports
+        return;
     }
     const int seen0 = n - T + 1;
     const int last_token = min(row0 + C::BM, rows) - 1;
@@ -875,13 +968,15 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
     if (t0 < p1) {
         blk.see(row0, rows, false, 0, a.c.prefix_len);
         blk.set_source(a.c.pk.row, a.c.pv.row);
-        blk.run(prefix, t0, p1, a.c.prefix_len / C::BN);
+        if (!blk.run(prefix, t0, p1, a.c.prefix_len / C::BN, stop)) return;
     }
     if (k0 < k1) {
         blk.see(row0, rows, true, seen0, n);
         blk.set_source(a.c.k.row, a.c.v.row);
-        blk.run(own, k0, k1, uniform(max(0, min(n, seen0 + row0 / a.G)) / C::BN));
+        const int full = uniform(max(0, min(n, seen0 + row0 / a.G)) / C::BN);
+        if (!blk.run(own, k0, k1, full, [&] { return t0 < p1 ? false : stop(); })) return;
     }
+    if (t0 >= p1 && k0 >= k1 && stop()) return;  // no keys at all
     blk.sum_rows();
     const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? a.set0 + part : -1, -1};
     blk.store(to);
@@ -1035,11 +1130,11 @@ struct Short {
     static constexpr int NS = RB <= 256 ? 4 : RB <= 512 && WR == 3 ? 4 : RB <= 512 && WR == 4 ? 3 : 2;
     using C = Cfg<T, 16, DP, WR, 1, NS, 1>;
 };
-// Long form, 32 x 32 tiles, four waves.
+// Long form, 32 x 32 tiles, four waves (eight at width 256 in half precision, where they share the queries' place).
 template <typename T, int DP>
 struct Long {
     static constexpr int RB = DP * (int)sizeof(typename T::storage);
-    using C = Cfg<T, 32, DP, 4, RB <= 256 ? 2 : 1, 2, RB <= 512 ? 2 : 1>;
+    using C = Cfg<T, 32, DP, RB == 512 && sizeof(typename T::storage) == 2 ? 8 : 4, RB <= 256 ? 2 : 1, 2, RB <= 512 ? 2 : 1>;
 };
 
 // What the host needs to know of a configuration: tile sizes, bytes of the ring and of a row in LDS.
