@@ -79,11 +79,11 @@ struct Parts {
 // groups of them share the parts.
 template <typename T>
 __global__ __launch_bounds__(256) void join_few_kernel(Args a, int bm, int local_set) {
-    if (*a.status != 0) return;
+    const int status = *a.status;  // asked for together with the row's information
     const int t = blockIdx.x / a.c.H, h = blockIdx.x - t * a.c.H;
     Parts parts;
     parts.find(a, t, h, local_set);
-    if (parts.all == 0) return;
+    if (parts.all == 0 || status != 0) return;
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4, e = blockIdx.y * 64 + 4 * lane;
     float top = kNoMax, l = 0.0f;
     f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -102,13 +102,13 @@ __global__ __launch_bounds__(256) void join_few_kernel(Args a, int bm, int local
 // Many rows: `lanes` (16, 32 or 64) of a wave hold a row's elements, its other groups of so many share the parts.
 template <typename T, int LANES>
 __global__ __launch_bounds__(256) void join_rows_kernel(Args a, int bm, int local_set) {
-    if (*a.status != 0) return;
+    const int status = *a.status;
     const long long row = blockIdx.x * 4ll + (threadIdx.x >> 6);
     if (row >= a.set_rows) return;
     const int t = (int)(row / a.c.H), h = (int)(row - (long long)t * a.c.H);
     Parts parts;
     parts.find(a, t, h, local_set);
-    if (parts.all == 0) return;
+    if (parts.all == 0 || status != 0) return;
     const int lane = threadIdx.x & (LANES - 1), group = (threadIdx.x & 63) / LANES, e = 4 * lane;
     float top = kNoMax, l = 0.0f;
     f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -125,8 +125,9 @@ __global__ __launch_bounds__(256) void join_rows_kernel(Args a, int bm, int loca
 // Many rows, of which few were cut: for every worker, the run that starts there and goes on; a wave a row.
 template <typename T>
 __global__ __launch_bounds__(256) void join_cut_kernel(Args a, int bm) {
-    if (*a.status != 0) return;
+    const int status = *a.status;
     const int4 cut = a.cut[blockIdx.x];  // first token, tokens, key head, pieces
+    if (status != 0) return;
     const int lane = threadIdx.x & 63, e = 4 * lane, r = blockIdx.y * 4 + (threadIdx.x >> 6);
     if (r >= cut.y * a.G) return;
     Parts parts{0, r, (int)blockIdx.x, cut.w, cut.w};

@@ -42,6 +42,7 @@ typedef short v4i16 __attribute__((ext_vector_type(4)));
 
 constexpr int kRsrc = 0x00020000;     // raw buffer, range checked
 constexpr int kOutside = 0x40000000;  // a byte offset past every tile's range
+constexpr int kMostKeys = INT_MAX - 4096;  // of a sequence: an index past its last tile still fits
 constexpr float kNoMax = -3.0e38f;    // running maximum before the first key: below every score
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -193,93 +194,129 @@ __device__ __forceinline__ Sequence sequence(const AttnLaunch& c, int i) {
     return s;
 }
 
-// Whether sequence i is malformed; T and n as the arrays have them.
-__device__ __forceinline__ bool bad_sequence(const AttnLaunch& c, int i, int* T, int* n) {
-    const int o = c.offsets[i], e = c.offsets[i + 1], t = e - o;
-    bool bad = (t < 0) | (t > c.max_q) | (i == 0 && o != 0) | (i == c.B - 1 && e != c.N);
-    *T = *n = t;
-    if (c.kv_len != nullptr) {
-        *n = c.kv_len[i];
-        const long long begin = c.kv_begin[i];
-        bad |= (*n < 0) | (begin < 0) | (begin > c.kv_rows) | (begin + *n > c.kv_rows);
-    } else {
-        bad |= (e > c.kv_rows);
+// Sequence i as the arrays have it, and whether it is malformed.
+struct Entry {
+    int o, e, n;
+    long long begin;
+    __device__ __forceinline__ void read(const AttnLaunch& c, int i) {
+        o = c.offsets[i];
+        e = c.offsets[i + 1];
+        n = c.kv_len != nullptr ? c.kv_len[i] : 0;
+        begin = c.kv_begin != nullptr ? c.kv_begin[i] : 0;
     }
-    return bad;
-}
+    __device__ __forceinline__ bool bad(const AttnLaunch& c, int i) const {
+        const int t = e - o;
+        const bool offsets = (t < 0) | (t > c.max_q) | (i == 0 && o != 0) | (i == c.B - 1 && e != c.N);
+        if (c.kv_len == nullptr) return offsets | (e > c.kv_rows) | (t > kMostKeys);
+        return offsets | (n < 0) | (n > kMostKeys) | (begin < 0) | (begin > c.kv_rows) | (begin + n > c.kv_rows);
+    }
+    __device__ __forceinline__ int keys(const AttnLaunch& c) const { return c.kv_len != nullptr ? n : e - o; }
+};
 // Whole-call check.  Reached by all threads.
 template <int NT>
 __device__ __forceinline__ bool check(const AttnLaunch& c) {
-    int bad = 0, T, n;
-    for (int i = threadIdx.x; i < c.B; i += NT) bad |= bad_sequence(c, i, &T, &n);
+    int bad = 0;
+    for (int i = threadIdx.x; i < c.B; i += NT) {
+        Entry s;
+        s.read(c, i);
+        bad |= s.bad(c, i);
+    }
     return __syncthreads_or(bad) != 0;
 }
-// The same with a per-sequence sum: `units(T, n)` of every sequence.
-// Returns whether the call is malformed; total = the sum over all sequences, and for the sequence that
-// holds unit `want` (want < total) seq = its index and base = the sum before it.  Reached by all threads.
-template <int NT, typename F>
-__device__ __forceinline__ bool check_and_find(const AttnLaunch& c, F units, long long* total_out) {
-    __shared__ long long wave_sum[NT / 64];
-    int bad = 0;
-    long long sum = 0;
-    for (int i = threadIdx.x; i < c.B; i += NT) {
-        int T, n;
-        bad |= bad_sequence(c, i, &T, &n);
-        sum += units(T, n);
-    }
-    const bool malformed = __syncthreads_or(bad) != 0;
-    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-    if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < NT / 64; ++w) total += wave_sum[w];
-    *total_out = uniform(total);
-    return malformed;
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ uint32_t scan_lanes(uint32_t x) {
+#define GDN_SCAN_STEP(ctrl, rows) x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, rows, 0xf, false)
+    GDN_SCAN_STEP(0x111, 0xf);  // from 1, 2, 4 and 8 lanes below, in each 16
+    GDN_SCAN_STEP(0x112, 0xf);
+    GDN_SCAN_STEP(0x114, 0xf);
+    GDN_SCAN_STEP(0x118, 0xf);
+    GDN_SCAN_STEP(0x142, 0xa);  // the sum of 16 to the second and fourth 16, that of 32 to the upper half
+    GDN_SCAN_STEP(0x143, 0xc);
+#undef GDN_SCAN_STEP
+    return x;
 }
 
-// The sequence that holds unit `want` (in sequence order) and the units before it; all threads.
-template <int NT, typename F>
-__device__ __forceinline__ void find_unit(const AttnLaunch& c, F units, long long want, int* seq, long long* base) {
-    __shared__ long long wave_sum[NT / 64], found_base;
-    __shared__ int found;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    long long before = 0;
-    for (int i0 = 0;; i0 += NT) {
-        const int i = i0 + threadIdx.x;
-        long long mine = 0;
-        if (i < c.B) {
-            const int t = c.offsets[i + 1] - c.offsets[i];
-            mine = units(t, c.kv_len != nullptr ? c.kv_len[i] : t);
+// The call's sequences with their key tiles: the whole-call check, the sum of the tiles, and the sequence that holds
+// a given tile.  Every wave goes over all sequences by itself, 64 a time; the first 256 stay in its registers, so a
+// decode step reads the call's arrays once.
+template <int BN>
+struct Tiles {
+    static constexpr int KEEP = 4;
+    const AttnLaunch& c;
+    uint32_t upto[KEEP];  // tiles of the 64 up to and with the lane's sequence
+    long long total = 0;
+    bool malformed = false;
+
+    // a sequence without keys still has rows to write: one (masked) tile
+    static __device__ __forceinline__ int of(int T, int n) { return T <= 0 ? 0 : n <= BN ? 1 : (int)(((unsigned)n + BN - 1) / BN); }
+
+    __device__ __forceinline__ explicit Tiles(const AttnLaunch& c_) : c(c_) {
+        const int lane = threadIdx.x & 63;
+        bool bad = false;
+        Entry s[KEEP] = {};
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j)
+            if (64 * j < c.B) s[j].read(c, min(64 * j + lane, c.B - 1));  // all on their way before one is used
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j) {
+            upto[j] = 0;
+            if (64 * j < c.B) {
+                upto[j] = count(s[j], 64 * j + lane, &bad);
+                total += (uint32_t)__builtin_amdgcn_readlane((int)upto[j], 63);
+            }
         }
-        long long inc = mine;
-        for (int m = 1; m < 64; m <<= 1) {
-            const long long y = __shfl_up(inc, m);
-            if (lane >= m) inc += y;
+        for (int i0 = 64 * KEEP; i0 < c.B; i0 += 64) {
+            s[0].read(c, min(i0 + lane, c.B - 1));
+            total += (uint32_t)__builtin_amdgcn_readlane((int)count(s[0], i0 + lane, &bad), 63);
         }
-        if (lane == 63) wave_sum[wave] = inc;
-        if (threadIdx.x == 0) found = -1;
-        __syncthreads();
-        long long at = before + inc - mine, all = before;
-        for (int w = 0; w < NT / 64; ++w) {
-            if (w < wave) at += wave_sum[w];
-            all += wave_sum[w];
-        }
-        if (want >= at && want < at + mine) {
-            found = i;
-            found_base = at;
-        }
-        __syncthreads();
-        const int f = found;
-        const long long fb = found_base;
-        __syncthreads();
-        if (f >= 0 || i0 + NT >= c.B) {
-            *seq = uniform(f < 0 ? 0 : f);
-            *base = uniform(fb);
-            return;
-        }
-        before = all;
+        malformed = __builtin_amdgcn_ballot_w64(bad) != 0;
     }
-}
+    // Tiles of the lanes' sequences (lane i has entry i) up to and with each one.
+    __device__ __forceinline__ uint32_t count(const Entry& s, int i, bool* bad) const {
+        *bad |= s.bad(c, min(i, c.B - 1));
+        return scan_lanes(i < c.B ? (uint32_t)of(s.e - s.o, s.keys(c)) : 0u);
+    }
+    // The sequence of tile v < total, and the tiles before that sequence.
+    __device__ __forceinline__ void find(long long v, int* b, long long* before) const {
+        const int lane = threadIdx.x & 63;
+        long long sum = 0;
+        auto here = [&](int i0, uint32_t with) {
+            const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)with, 63);
+            if (v - sum >= all) {
+                sum += all;
+                return false;
+            }
+            // the first lane whose tiles go past v
+            const int at = __ffsll((unsigned long long)__builtin_amdgcn_ballot_w64(with > (uint32_t)(v - sum))) - 1;
+            *b = i0 + at;
+            *before = sum + (at == 0 ? 0u : (uint32_t)__builtin_amdgcn_readlane((int)with, at - 1));
+            return true;
+        };
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j)
+            if (here(64 * j, upto[j])) return;
+        for (int i0 = 64 * KEEP; i0 < c.B; i0 += 64) {
+            Entry s;
+            bool bad = false;
+            s.read(c, min(i0 + lane, c.B - 1));
+            if (here(i0, count(s, i0 + lane, &bad))) return;
+        }
+    }
+};
+
+// `total` units in W parts that differ by one at most: where part w starts, and which part holds unit u.
+struct Cut {
+    long long size, longer;  // the first `longer` parts have size + 1
+    __device__ __forceinline__ Cut(long long total, int W) {
+        size = total >> 31 ? total / W : (long long)((unsigned)total / (unsigned)W);
+        longer = total - size * W;
+    }
+    __device__ __forceinline__ long long start(long long w) const { return w * size + min(w, longer); }
+    __device__ __forceinline__ int part(long long u) const {
+        const long long x = longer * (size + 1), a = u < x ? u : u - x, d = u < x ? size + 1 : size;
+        return (int)((u < x ? 0 : longer) + (a >> 31 ? a / d : (long long)((unsigned)a / (unsigned)d)));
+    }
+};
 
 template <typename T_, int M_, int DP_, int WR_, int KT_, int NS_, int WAVES_>
 struct Cfg {
@@ -998,23 +1035,24 @@ template <typename C>
 __global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
     extern __shared__ __align__(1024) char lds[];
     const int HK = a.c.HK;
-    // a sequence without keys still has rows to write: one (masked) tile
-    auto tiles_of = [](int T, int n) { return T <= 0 ? 0 : n <= C::BN ? 1 : (n + C::BN - 1) / C::BN; };
-    auto units = [&](int T, int n) { return (long long)HK * tiles_of(T, n); };
-    long long total;
-    const bool malformed = check_and_find<C::NT>(a.c, units, &total);
-    report(a, malformed);
+    const Tiles<C::BN> all(a.c);
+    auto tiles_of = [](int T, int n) { return Tiles<C::BN>::of(T, n); };
+    const long long total = uniform(all.total) * HK;
+    report(a, all.malformed);
     const int w = blockIdx.x;
-    const long long W = total < a.workers ? total : a.workers;
-    if (malformed || w >= W) {
+    const int W = (int)min(total, (long long)a.workers);
+    if (all.malformed || w >= W) {
         if (a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(0, 0, 0, 0);
         return;
     }
-    long long u = w * total / W;  // first unit of the consumer's run
-    const long long u1 = (w + 1ll) * total / W;
-    long long base;
+    const Cut cut(total, W);
+    long long u = uniform(cut.start(w));  // first unit of the consumer's run
+    const long long u1 = uniform(cut.start(w + 1));
     Run ld;  // the run whose tiles are being asked for
-    find_unit<C::NT>(a.c, units, u, &ld.b, &base);
+    long long base;
+    all.find(u >> 31 ? u / HK : (unsigned)u / (unsigned)HK, &ld.b, &base);
+    ld.b = uniform(ld.b);
+    base = uniform(base) * HK;
     auto open = [&] {
         ld.first = uniform(entry(a.c.offsets, ld.b));
         ld.T = uniform(entry(a.c.offsets, ld.b + 1)) - ld.first;
@@ -1029,7 +1067,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
 
     int left = (int)(u1 - u);  // tiles not asked for yet
     const int within = (int)(u - base);
-    ld.hk = within / ld.tiles;
+    ld.hk = uniform(within / ld.tiles);
     ld.t0 = within - ld.hk * ld.tiles;
     Keys keys;
     auto enter = [&] {  // the loads go on in run ld
@@ -1086,9 +1124,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
                 blk.redo(to, own, 0, 0, own, run.t0 * C::BN, min(run.t1 * C::BN, run.n), run.n - run.T + 1);
             }
             if (run.t0 == 0) {
-                // the worker that holds the run's last unit
-                const long long last = u + run.tiles - 1;
-                const int pieces = whole ? 1 : (int)(((last + 1) * W - 1) / total) - w + 1;
+                const int pieces = whole ? 1 : cut.part(u + run.tiles - 1) - w + 1;
                 if (a.row_info != nullptr)
                     for (int i = threadIdx.x; i < run.T; i += C::NT)
                         a.row_info[(long long)(run.first + i) * HK + run.hk] = make_int2(whole ? -1 : w, pieces * 128 + i);
