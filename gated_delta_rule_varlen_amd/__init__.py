@@ -8,7 +8,6 @@ library.  Every step of the computation runs in the library's HIP kernels; there
 from __future__ import annotations
 
 import ctypes
-import struct
 from typing import Optional
 
 import torch
@@ -355,54 +354,30 @@ def decode_step(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, *,
     return out, state_out, conv_state_out
 
 
-# The operators below are called once a layer and token, so their host side is kept short: descriptors are
-# packed straight to bytes (gdn_rope_desc and gdn_attn_desc have one layout), and addresses and streams
-# passed as plain integers.
-_DESC = struct.Struct("=7iIfi13q")
-_NO_ROWS = (None, 0, 0, 0)
+# The operators below are called once a layer and token, so their arguments are marshalled in native code
+# (csrc/gdn_bind.cpp, built as _bind.so), which calls libgdn's entry points by address.
+_native = None
 
 
-def _raw_stream(dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev)
+def _marshal():
+    global _native
+    if _native is None:
+        L = lib()
+        try:
+            from . import _bind
+        except ImportError as e:
+            raise ImportError(f"_bind.so is missing or does not load ({e}): build it with "
+                              "`python -m gated_delta_rule_varlen_amd.build`") from e
+        _bind.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.gdn_qk_norm_rope_varlen, L.gdn_attention_varlen, L.gdn_attention_prefix_varlen, L.gdn_attention_workspace_bytes)))
+        _native = _bind
+    return _native
 
 
-def _head_rows(t: torch.Tensor, heads: int, D: int, dtype, dev: int, what: str):
-    """(device address, row stride, head stride, rows) of a [rows, heads, D] tensor with contiguous heads."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{what}: dtype {t.dtype} differs from {dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{what} must be on cuda:{dev}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
-        raise ValueError(f"{what} must be [rows, {heads}, {D}], got {tuple(shape)}")
-    if stride[2] != 1 and D != 1:
-        raise ValueError(f"{what}: the elements of a head must be contiguous")
-    # the stride of an axis of one entry names nothing
-    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * D, stride[1] if heads > 1 else D, shape[0]
-
-
-def _flat(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, dev: int, what: str):
-    """Device address of a contiguous vector of n entries (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{what} must be on cuda:{dev}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous with {n} entries")
-    return t.data_ptr()
-
-
-def _query_shape(q: torch.Tensor):
-    """(N, H, D, device index) of the queries."""
-    if q.dim() != 3:
-        raise ValueError(f"q must be [N, heads, D], got {tuple(q.shape)}")
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("q must be a device tensor")
-    N, H, D = q.shape
-    return N, H, D, dev
+def _raw_stream(q) -> int:
+    """Address of torch's current stream on q's device; what is no device tensor is refused with the others."""
+    dev = q.get_device() if isinstance(q, torch.Tensor) else -1
+    return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
 
 
 def qk_norm_rope_varlen(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], offsets: torch.Tensor, *,
@@ -418,95 +393,12 @@ def qk_norm_rope_varlen(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
     (int64 [B]), goes to row kv_begin[b] + past[b] + i of k_out and v_out [rows, HK, D]; without
     kv_begin to the row of its own index.  q_out may be q; outputs not given are allocated (k_out and
     v_out only without kv_begin).  Returns (q_out, k_out, v_out)."""
-    N, H, D, dev = _query_shape(q)
-    HK = k.shape[1]
-    B = offsets.numel() - 1
-    dtype = q.dtype
-    if kv_begin is not None and (k_out is None or (v is not None and v_out is None)):
-        raise ValueError("k_out and v_out are required with kv_begin")
-    if q_out is None:
-        q_out = q.new_empty((N, H, D))
-    if k_out is None:
-        k_out = q.new_empty((N, HK, D))
-    qp, qr, qh, _ = _head_rows(q, H, D, dtype, dev, "q")
-    kp, kr, kh, nk = _head_rows(k, HK, D, dtype, dev, "k")
-    qop, qor, qoh, nqo = _head_rows(q_out, H, D, dtype, dev, "q_out")
-    kop, kor, koh, rows = _head_rows(k_out, HK, D, dtype, dev, "k_out")
-    if nk != N or nqo != N:
-        raise ValueError("q, k and q_out must have one row per token")
-    if v is None:
-        v_out = None
-        vp, vr, vh, _ = vop, vor, voh, _ = _NO_ROWS
-    else:
-        if v_out is None:
-            v_out = q.new_empty((N, HK, D))
-        vp, vr, vh, nv = _head_rows(v, HK, D, dtype, dev, "v")
-        vop, vor, voh, nvo = _head_rows(v_out, HK, D, dtype, dev, "v_out")
-        if nv != N or nvo != rows:
-            raise ValueError("v must have one row per token and v_out as many rows as k_out")
-    half = inv_freq.numel()
-    desc = _DESC.pack(B, N, H, HK, D, 2 * half, _code(q, "q"), _abi.ROPE_INTERLEAVED if interleaved else 0, eps, 0, rows,
-                      qr, qh, kr, kh, vr, vh, qor, qoh, kor, koh, vor, voh)
-    st = lib().gdn_qk_norm_rope_varlen(
-        desc, qp, kp, vp, _flat(inv_freq, half, torch.float32, dev, "inv_freq"),
-        _flat(q_weight, D, torch.float32, dev, "q_weight"), _flat(k_weight, D, torch.float32, dev, "k_weight"),
-        _flat(offsets, B + 1, torch.int32, dev, "offsets"), _flat(past, B, torch.int32, dev, "past"),
-        _flat(positions, B, torch.int32, dev, "positions"), _flat(kv_begin, B, torch.int64, dev, "kv_begin"), qop, kop,
-        vop, _flat(dev_status, 1, torch.int32, dev, "dev_status"), _raw_stream(dev))
-    _check(st, "gdn_qk_norm_rope_varlen")
+    st, q_out, k_out, v_out = (_native or _marshal()).rope(
+        q, k, v, offsets, inv_freq, q_weight, k_weight, eps, interleaved, past, positions, kv_begin, q_out, k_out, v_out,
+        dev_status, _raw_stream(q))
+    if st:
+        _check(st, "gdn_qk_norm_rope_varlen")
     return q_out, k_out, v_out
-
-
-def _attention(q, prefix_k, prefix_v, k, v, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse, workspace,
-               dev_status, where):
-    N, H, D, dev = _query_shape(q)
-    HK = k.shape[1]
-    B = offsets.numel() - 1
-    dtype = q.dtype
-    qp, qr, qh, _ = _head_rows(q, H, D, dtype, dev, "q")
-    kp, kr, kh, rows = _head_rows(k, HK, D, dtype, dev, "k")
-    vp, vr, vh, nv = _head_rows(v, HK, D, dtype, dev, "v")
-    if nv != rows:
-        raise ValueError("k and v must have the same rows")
-    if out is None:
-        out = q.new_empty((N, H, D))
-        op, orow, oh = out.data_ptr(), H * D, D
-    else:
-        op, orow, oh, no = _head_rows(out, H, D, dtype, dev, "out")
-        if no != N:
-            raise ValueError("out must have one row per token")
-    if prefix_k is None:
-        pkp, pkr, pkh, prefix = pvp, pvr, pvh, _ = _NO_ROWS
-    else:
-        pkp, pkr, pkh, prefix = _head_rows(prefix_k, HK, D, dtype, dev, "prefix_k")
-        pvp, pvr, pvh, npv = _head_rows(prefix_v, HK, D, dtype, dev, "prefix_v")
-        if npv != prefix:
-            raise ValueError("prefix_k and prefix_v must have the same rows")
-    if lse is None and return_lse:
-        lse = torch.empty((N, H), dtype=torch.float32, device=q.device)
-    desc = _DESC.pack(B, N, H, HK, D, N if max_q is None else min(max_q, N), _code(q, "q"), 0, scale, prefix, rows,
-                      qr, qh, kr, kh, vr, vh, orow, oh, pkr, pkh, pvr, pvh)
-    L = lib()
-    if workspace is None:
-        n = ctypes.c_size_t()
-        _check(L.gdn_attention_workspace_bytes(desc, ctypes.byref(n)), "gdn_attention_workspace_bytes")
-        ws_bytes = n.value
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-            ws = workspace.data_ptr()
-        else:
-            ws = None
-    else:
-        ws, ws_bytes = _ptr(workspace, "workspace"), workspace.nbytes
-    tail = (_flat(offsets, B + 1, torch.int32, dev, "offsets"), _flat(kv_begin, B, torch.int64, dev, "kv_begin"),
-            _flat(kv_len, B, torch.int32, dev, "kv_len"), op, _flat(lse, N * H, torch.float32, dev, "lse"), ws, ws_bytes,
-            _flat(dev_status, 1, torch.int32, dev, "dev_status"), _raw_stream(dev))
-    if prefix_k is None:
-        st = L.gdn_attention_varlen(desc, qp, kp, vp, *tail)
-    else:
-        st = L.gdn_attention_prefix_varlen(desc, qp, pkp, pvp, kp, vp, *tail)
-    _check(st, where)
-    return out, lse
 
 
 def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, *, kv_len=None,
@@ -519,8 +411,11 @@ def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets:
     [B]), its own new tokens last; without them row t belongs to token t.  max_q is the longest
     sequence's token count or any larger number (default N: correct, with idle blocks).  scale 0 is
     1/sqrt(D).  Returns (out [N, H, D], lse [N, H] fp32, or None unless asked for)."""
-    return _attention(q, None, None, k, v, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse, workspace,
-                      dev_status, "gdn_attention_varlen")
+    st, out, lse = (_native or _marshal()).attention(q, None, None, k, v, offsets, kv_len, kv_begin, max_q, scale, out, lse,
+                                                     return_lse, workspace, dev_status, _raw_stream(q))
+    if st:
+        _check(st, "gdn_attention_varlen")
+    return out, lse
 
 
 def attention_prefix_varlen(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor, k: torch.Tensor,
@@ -530,8 +425,13 @@ def attention_prefix_varlen(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: t
     """attention_varlen where every sequence's keys start with the rows of prefix_k, prefix_v
     [P, HK, D], read once for the whole batch (gdn_attention_prefix_varlen); kv_len counts a sequence's own
     rows only."""
-    return _attention(q, prefix_k, prefix_v, k, v, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse,
-                      workspace, dev_status, "gdn_attention_prefix_varlen")
+    if prefix_k is None or prefix_v is None:
+        raise TypeError("prefix_k and prefix_v must be tensors")
+    st, out, lse = (_native or _marshal()).attention(q, prefix_k, prefix_v, k, v, offsets, kv_len, kv_begin, max_q, scale, out,
+                                                     lse, return_lse, workspace, dev_status, _raw_stream(q))
+    if st:
+        _check(st, "gdn_attention_prefix_varlen")
+    return out, lse
 
 
 def attention_workspace_bytes(q: torch.Tensor, B: int, *, HK: int, max_q: int, kv_rows: int, prefix_len: int = 0) -> int:
@@ -539,8 +439,10 @@ def attention_workspace_bytes(q: torch.Tensor, B: int, *, HK: int, max_q: int, k
     `workspace` for queries like q; it allocates them itself when the caller keeps none."""
     N, H, D = q.shape
     qr, qh, _ = q.stride()
-    desc = _DESC.pack(B, N, H, HK, D, min(max_q, N), _code(q, "q"), 0, 0.0, prefix_len, kv_rows, qr if N > 1 else H * D,
-                      qh if H > 1 else D, *([0] * 10))
+    pair = ctypes.c_int64 * 2
+    none = pair()
+    d = _abi.AttnDesc(B, N, H, HK, D, min(max_q, N), _code(q, "q"), 0, 0.0, prefix_len, kv_rows,
+                      pair(qr if N > 1 else H * D, qh if H > 1 else D), none, none, none, none, none)
     n = ctypes.c_size_t()
-    _check(lib().gdn_attention_workspace_bytes(desc, ctypes.byref(n)), "gdn_attention_workspace_bytes")
+    _check(lib().gdn_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)), "gdn_attention_workspace_bytes")
     return n.value

@@ -168,7 +168,6 @@ def lib() -> ctypes.CDLL:
         L.gdn_decode_step.restype = st
         L.gdn_scan_workspace_bytes.argtypes = [ctypes.POINTER(ScanDesc), ctypes.POINTER(ctypes.c_size_t)]
         L.gdn_scan_workspace_bytes.restype = st
-        # descriptors as addresses: a structure by reference, or its bytes
         L.gdn_qk_norm_rope_varlen.argtypes = [vp] + [vp] * 15
         L.gdn_qk_norm_rope_varlen.restype = st
         L.gdn_attention_varlen.argtypes = [vp] + [vp] * 9 + [ctypes.c_size_t, vp, vp]

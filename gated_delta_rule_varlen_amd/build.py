@@ -1,6 +1,7 @@
-"""Build libgdn.so (the C-ABI library) in-tree with hipcc for gfx950.
+"""Build libgdn.so (the C-ABI library) in-tree with hipcc for gfx950, and _bind.so (host code only: the argument
+marshalling of the softmax-attention operators) against torch's headers.
 
-Every source under csrc/ is compiled to an object in _build/ (in parallel), then linked into
+Every source of libgdn.so under csrc/ is compiled to an object in _build/ (in parallel), then linked into
 gated_delta_rule_varlen_amd/libgdn.so.  Run as ``python -m gated_delta_rule_varlen_amd.build``.
 """
 from __future__ import annotations
@@ -16,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+BIND = os.path.join(PKG, "_bind.so")
 SOURCES = ["gdn_api.cpp", "gdn_conv.hip", "gdn_prepare.hip", "gdn_scan.hip", "gdn_seq.hip", "gdn_chunk.hip",
            "gdn_chunk_k64.hip", "gdn_chunk_k128.hip", "gdn_chunk_k256.hip",
            "gdn_decode.hip", "gdn_noalloc.hip", "gdn_attn_api.cpp", "gdn_rope.hip", "gdn_attn.hip",
@@ -44,12 +46,35 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_bind() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = BIND + f".tmp{os.getpid()}"
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
+    dirs = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"),
+                                            os.path.join(rocm, "include"), "/opt/rocm/include"]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           "-D__HIP_PLATFORM_AMD__=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(x for d in dirs for x in ("-isystem", d)), os.path.join(CSRC, "gdn_bind.cpp"), "-o", tmp, "-L" + libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for gdn_bind.cpp:\n{r.stderr}")
+    os.replace(tmp, BIND)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link libgdn.so; returns the library path."""
+    """Compile every HIP source and link libgdn.so, and the binding beside it; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     jobs = min(len(SOURCES), int(os.environ.get("MAX_JOBS", os.cpu_count() or 4)))
     with ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
+        bind = ex.submit(_build_bind)
         objs = list(ex.map(_compile, SOURCES))
+        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
