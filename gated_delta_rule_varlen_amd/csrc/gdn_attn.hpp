@@ -585,20 +585,40 @@ struct Block {
         if (vis_lo < min(base + C::BN, run_n)) spoiled |= any_not_finite(vt);
     }
 
-    // A stage's keys and values against the wave's rows.
+    // A stage's keys and values against the wave's rows.  The reads of values run ahead of their products, the first
+    // of them ahead of the softmax: one after the other they took longer than the tile's bytes from memory.
     __device__ __forceinline__ void use_tile(int stage, int base) {
         if (base >= vis_hi) return;
+        static_assert(KT == 1, "a tile of 32 keys");
+        const char* vt = lds + stage * C::STAGE + C::KTILE;
+        constexpr int N = C::HALF ? DT * (SN / 8) : DT * SN, AHEAD = N < 8 ? N : 8;
+        using Value = std::conditional_t<C::HALF, u32x4, float>;
+        Value v[N];
+        auto read = [&](int x) {
+            if constexpr (C::HALF) v[x] = values(vt, 0, x / DT, x % DT);
+            else v[x] = value(vt, 0, x / DT, x % DT);
+        };
         Scores s;
         scores<true>(stage, s);
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) read(x);
+        __builtin_amdgcn_sched_barrier(0);
         if (base + C::BN > vis_lo) {
             hide(s, base);
             asm volatile("");  // keeps this a branch: most tiles hide nothing
         }
         follow(largest(s));
         exponentials(s);
-        const char* vt = lds + stage * C::STAGE + C::KTILE;
         look(vt, base);
-        product(vt, s);
+        u32x4 p;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            if (C::HALF && x % DT == 0) p = packed(s, 0, x / DT);
+            if (x + AHEAD < N) read(x + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (C::HALF) multiply<T, M>(v[x], p, o[x % DT]);
+            else multiply1<M>(v[x], s[0][x / DT / C::EA][x / DT % C::EA], o[x % DT]);
+        }
     }
 
     __device__ __forceinline__ bool any_not_finite(const char* vt) {
@@ -638,6 +658,12 @@ struct Block {
         return f.v;
     }
 
+    __device__ __forceinline__ float value(const char* vt, int k, int i, int d) {
+        const int key = 4 * grp + i % 4, sw = C::place_v(key);
+        const char* row = vt + (32 * k + 4 * C::NG * (i / 4) + key) * C::RB + (col & 3) * 4;
+        return *reinterpret_cast<const float*>(row + (((M / 4 * d + (col >> 2)) ^ sw) * 16));
+    }
+
     // O^T += V^T P^T for the tile at vt.
     __device__ __forceinline__ void product(const char* vt, const Scores& s) {
         if constexpr (C::HALF) {
@@ -653,13 +679,9 @@ struct Block {
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int i = 0; i < SN; ++i) {
-                    const int key = 4 * grp + i % 4, sw = C::place_v(key);
-                    const char* row = vt + (32 * k + 4 * C::NG * (i / 4) + key) * C::RB + (col & 3) * 4;
+                for (int i = 0; i < SN; ++i)
 #pragma unroll
-                    for (int d = 0; d < DT; ++d)
-                        multiply1<M>(*reinterpret_cast<const float*>(row + (((M / 4 * d + (col >> 2)) ^ sw) * 16)), s[k][i / C::EA][i % C::EA], o[d]);
-                }
+                    for (int d = 0; d < DT; ++d) multiply1<M>(value(vt, k, i, d), s[k][i / C::EA][i % C::EA], o[d]);
         }
     }
 

@@ -93,8 +93,8 @@ __global__ __launch_bounds__(NT) void rope_rows_kernel(RopeLaunch a, int tpb, in
     // lanes without a piece read the row's first (and count it as zero below): no load stands in a branch
     const int r0 = in0 ? e0 : 0, r1 = in1 ? e1 : 0;
 
-    // A pass is R rows (heads) of the queries, the keys or the values of a token.
-    const int pq = (a.H + R - 1) / R, pk = (a.HK + R - 1) / R, passes = pq + pk + (a.v.p != nullptr ? pk : 0);
+    // A pass is R rows: of the queries, or of the keys with the values behind them, of a token.
+    const int kv = a.v.p != nullptr ? 2 * a.HK : a.HK, pq = (a.H + R - 1) / R, passes = pq + (kv + R - 1) / R;
     union Piece {
         u32x4 v;
         TS e[VEC];
@@ -102,10 +102,17 @@ __global__ __launch_bounds__(NT) void rope_rows_kernel(RopeLaunch a, int tpb, in
     struct Rows {
         Piece x[2];
     };
+    const TS* const qp = static_cast<const TS*>(a.q.p);
+    const TS* const kp = static_cast<const TS*>(a.k.p);
+    const TS* const vp = static_cast<const TS*>(a.v.p);
     auto fetch = [&](int t, int p) {
-        const HeadRows& s = p < pq ? a.q : p < pq + pk ? a.k : a.v;
-        const int heads = p < pq ? a.H : a.HK, h = (p < pq ? p : p < pq + pk ? p - pq : p - pq - pk) * R + lane / L;
-        const TS* src = static_cast<const TS*>(s.p) + t * s.row + min(h, heads - 1) * s.head;
+        const TS* src;
+        if (p < pq) {
+            src = qp + t * a.q.row + min(p * R + lane / L, a.H - 1) * a.q.head;
+        } else {
+            const int r = min((p - pq) * R + lane / L, kv - 1);
+            src = r < a.HK ? kp + t * a.k.row + r * a.k.head : vp + t * a.v.row + (r - a.HK) * a.v.head;
+        }
         Rows y;
         y.x[0].v = *reinterpret_cast<const u32x4*>(src + r0);
         y.x[1].v = *reinterpret_cast<const u32x4*>(src + r1);
@@ -125,11 +132,41 @@ __global__ __launch_bounds__(NT) void rope_rows_kernel(RopeLaunch a, int tpb, in
         wq[i] = a.q_weight != nullptr ? a.q_weight[e] : 1.0f;
         wk[i] = a.k_weight != nullptr ? a.k_weight[e] : 1.0f;
     }
+    // past the pairs the table turns by nothing, for the pieces of the tail
+    for (int i = half + lane; i < MAX_HALF; i += 64) turn[wave][i] = make_float2(1.0f, 0.0f);
+    const int pair0 = min(NEIGHBOURS ? e0 / 2 : e0, MAX_HALF - VEC);
     const bool malformed = rope_malformed(a, t0, t1, tok);
     report_status(a.dev_status, malformed);
     if (malformed) return;
 
     const float inv_d = 1.0f / (float)a.D;
+    float2 cs[VEC];
+    auto turned = [&](Rows x, const float (&w)[2 * VEC]) {
+        float y[2 * VEC], s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * VEC; ++i) {
+            y[i] = to_f32<T>(x.x[i / VEC].e[i % VEC]);
+            (i < VEC ? s0 : s1) = fmaf(y[i], y[i], i < VEC ? s0 : s1);
+        }
+        const float ss = (in0 ? s0 : 0.0f) + (in1 ? s1 : 0.0f);
+        const float inv = __builtin_amdgcn_rsqf(fmaf(group_sum<L>(ss), inv_d, a.eps));
+#pragma unroll
+        for (int i = 0; i < 2 * VEC; ++i) y[i] = y[i] * inv * w[i];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int lo = NEIGHBOURS ? 2 * i : i, hi = NEIGHBOURS ? 2 * i + 1 : VEC + i;
+            const float u = y[lo], v = y[hi];
+            y[lo] = u * cs[i].x - v * cs[i].y;
+            y[hi] = u * cs[i].y + v * cs[i].x;
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * VEC; ++i) x.x[i / VEC].e[i % VEC] = from_f32<T>(y[i]);
+        return x;
+    };
+    auto put = [&](TS* dst, const Rows& x) {
+        if (in0) *reinterpret_cast<u32x4*>(dst + e0) = x.x[0].v;
+        if (in1) *reinterpret_cast<u32x4*>(dst + e1) = x.x[1].v;
+    };
     for (; t < t1; t += NT / 64 / wpt) {
         const long long pos = uniform(tok[t - t0].pos), row = uniform(tok[t - t0].row);
 #pragma unroll
@@ -138,52 +175,32 @@ __global__ __launch_bounds__(NT) void rope_rows_kernel(RopeLaunch a, int tpb, in
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        float2 cs[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int pair = (NEIGHBOURS ? e0 / 2 : e0) + i;  // the tail's lanes lie past the pairs
-            const float2 c = turn[wave][min(pair, MAX_HALF - 1)];
-            cs[i] = pair < half ? c : make_float2(1.0f, 0.0f);
-        }
+        for (int i = 0; i < VEC; ++i) cs[i] = turn[wave][pair0 + i];
         __builtin_amdgcn_wave_barrier();
-        for (int p = share; p < passes; p += wpt) {
-            Rows now = next;
-            // the next rows of this token, or the first of the wave's next one
+        // the next rows of this token, or the first of the wave's next one
+        auto take = [&](int p) {
+            const Rows now = next;
             if (p + wpt < passes) next = fetch(t, p + wpt);
             else if (t + NT / 64 / wpt < t1) next = fetch(t + NT / 64 / wpt, share);
-            const bool is_q = p < pq, is_v = p >= pq + pk;
-            const int h = (is_q ? p : is_v ? p - pq - pk : p - pq) * R + lane / L;
-            if (!is_v) {
-                float y[2 * VEC], ss = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 2 * VEC; ++i) {
-                    y[i] = to_f32<T>(now.x[i / VEC].e[i % VEC]);
-                    ss = fmaf(y[i], (i < VEC ? in0 : in1) ? y[i] : 0.0f, ss);
-                }
-                const float inv = __builtin_amdgcn_rsqf(fmaf(group_sum<L>(ss), inv_d, a.eps));
-                if (is_q) {
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) y[i] = y[i] * inv * wq[i];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) y[i] = y[i] * inv * wk[i];
-                }
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int lo = NEIGHBOURS ? 2 * i : i, hi = NEIGHBOURS ? 2 * i + 1 : VEC + i;
-                    const float u = y[lo], w = y[hi];
-                    y[lo] = u * cs[i].x - w * cs[i].y;
-                    y[hi] = u * cs[i].y + w * cs[i].x;
-                }
-#pragma unroll
-                for (int i = 0; i < 2 * VEC; ++i) now.x[i / VEC].e[i % VEC] = from_f32<T>(y[i]);
+            return now;
+        };
+        int p = share;
+        for (; p < pq; p += wpt) {
+            const Rows x = turned(take(p), wq);
+            const int h = p * R + lane / L;
+            if (h < a.H) put(static_cast<TS*>(a.q_out.p) + t * a.q_out.row + h * a.q_out.head, x);
+        }
+        for (; p < passes; p += wpt) {
+            Rows x = take(p);
+            const int first = (p - pq) * R, r = first + lane / L;
+            const bool is_k = r < a.HK;
+            if (first < a.HK) {
+                const Rows y = turned(x, wk);
+                if (is_k) x = y;
             }
-            const HeadRows& d = is_q ? a.q_out : is_v ? a.v_out : a.k_out;
-            TS* dst = static_cast<TS*>(d.p) + (is_q ? t : row) * d.row + h * d.head;
-            if (h < (is_q ? a.H : a.HK)) {
-                if (in0) *reinterpret_cast<u32x4*>(dst + e0) = now.x[0].v;
-                if (in1) *reinterpret_cast<u32x4*>(dst + e1) = now.x[1].v;
-            }
+            if (is_k) put(static_cast<TS*>(a.k_out.p) + row * a.k_out.row + r * a.k_out.head, x);
+            else if (r < kv) put(static_cast<TS*>(a.v_out.p) + row * a.v_out.row + (r - a.HK) * a.v_out.head, x);
         }
     }
 }
