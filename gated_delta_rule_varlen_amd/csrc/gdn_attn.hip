@@ -3,8 +3,9 @@
 //
 // Short form (max_q * G rows fit a tile of 32, 64 or 128): decode steps and short blocks, bound by the
 // cache's bytes.  Long form: prompts, bound by the matrix cores.  A shared prefix is one more run of
-// keys for the long form's tiles; for the short form a launch of its own first runs all tokens' rows
-// over the prefix, reading it once for the whole batch.
+// keys for the long form's tiles; beside the short form, blocks of the long form run all tokens' rows over
+// the prefix, reading it once for the whole batch: in a launch of their own, or for small calls in the same one
+// (both_kernel).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -16,7 +17,6 @@ namespace {
 
 using namespace attn;
 
-constexpr int kCUs = 256;
 constexpr int kShortRows = 128;
 
 // A row's result from its parts' sums: out and lse.
@@ -141,10 +141,10 @@ __global__ __launch_bounds__(256) void join_cut_kernel(Args a, int bm) {
 
 struct Plan {
     Args a;
-    bool is_short, join;
+    bool is_short, join, both;
     int dp, wr, bm;
     int lds, long_lds;
-    long long blocks, prefix_blocks;
+    long long blocks;
     size_t bytes;
 };
 
@@ -173,9 +173,9 @@ Plan plan(const AttnLaunch& c) {
     const long double q_span = ((long double)c.max_q * c.q.row + (long double)a.G * c.q.head) * es;
     p.is_short = rows <= kShortRows && s.ring + q_lds <= kMaxLds && q_span < kOutside;
     p.long_lds = whole.ring;
-    // key parts of the long form: enough blocks for two a CU, each with a few tiles at least
+    // key parts of the long form: enough blocks for two a CU, each of 128 keys at least
     auto parts = [&](long long tiles, long long keys) {
-        const long long want = (2 * kCUs + tiles - 1) / std::max(1ll, tiles), most = keys / (4 * whole.bn);
+        const long long want = (2 * kCUs + tiles - 1) / std::max(1ll, tiles), most = keys / 128;
         return (int)std::max(1ll, std::min(std::min(want, most), 64ll));
     };
     const long long N = c.N, all_rows = N * a.G;
@@ -183,17 +183,25 @@ Plan plan(const AttnLaunch& c) {
     if (p.is_short) {
         p.bm = s.bm;
         p.lds = (int)(s.ring + q_lds);
+        if (c.prefix_len > 0 && c.N > 0) {
+            const long long tiles = (all_rows + whole.bm - 1) / whole.bm;
+            a.splits = parts(tiles * c.HK, c.prefix_len);
+            a.prefix_blocks = tiles * c.HK * a.splits;
+            a.sets = a.splits + 1;
+            a.to_sets = true;
+            a.local_set = a.splits;
+        }
         const int per_cu = std::min(8, (int)(160 * 1024 / (p.lds + 256)));
         const long long units = c.HK * (c.kv_rows / s.bn + c.B);  // fewer blocks than that have work, bar overlapping runs
         a.workers = (int)std::max(1ll, std::min((long long)kCUs * per_cu, units));
         p.blocks = a.workers;
-        if (c.prefix_len > 0 && c.N > 0) {
-            const long long tiles = (all_rows + whole.bm - 1) / whole.bm;
-            a.splits = parts(tiles * c.HK, c.prefix_len);
-            p.prefix_blocks = tiles * c.HK * a.splits;
-            a.sets = a.splits + 1;
-            a.to_sets = true;
-            a.set0 = a.splits;
+        // Both forms in one launch where all blocks run at once (8 drafts behind 1001 shared keys: 12.8 us, in two
+        // launches 19.2).  In more rounds the short form's blocks are too few on a CU beside the long form's
+        // (256 sequences behind 8192 keys: 138 us, in two launches 127).
+        p.both = a.prefix_blocks > 0 && a.prefix_blocks + a.workers <= 2 * kCUs && p.wr <= 4 && joint(whole.ring, p.lds);
+        if (p.both) {
+            p.lds = std::max(p.lds, whole.ring);
+            p.blocks = ((a.prefix_blocks + kCUs - 1) / kCUs + (a.workers + kCUs - 1) / kCUs) * kCUs;  // whole turns
         }
         p.join = c.N > 0 && (a.workers > 1 || a.sets > 0);
         by_rows = a.sets > 0 || few_rows(a);
@@ -238,22 +246,23 @@ Plan plan(const AttnLaunch& c) {
 template <typename T>
 hipError_t launch(const AttnLaunch& c, hipStream_t stream) {
     Plan p = plan<T>(c);
-    if (p.blocks > kMaxBlocks || p.prefix_blocks > kMaxBlocks || (p.join && p.a.set_rows > kMaxBlocks))
+    if (p.blocks > kMaxBlocks || p.a.prefix_blocks > kMaxBlocks || (p.join && p.a.set_rows > kMaxBlocks))
         return hipErrorInvalidConfiguration;
     hipError_t e;
     if (p.is_short) {
-        if (p.prefix_blocks > 0) {
-            Args a = p.a;
-            a.prefix_rows = true;
-            a.set0 = 0;
-            if ((e = start_long<T>(a, p.dp, p.prefix_blocks, p.long_lds, stream)) != hipSuccess) return e;
+        if (p.both) {
+            e = start_both<T>(p.a, p.dp, p.wr, p.blocks, p.lds, stream);
+        } else {
+            if (p.a.prefix_blocks > 0 &&
+                (e = start_long<T>(p.a, p.dp, p.a.prefix_blocks, p.long_lds, stream)) != hipSuccess)
+                return e;
+            e = start_short<T>(p.a, p.dp, p.wr, p.blocks, p.lds, stream);
         }
-        e = start_short<T>(p.a, p.dp, p.wr, p.blocks, p.lds, stream);
     } else {
         e = start_long<T>(p.a, p.dp, p.blocks, p.long_lds, stream);
     }
     if (e != hipSuccess || !p.join) return e;
-    const int local = p.is_short && p.a.sets > 0 ? p.a.set0 : -1;
+    const int local = p.is_short && p.a.sets > 0 ? p.a.local_set : -1;
     const unsigned rows = (unsigned)p.a.set_rows, fours = (unsigned)((p.a.set_rows + 3) / 4);
     if (p.a.cut != nullptr) {
         const unsigned most = (unsigned)(c.max_q * p.a.G + 3) / 4;

@@ -25,6 +25,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <type_traits>
@@ -55,9 +56,9 @@ struct Args {
     int splits;     // key parts of the long form
     int chunk;      // row tiles of a sequence that follow one another
     int workers;    // blocks of the short form
-    bool prefix_rows;  // the long form runs all tokens' rows over the prefix alone
     bool to_sets;   // results go to the workspace, for the joining kernel
-    int set0;       // first set this launch writes
+    int local_set;  // the set of a sequence's own keys, behind the prefix's key parts
+    long long prefix_blocks;  // blocks of the long form that run all tokens' rows over the prefix alone
     // workspace
     int* status;
     int2* row_info;    // [N][HK]: x = worker a cut run starts in (-1: not cut), y = pieces * 128 + token in sequence
@@ -168,9 +169,15 @@ struct Range {
         r = u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)bytes, (uint32_t)kRsrc};
     }
 };
+// STREAM: the bytes are read by this block alone (decode of 256 sequences: 357 us, without the hint 410).
+template <bool STREAM>
 __device__ __forceinline__ void load_to_lds(const Range& s, uint32_t at, int voff, int soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 ::"s"(at), "v"(voff), "s"(s.r), "s"(soff) : "m0", "memory");
+    if constexpr (STREAM)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                     ::"s"(at), "v"(voff), "s"(s.r), "s"(soff) : "m0", "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     ::"s"(at), "v"(voff), "s"(s.r), "s"(soff) : "m0", "memory");
 }
 
 // Sequence i of the call as its arrays give it, in bounds whatever they hold: what a block asks for before the
@@ -426,7 +433,7 @@ struct Block {
         const uint32_t to = lds_base + stage * C::STAGE + (V ? C::KTILE : 0) + wave * STEP;
 #pragma unroll
         for (int j = 0; j < C::JN; ++j)
-            load_to_lds(r, to + j * C::LW * STEP, (V ? voff : koff)[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * stride);
+            load_to_lds<M == 16>(r, to + j * C::LW * STEP, (V ? voff : koff)[j % C::PRE], (j / C::PRE) * C::PRE * C::RPI * stride);
     }
     __device__ __forceinline__ void load_tile(const Keys& s, int tile, bool real, int stage) {
         load_half<false>(s, tile, real, stage);
@@ -483,7 +490,7 @@ struct Block {
             const int r = (x + lane) / C::CPR, piece = ((x + lane) % C::CPR) ^ C::place_k(r), i = r / G, g = r - i * G;
             const int off = r < rows && piece * 16 < a.c.D * C::ES
                                 ? (int)((i * a.c.q.row + g * a.c.q.head) * C::ES) + piece * 16 : kOutside;
-            load_to_lds(rq, lds_base + at + x * 16, off, 0);
+            load_to_lds<false>(rq, lds_base + at + x * 16, off, 0);
         }
     }
     __device__ __forceinline__ void take_rows(const char* at, int rows) {
@@ -974,8 +981,8 @@ struct Block {
     }
 };
 
-__device__ __forceinline__ void report(const Args& a, bool malformed) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+__device__ __forceinline__ void report(const Args& a, bool malformed, unsigned block) {
+    if (block == 0 && threadIdx.x == 0) {
         if (a.c.dev_status != nullptr) *a.c.dev_status = malformed ? GDN_ERR_OFFSETS : GDN_OK;
         if (a.status != nullptr) *a.status = malformed ? 1 : 0;
     }
@@ -986,29 +993,28 @@ __device__ __forceinline__ void report(const Args& a, bool malformed) {
 // fastest index, so the blocks that read one head's keys at a time lie on few XCDs.  With prefix_rows the rows
 // are all tokens' and the keys the prefix alone.
 template <typename C>
-__global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
-    extern __shared__ __align__(1024) char lds[];
-    unsigned x = blockIdx.x;
+__device__ __forceinline__ void long_form(const Args& a, char* lds, const unsigned block, const bool prefix_rows) {
+    unsigned x = block;
     const int hk = x % a.c.HK;
     x /= a.c.HK;
     const int lo = x % a.chunk;
     x /= a.chunk;
-    const int B = a.prefix_rows ? 1 : a.c.B, b = x % B;
+    const int B = prefix_rows ? 1 : a.c.B, b = x % B;
     x /= B;
     const int part = x % a.splits, back = x / a.splits * a.chunk + lo;
     // Queries and the first keys are on their way while the call is checked.
-    const Sequence seq = a.prefix_rows ? Sequence{0, a.c.N, 0, 0} : sequence(a.c, b);
+    const Sequence seq = prefix_rows ? Sequence{0, a.c.N, 0, 0} : sequence(a.c, b);
     const int first = seq.first, T = seq.T, n = seq.n;
     const long long begin = seq.begin;
     auto stop = [&] {
         const bool malformed = check<C::NT>(a.c);
-        report(a, malformed);
+        report(a, malformed, block);
         if (malformed) wait_and_meet<0>();
         return malformed;
     };
     const int rows = T * a.G, tiles = (rows + C::BM - 1) / C::BM, row0 = (tiles - 1 - back) * C::BM;
     if (row0 < 0 || rows == 0) {
-        if (blockIdx.x == 0) stop();  // the block that reports
+        if (block == 0) stop();  // the block that reports
         return;
     }
     const int seen0 = n - T + 1;
@@ -1037,7 +1043,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
     }
     if (t0 >= p1 && k0 >= k1 && stop()) return;  // no keys at all
     blk.sum_rows();
-    const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? a.set0 + part : -1, -1};
+    const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? part : -1, -1};
     blk.store(to);
     if (blk.spoiled)
         blk.redo(to, prefix, t0 * C::BN, min(p1 * C::BN, a.c.prefix_len), own, k0 * C::BN, max(0, min(k1 * C::BN, n)), seen0);
@@ -1054,14 +1060,12 @@ struct Run {
 };
 
 template <typename C>
-__global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
-    extern __shared__ __align__(1024) char lds[];
+__device__ __forceinline__ void short_form(const Args& a, char* lds, const int w) {
     const int HK = a.c.HK;
     const Tiles<C::BN> all(a.c);
     auto tiles_of = [](int T, int n) { return Tiles<C::BN>::of(T, n); };
     const long long total = uniform(all.total) * HK;
-    report(a, all.malformed);
-    const int w = blockIdx.x;
+    report(a, all.malformed, w);
     const int W = (int)min(total, (long long)a.workers);
     if (all.malformed || w >= W) {
         if (a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(0, 0, 0, 0);
@@ -1136,7 +1140,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
             const int rows = run.T * a.G;
             const bool whole = run.t1 - run.t0 == run.tiles;
             // a worker's slot 0: a run cut at the front; slot 1: a run that starts here and goes on in the next worker
-            const typename Block<C>::To to{0, rows, run.first, run.hk, whole && a.to_sets ? a.set0 : -1,
+            const typename Block<C>::To to{0, rows, run.first, run.hk, whole && a.to_sets ? a.local_set : -1,
                                            whole ? -1 : w * 2ll + (run.t0 == 0 ? 1 : 0)};
             blk.store(to);
             if (blk.spoiled) {
@@ -1177,6 +1181,37 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
     }
 }
 
+template <typename C>
+__global__ __launch_bounds__(C::NT, C::WAVES) void long_kernel(Args a) {
+    extern __shared__ __align__(1024) char lds[];
+    long_form<C>(a, lds, blockIdx.x, a.prefix_blocks > 0);
+}
+template <typename C>
+__global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
+    extern __shared__ __align__(1024) char lds[];
+    short_form<C>(a, lds, blockIdx.x);
+}
+
+// A small batch behind a shared prefix, in one launch: blocks of the long form over the prefix beside blocks of the
+// short form over the sequences' own keys, so that neither waits for the other's launch and latency.  They take
+// turns by as many blocks as there are CUs.
+constexpr int kCUs = 256;
+template <typename CL, typename CS>
+__global__ __launch_bounds__(CL::NT, CL::WAVES) void both_kernel(Args a) {
+    static_assert(CS::NT <= CL::NT, "a block of either form");
+    extern __shared__ __align__(1024) char lds[];
+    const int turn = blockIdx.x / kCUs, at = blockIdx.x % kCUs;
+    const int pt = (int)((a.prefix_blocks + kCUs - 1) / kCUs), st = (a.workers + kCUs - 1) / kCUs, both = min(pt, st);
+    const bool over_prefix = turn < 2 * both ? turn % 2 == 0 : pt > st;
+    const int block = (turn < 2 * both ? turn / 2 : turn - both) * kCUs + at;
+    if (over_prefix) {
+        if (block < a.prefix_blocks) long_form<CL>(a, lds, block, true);
+    } else {
+        // the waves a block of the short form does not have end here; barriers wait for those that are left
+        if (block < a.workers && threadIdx.x < CS::NT) short_form<CS>(a, lds, block);
+    }
+}
+
 // ---- which tile for which call -------------------------------------------------------------------
 // Head widths are compiled for 64, 128 and 256.
 //
@@ -1184,6 +1219,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short_kernel(Args a) {
 // 64 to 96 KB a CU over its blocks.
 template <typename T, int DP, int WR>
 struct Short {
+    static constexpr int WIDTH = DP;
     static constexpr int RB = DP * (int)sizeof(typename T::storage);
     static constexpr int NS = RB <= 256 ? 4 : RB <= 512 && WR == 3 ? 4 : RB <= 512 && WR == 4 ? 3 : 2;
     using C = Cfg<T, 16, DP, WR, 1, NS, 1>;
@@ -1191,6 +1227,7 @@ struct Short {
 // Long form, 32 x 32 tiles, four waves (eight at width 256 in half precision, where they share the queries' place).
 template <typename T, int DP>
 struct Long {
+    static constexpr int WIDTH = DP;
     static constexpr int RB = DP * (int)sizeof(typename T::storage);
     using C = Cfg<T, 32, DP, RB == 512 && sizeof(typename T::storage) == 2 ? 8 : 4, RB <= 256 ? 2 : 1, 2, RB <= 512 ? 2 : 1>;
 };
@@ -1205,28 +1242,6 @@ constexpr Shape shape_of() {
 }
 
 constexpr int kMaxLds = 159 * 1024;  // of the 160 KB, less the kernels' own few words
-
-template <typename C, bool LONG>
-hipError_t start(const Args& a, long long blocks, int lds, hipStream_t stream) {
-    if (blocks > kMaxBlocks || lds > kMaxLds) return hipErrorInvalidConfiguration;
-    void (*f)(Args);
-    if constexpr (LONG) f = &long_kernel<C>;
-    else f = &short_kernel<C>;
-    if (lds > 64 * 1024) {
-        // has to be asked for, once on each device (asking twice does no harm)
-        static std::atomic<uint64_t> asked{0};
-        int dev = 0;
-        hipError_t e = hipGetDevice(&dev);
-        const uint64_t bit = 1ull << (dev & 63);
-        if (e == hipSuccess && (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit))) {
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
-            if (e == hipSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
-        }
-        if (e != hipSuccess) return e;
-    }
-    f<<<(unsigned)blocks, C::NT, lds, stream>>>(a);
-    return hipGetLastError();
-}
 
 // dp 64, 128 or 256; wr 1, 2, 3, 4 or 8.
 template <typename T, int DP, typename F>
@@ -1248,20 +1263,74 @@ auto with_long(int dp, F f) {
     return dp == 64 ? f(Long<T, 64>{}) : dp == 128 ? f(Long<T, 128>{}) : f(Long<T, 256>{});
 }
 
+// Both forms in one launch: for the widths and waves whose blocks of either form fit a CU twice.
+constexpr bool joint(int ring_long, int lds_short) { return std::max(ring_long, lds_short) <= 80 * 1024 - 512; }
+
 // One translation unit per type holds its kernels.
 template <typename T>
 hipError_t start_short(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream);
 template <typename T>
 hipError_t start_long(const Args& a, int dp, long long blocks, int lds, hipStream_t stream);
+template <typename T>
+hipError_t start_both(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream);
+
+// `asked`: the devices on which the kernel may have more than 64 KB of LDS already.
+template <typename F>
+hipError_t start_kernel(F* f, std::atomic<uint64_t>& asked, const Args& a, long long blocks, int threads, int lds,
+                        hipStream_t stream) {
+    if (blocks > kMaxBlocks || lds > kMaxLds) return hipErrorInvalidConfiguration;
+    if (lds > 64 * 1024) {
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        const uint64_t bit = 1ull << (dev & 63);
+        if (e == hipSuccess && (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit))) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
+            if (e == hipSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
+        }
+        if (e != hipSuccess) return e;
+    }
+    f<<<(unsigned)blocks, threads, lds, stream>>>(a);
+    return hipGetLastError();
+}
+template <typename C>
+hipError_t start_one_long(const Args& a, long long blocks, int lds, hipStream_t stream) {
+    static std::atomic<uint64_t> asked{0};
+    return start_kernel(&long_kernel<C>, asked, a, blocks, C::NT, lds, stream);
+}
+template <typename C>
+hipError_t start_one_short(const Args& a, long long blocks, int lds, hipStream_t stream) {
+    static std::atomic<uint64_t> asked{0};
+    return start_kernel(&short_kernel<C>, asked, a, blocks, C::NT, lds, stream);
+}
+template <typename CL, typename CS>
+hipError_t start_one_both(const Args& a, long long blocks, int lds, hipStream_t stream) {
+    if constexpr (CS::NT <= CL::NT && joint(CL::LDS, CS::LDS)) {
+        static std::atomic<uint64_t> asked{0};
+        return start_kernel(&both_kernel<CL, CS>, asked, a, blocks, CL::NT, lds, stream);
+    } else {
+        return hipErrorInvalidConfiguration;
+    }
+}
 
 #define GDN_ATTN_INSTANCES(T)                                                                                           \
     template <>                                                                                                         \
     hipError_t start_short<T>(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream) {           \
-        return with_short<T>(dp, wr, [&](auto p) { return start<typename decltype(p)::C, false>(a, blocks, lds, stream); }); \
+        return with_short<T>(dp, wr, [&](auto p) { return start_one_short<typename decltype(p)::C>(a, blocks, lds, stream); }); \
     }                                                                                                                   \
     template <>                                                                                                         \
     hipError_t start_long<T>(const Args& a, int dp, long long blocks, int lds, hipStream_t stream) {                    \
-        return with_long<T>(dp, [&](auto p) { return start<typename decltype(p)::C, true>(a, blocks, lds, stream); });   \
+        return with_long<T>(dp, [&](auto p) { return start_one_long<typename decltype(p)::C>(a, blocks, lds, stream); }); \
+    }                                                                                                                   \
+    template <>                                                                                                         \
+    hipError_t start_both<T>(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream) {            \
+        return with_long<T>(dp, [&](auto l) {                                                                           \
+            return with_short<T>(dp, wr, [&](auto p) {                                                                  \
+                using L = decltype(l);                                                                                  \
+                using P = decltype(p);                                                                                  \
+                if constexpr (L::WIDTH == P::WIDTH) return start_one_both<typename L::C, typename P::C>(a, blocks, lds, stream); \
+                else return hipErrorInvalidConfiguration;                                                               \
+            });                                                                                                         \
+        });                                                                                                             \
     }
 
 }  // namespace attn
