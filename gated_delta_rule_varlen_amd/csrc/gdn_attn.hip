@@ -208,11 +208,11 @@ Plan plan(const AttnLaunch& c) {
     } else {
         const long long most = (rows + whole.bm - 1) / whole.bm;  // tiles of the longest sequence
         a.splits = parts(std::min(most * c.B, all_rows / whole.bm + c.B) * c.HK, c.kv_rows + c.prefix_len);
-        // Where blocks come in many rounds, 16 tiles of a sequence follow one another and find its keys in the L2
-        // (prefill batch of 24748 tokens, 12 rounds: 670 us against 730 at one); in few rounds the even end counts,
-        // which the largest tiles first give (f32 batch of 10277 tokens, 2.5 rounds: 389 us at one, 465 at 16).
+        // 16 tiles of a sequence follow one another and find its keys in the L2 (prefill batch of 24748 tokens: 670 us
+        // against 730 at one).  More sequences than the kernel sorts by length do so only where blocks come in
+        // many rounds; in few the even end counts, which one tile of each, the last ones first, gives.
         const long long real = std::min(most * c.B, all_rows / whole.bm + c.B) * c.HK * a.splits;
-        a.chunk = real >= 8 * 2 * kCUs ? 16 : 1;
+        a.chunk = c.B <= 64 || real >= 8 * 2 * kCUs ? 16 : 1;
         p.blocks = (most + a.chunk - 1) / a.chunk * a.chunk * c.B * c.HK * a.splits;
         if (a.splits > 1) {
             a.sets = a.splits;

@@ -201,6 +201,18 @@ __device__ __forceinline__ Sequence sequence(const AttnLaunch& c, int i) {
     return s;
 }
 
+// The sequence of rank `place` by its keys, of 2 to 64: a sequence a lane.
+__device__ __forceinline__ int by_length(const AttnLaunch& c, int place) {
+    const int lane = threadIdx.x & 63, i = min(lane, c.B - 1);
+    const int n = c.kv_len != nullptr ? c.kv_len[i] : c.offsets[i + 1] - c.offsets[i];
+    int rank = 0;
+    for (int j = 0; j < c.B; ++j) {
+        const int other = __builtin_amdgcn_readlane(n, j);
+        rank += (other > n) | (other == n && j < lane);
+    }
+    return uniform(__ffsll((unsigned long long)__builtin_amdgcn_ballot_w64(lane < c.B && rank == place)) - 1);
+}
+
 // Sequence i as the arrays have it, and whether it is malformed.
 struct Entry {
     int o, e, n;
@@ -989,8 +1001,9 @@ __device__ __forceinline__ void report(const Args& a, bool malformed, unsigned b
 }
 
 // The long form: one block per key head, sequence, tile of BM rows and key part; the last tiles of a
-// sequence (which see most keys) come first, `chunk` of them before the next sequence's.  Key heads are the
-// fastest index, so the blocks that read one head's keys at a time lie on few XCDs.  With prefix_rows the rows
+// sequence (which see most keys) come first, `chunk` of them before the next sequence's, and up to 64 sequences go
+// by their keys, the longest first, so that the last blocks are short ones.  Key heads are the fastest index, so
+// the blocks that read one head's keys at a time lie on few XCDs.  With prefix_rows the rows
 // are all tokens' and the keys the prefix alone.
 template <typename C>
 __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsigned block, const bool prefix_rows) {
@@ -999,9 +1012,10 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
     x /= a.c.HK;
     const int lo = x % a.chunk;
     x /= a.chunk;
-    const int B = prefix_rows ? 1 : a.c.B, b = x % B;
+    const int B = prefix_rows ? 1 : a.c.B, place = x % B, b = B > 1 && B <= 64 ? by_length(a.c, place) : place;
     x /= B;
-    const int part = x % a.splits, back = x / a.splits * a.chunk + lo;
+    // a chunk's order differs by sequence: else an XCD (every eighth block) would get the same few tiles of all
+    const int part = x % a.splits, back = x / a.splits * a.chunk + (a.chunk > 1 ? lo ^ (place & 7) : lo);
     // Queries and the first keys are on their way while the call is checked.
     const Sequence seq = prefix_rows ? Sequence{0, a.c.N, 0, 0} : sequence(a.c, b);
     const int first = seq.first, T = seq.T, n = seq.n;
