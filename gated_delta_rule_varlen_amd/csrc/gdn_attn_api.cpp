@@ -56,7 +56,8 @@ gdn_status check_attn_desc(const gdn_attn_desc* d, gdn::AttnLaunch* a) {
     if (d->flags != 0) return GDN_ERR_UNSUPPORTED;
     if (std::isnan(d->scale) || std::isinf(d->scale)) return GDN_ERR_SHAPE;
     if ((d->D * dsize(d->dtype)) % 16 != 0) return GDN_ERR_ALIGN;
-    if (d->kv_rows > LLONG_MAX / 16) return GDN_ERR_OVERFLOW;
+    // an index past the last key tile still fits 32 bits (the device checks kv_len the same way)
+    if (d->kv_rows > LLONG_MAX / 16 || d->prefix_len > INT_MAX - 4096) return GDN_ERR_OVERFLOW;
     const int64_t* rows[4] = {d->k_stride, d->v_stride, d->prefix_k_stride, d->prefix_v_stride};
     for (int i = 0; i < (d->prefix_len > 0 ? 4 : 2); ++i)
         if (rows[i][0] > kMaxRowBytes / dsize(d->dtype)) return GDN_ERR_OVERFLOW;

@@ -39,6 +39,7 @@ struct Call {
         failed = true;
     }
     const at::Tensor* tensor(PyObject* o, const char* what) {
+        if (failed) return nullptr;  // nothing may be asked of Python with an error set
         if (THPVariable_Check(o)) return &THPVariable_Unpack(o);
         refuse(PyExc_TypeError, "%s must be a tensor", what);
         return nullptr;
@@ -144,7 +145,8 @@ PyObject* rope(PyObject*, PyObject* const* x, Py_ssize_t count) {
         return nullptr;
     }
     Call c;
-    const at::Tensor *q = c.queries(x[0]), *k = c.tensor(x[1], "k"), *off = c.tensor(x[3], "offsets");
+    const at::Tensor* q = c.queries(x[0]);
+    const at::Tensor *k = c.tensor(x[1], "k"), *off = c.tensor(x[3], "offsets");
     const at::Tensor* freq = c.tensor(x[4], "inv_freq");
     if (!c.failed && k->dim() != 3) c.refuse(PyExc_ValueError, "k must be [N, heads, D]");
     if (c.failed) return nullptr;
@@ -166,6 +168,7 @@ PyObject* rope(PyObject*, PyObject* const* x, Py_ssize_t count) {
     d.dtype = dtype_code(c.dtype);
     d.flags = PyObject_IsTrue(x[8]) == 1 ? GDN_ROPE_INTERLEAVED : 0;
     d.eps = (float)PyFloat_AsDouble(x[7]);
+    if (c.failed || PyErr_Occurred()) return nullptr;
     const auto qr = c.head_rows(q, H, d.q_stride, "q"), kr = c.head_rows(k, HK, d.k_stride, "k");
     const auto qo = c.head_rows(c.tensor(q_out.object, "q_out"), H, d.q_out_stride, "q_out");
     const auto ko = c.head_rows(c.tensor(k_out.object, "k_out"), HK, d.k_out_stride, "k_out");
@@ -207,7 +210,8 @@ PyObject* attention(PyObject*, PyObject* const* x, Py_ssize_t count) {
         return nullptr;
     }
     Call c;
-    const at::Tensor *q = c.queries(x[0]), *k = c.tensor(x[3], "k"), *v = c.tensor(x[4], "v"), *off = c.tensor(x[5], "offsets");
+    const at::Tensor* q = c.queries(x[0]);
+    const at::Tensor *k = c.tensor(x[3], "k"), *v = c.tensor(x[4], "v"), *off = c.tensor(x[5], "offsets");
     if (!c.failed && k->dim() != 3) c.refuse(PyExc_ValueError, "k must be [rows, heads, D]");
     if (c.failed) return nullptr;
     gdn_attn_desc d{};
@@ -227,6 +231,7 @@ PyObject* attention(PyObject*, PyObject* const* x, Py_ssize_t count) {
         d.max_q = (int32_t)std::max(-1ll, std::min<long long>(most, N));
     }
     d.scale = (float)PyFloat_AsDouble(x[9]);
+    if (c.failed || PyErr_Occurred()) return nullptr;
     const auto qr = c.head_rows(q, H, d.q_stride, "q");
     const auto kr = c.head_rows(k, HK, d.k_stride, "k"), vr = c.head_rows(v, HK, d.v_stride, "v");
     c.rows_are(kr.rows == vr.rows, "k and v must have the same rows");

@@ -429,9 +429,10 @@ gdn_status gdn_qk_norm_rope_varlen(const gdn_rope_desc *desc, const void *q, con
  *   workspace   device scratch of ws_bytes >= gdn_attention_workspace_bytes(desc)
  * Constraints: B >= 1, N >= 0, H, HK >= 1, H % HK == 0, 1 <= D <= 256, D, every stride and every base a
  * multiple of 16 bytes (GDN_ERR_ALIGN), strides not negative, rows of k and v at most 4 MiB apart
- * (GDN_ERR_OVERFLOW), max_q >= 1 unless N == 0.  scale == 0 selects 1/sqrt(D); any other value is
- * applied as given.  Malformed offsets, a sequence of more than max_q tokens and a key run outside
- * [0, kv_rows) write nothing (GDN_ERR_OFFSETS in *dev_status).
+ * (GDN_ERR_OVERFLOW), prefix_len at most 2^31 - 4097 (GDN_ERR_OVERFLOW), max_q >= 1 unless N == 0.
+ * scale == 0 selects 1/sqrt(D); any other value is applied as given.  Malformed offsets, a sequence of
+ * more than max_q tokens or 2^31 - 4097 keys and a key run outside [0, kv_rows) write nothing
+ * (GDN_ERR_OFFSETS in *dev_status).
  * ---------------------------------------------------------------------------------------------- */
 typedef struct gdn_attn_desc {
     int32_t B, N, H, HK, D;

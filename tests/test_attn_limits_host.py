@@ -1,0 +1,46 @@
+"""Refusals of lengths past what the attention's index arithmetic holds, on the host."""
+import pytest
+
+from test_attn_host import P, abi, attn_desc, attention  # noqa: F401
+
+
+@pytest.mark.parametrize("prefix_len", [2**31 - 1, 2**31 - 4096])
+def test_prefix_past_the_last_index(abi, prefix_len):  # noqa: F811
+    import ctypes
+
+    d = attn_desc(abi, prefix_len=prefix_len)
+    n = ctypes.c_size_t()
+    assert abi.lib().gdn_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)) == abi.ERR_OVERFLOW
+    assert abi.lib().gdn_attention_prefix_varlen(ctypes.byref(d), P, P, P, P, P, P, P, P, P, None, P, 1 << 40, None,
+                                                 None) == abi.ERR_OVERFLOW
+
+
+@pytest.mark.parametrize("bad", ["q", "k", "offsets"])
+def test_the_binding_takes_tensors_only(abi, bad):  # noqa: F811
+    import torch
+
+    import gated_delta_rule_varlen_amd as gdn
+
+    x = dict(q=torch.zeros(4, 2, 64), k=torch.zeros(4, 2, 64), v=torch.zeros(4, 2, 64),
+             offsets=torch.tensor([0, 4], dtype=torch.int32))
+    x[bad] = 3
+    with pytest.raises((TypeError, ValueError)):
+        gdn.attention_varlen(*x.values())
+    with pytest.raises((TypeError, ValueError)):
+        gdn.qk_norm_rope_varlen(*x.values(), inv_freq=torch.ones(32))
+    with pytest.raises((TypeError, ValueError)):
+        gdn.attention_prefix_varlen(x["q"], None, None, x["k"], x["v"], x["offsets"])
+
+
+@pytest.mark.parametrize("call", ["eps", "scale", "max_q"])
+def test_numbers_that_are_none(abi, call):  # noqa: F811
+    import torch
+
+    import gated_delta_rule_varlen_amd as gdn
+
+    x, off = torch.zeros(4, 2, 64), torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises((TypeError, ValueError)):
+        if call == "eps":
+            gdn.qk_norm_rope_varlen(x, x, x, off, inv_freq=torch.ones(32), eps="small")
+        else:
+            gdn.attention_varlen(x, x, x, off, **{call: "one"})
