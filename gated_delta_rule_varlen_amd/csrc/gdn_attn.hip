@@ -1,7 +1,7 @@
 // gdn_attn.hip -- host side of the softmax attention: which form and tile a call takes, its workspace, and
 // the kernel that joins key parts.  The tile kernels are in gdn_attn.hpp.
 //
-// Short form (max_q * G rows fit a tile of 32, 64 or 128): decode steps and short blocks, bound by the
+// Short form (max_q * G rows are 128 at most): decode steps and short blocks, bound by the
 // cache's bytes.  Long form: prompts, bound by the matrix cores.  A shared prefix is one more run of
 // keys for the long form's tiles; beside the short form, blocks of the long form run all tokens' rows over
 // the prefix, reading it once for the whole batch: in a launch of their own, or for small calls in the same one

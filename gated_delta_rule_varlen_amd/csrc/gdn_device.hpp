@@ -57,6 +57,19 @@ __device__ __forceinline__ uint16_t from_f32<BF16>(float v) { return f32_to_bf16
 template <>
 __device__ __forceinline__ uint16_t from_f32<F16>(float v) { return f32_to_f16_bits(v); }
 
+// Whether any thread of a block of NT says so; a barrier for all of them.
+template <int NT>
+__device__ __forceinline__ bool any_in_block(bool here) {
+    __shared__ int wave_says[NT / 64];
+    const bool says = __builtin_amdgcn_ballot_w64(here) != 0;
+    if ((threadIdx.x & 63) == 0) wave_says[threadIdx.x >> 6] = says;
+    __syncthreads();
+    int any = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) any |= wave_says[w];
+    return any != 0;
+}
+
 // Load one element of a runtime-typed tensor (gate inputs) as fp32.
 __device__ __forceinline__ float load_any(const void* p, int dtype, size_t i) {
     if (dtype == GDN_F32) return static_cast<const float*>(p)[i];

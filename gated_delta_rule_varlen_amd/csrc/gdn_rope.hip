@@ -1,16 +1,20 @@
 // gdn_rope.hip -- per-head RMS norm of q and k, rotary positions and the write of the new keys and
 // values into the cache, in one pass over the packed tokens (gdn_qk_norm_rope_varlen).
 //
-// One row is one head of one token.  A wave takes a token (or a quarter of its rows, where tokens are few):
-// 64 / L rows at a time, L lanes of two 16-byte pieces each.  The two pieces of a lane hold whole pairs --
-// piece j of the low and of the high half, or two neighbouring pieces when pairs are neighbours -- so a
-// rotation needs no exchange, and the sum of squares is a butterfly over L lanes.  The token's (cos, sin)
-// table is computed once, a pair a lane, and read back from LDS.  Halves that are no multiple of 16
-// bytes take the plain kernel at the end, one piece a lane and the pair's other element read by itself.
+// One row is one head of one token.  A wave takes a token (or a quarter of its passes, where tokens are few), 64 / L
+// rows a pass -- the queries, then the keys with the values behind them -- and L lanes of two 16-byte pieces a row.
+// The two pieces of a lane hold whole pairs -- piece j of the low and of the high half, or two neighbouring pieces
+// when pairs are neighbours -- so a rotation needs no exchange, and the sum of squares is a butterfly over L
+// lanes.  The token's (cos, sin) table is computed once, a pair a lane, and read back from LDS.  Halves that are no
+// multiple of 16 bytes take the plain kernel at the end, one piece a lane and the pair's other element read by itself.
 //
 // The angle is formed and reduced to a fraction of a turn in fp64 -- position * frequency passes 2^20 turns
 // on long contexts, where an fp32 product has no fraction left -- and only that fraction goes to the fp32
-// sincos.  Bound by the bytes of the rows.
+// sincos.
+//
+// Large batches are bound by the bytes of the rows (24748 tokens, 608 MB, D = 128: 128 us = 4.8 TB/s), narrow heads
+// by vector instructions (10277 tokens, D = 64: 18.7 us; 21.7 with values in passes of their own and more selects), a
+// decode step by the latencies of one launch (64 tokens: 7.6 us).
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -49,7 +53,7 @@ __device__ __forceinline__ bool rope_malformed(const RopeLaunch& a, int t0, int 
         for (int t = max(o, t0); t < min(e, t1); ++t)
             tok[t - t0] = Token{first + (t - o), a.kv_begin != nullptr ? begin + past + (t - o) : t};
     }
-    return __syncthreads_or(bad) != 0;
+    return any_in_block<NT>(bad != 0);
 }
 
 // (cos, sin) of pair j at position pos.
@@ -287,7 +291,7 @@ hipError_t launch(const RopeLaunch& a, hipStream_t stream) {
     }
     // A block's four waves share a token while that leaves CUs idle.  Else a wave takes tokens of its own: as many
     // as let all blocks run at once (10277 tokens, D = 64: 23 us at three, 28 at one), and where there are too
-    // many for that, one, which evens out the last round (24748 tokens, D = 128: 130 us at one, 141 at three).
+    // many for that, one, which evens out the last round (24748 tokens, D = 128: 128 us at one, 141 at three).
     const bool few = a.N <= 1024;
     const int wpt = few ? 4 : 1, tpb = few ? 1 : a.N <= 12288 ? 4 * ((a.N + 4095) / 4096) : 4;
     const int blocks = a.N > 0 ? (a.N + tpb - 1) / tpb : 1;
