@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void join_few_kernel(Args a, int bm, int local
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4, e = blockIdx.y * 64 + 4 * lane;
     float top = kNoMax, l = 0.0f;
     f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
     for (int p = group; p < parts.all; p += 16) parts.add(a, bm, p, e, top, l, o);
     __shared__ f32x4 xo[16][16];
     __shared__ float2 xm[16];
