@@ -13,8 +13,8 @@
 // sincos.
 //
 // Large batches are bound by the bytes of the rows (24748 tokens, 608 MB, D = 128: 128 us = 4.8 TB/s), narrow heads
-// by vector instructions (10277 tokens, D = 64: 18.7 us; 21.7 with values in passes of their own and more selects), a
-// decode step by the latencies of one launch (64 tokens: 7.6 us).
+// by vector instructions (10277 tokens, D = 64: 18.3 us; 21.7 with values in passes of their own and more selects), a
+// decode step by the latencies of one launch (64 tokens: 7.5 us).
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -290,8 +290,8 @@ hipError_t launch(const RopeLaunch& a, hipStream_t stream) {
         return hipGetLastError();
     }
     // A block's four waves share a token while that leaves CUs idle.  Else a wave takes tokens of its own: as many
-    // as let all blocks run at once (10277 tokens, D = 64: 23 us at three, 28 at one), and where there are too
-    // many for that, one, which evens out the last round (24748 tokens, D = 128: 128 us at one, 141 at three).
+    // as let all blocks run at once (10277 tokens, D = 64: 19 us at three, 24 at one), and where there are too
+    // many for that, one, which evens out the last round (24748 tokens, D = 128: 131 us at one, 137 at three).
     const bool few = a.N <= 1024;
     const int wpt = few ? 4 : 1, tpb = few ? 1 : a.N <= 12288 ? 4 * ((a.N + 4095) / 4096) : 4;
     const int blocks = a.N > 0 ? (a.N + tpb - 1) / tpb : 1;
