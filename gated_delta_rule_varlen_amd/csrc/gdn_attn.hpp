@@ -942,7 +942,8 @@ struct Block {
     }
 
     // The wave's rows again, plainly: one after the other, 64 keys at a time, over the keys p0 .. p1 - 1 of the prefix
-    // and k0 .. k1 - 1 of the run (seen0 + token of them seen).
+    // and k0 .. k1 - 1 of the run (seen0 + token of them seen).  In place of store(): where out is q, a row's queries
+    // are read before its result is written, and no other row's are written.
     __device__ __forceinline__ void redo(const To& to, const Keys& prefix, int p0, int p1, const Keys& own, int k0, int k1,
                                          int seen0) {
 #pragma unroll 1
@@ -1061,8 +1062,9 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
     if (t0 >= p1 && k0 >= k1 && stop()) return;  // no keys at all
     blk.sum_rows();
     const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? part : -1, -1};
-    blk.store(to);
-    if (blk.spoiled)
+    // one or the other: redo() reads the queries, which may be where the results go
+    if (!blk.spoiled) blk.store(to);
+    else
         blk.redo(to, prefix, t0 * C::BN, min(p1 * C::BN, a.c.prefix_len), own, k0 * C::BN, max(0, min(k1 * C::BN, n)), seen0);
 }
 
@@ -1159,8 +1161,9 @@ __device__ __forceinline__ void short_form(const Args& a, char* lds, const int w
             // a worker's slot 0: a run cut at the front; slot 1: a run that starts here and goes on in the next worker
             const typename Block<C>::To to{0, rows, run.first, run.hk, whole && a.to_sets ? a.local_set : -1,
                                            whole ? -1 : w * 2ll + (run.t0 == 0 ? 1 : 0)};
-            blk.store(to);
-            if (blk.spoiled) {
+            if (!blk.spoiled) {
+                blk.store(to);
+            } else {
                 const Keys own{static_cast<const char*>(a.c.k.p) + (run.begin * a.c.k.row + run.hk * a.c.k.head) * C::ES,
                                static_cast<const char*>(a.c.v.p) + (run.begin * a.c.v.row + run.hk * a.c.v.head) * C::ES,
                                run.n};

@@ -420,7 +420,7 @@ gdn_status gdn_qk_norm_rope_varlen(const gdn_rope_desc *desc, const void *q, con
  * to that type as operands of the second product (the sum that divides them is of the unrounded ones).
  *
  * Tensors (strides as above):
- *   q, out [N, H, D] dtype             required unless N == 0
+ *   q, out [N, H, D] dtype             required unless N == 0; out may be q itself (same strides)
  *   k, v [kv_rows, HK, D] dtype        required unless kv_rows == 0
  *   prefix_k, prefix_v [prefix_len, HK, D] dtype   required unless prefix_len == 0
  *   lse [N, H] fp32                    NULL = not produced
@@ -430,7 +430,8 @@ gdn_status gdn_qk_norm_rope_varlen(const gdn_rope_desc *desc, const void *q, con
  * Constraints: B >= 1, N >= 0, H, HK >= 1, H % HK == 0, 1 <= D <= 256, D, every stride and every base a
  * multiple of 16 bytes (GDN_ERR_ALIGN), strides not negative, rows of k and v at most 4 MiB apart
  * (GDN_ERR_OVERFLOW), prefix_len at most 2^31 - 4097 (GDN_ERR_OVERFLOW), max_q >= 1 unless N == 0.
- * scale == 0 selects 1/sqrt(D); any other value is applied as given.  Malformed offsets, a sequence of
+ * out, lse and workspace do not overlap each other or (out = q aside) the inputs, and no two elements of out
+ * share memory.  scale == 0 selects 1/sqrt(D); any other value is applied as given.  Malformed offsets, a sequence of
  * more than max_q tokens or 2^31 - 4097 keys and a key run outside [0, kv_rows) write nothing
  * (GDN_ERR_OFFSETS in *dev_status).
  * ---------------------------------------------------------------------------------------------- */

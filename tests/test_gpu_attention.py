@@ -326,3 +326,25 @@ def test_random_shapes(torch, seed):
     if sum(t for t, _ in lengths) == 0:
         lengths[0] = (1, 5)
     Case(torch, kind, HK, G, D, lengths, prefix=r.choice([0, 0, r.randrange(1, 600)]), seed=seed).check(f"random {seed}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,D,lengths,prefix", [
+    (4, 64, [(6, 40), (3, 3)], 0),       # short form, runs whole in a block and cut
+    (2, 128, [(70, 170), (200, 200)], 0),  # long form
+    (4, 256, [(40, 40)], 33),
+    (1, 64, [(5, 90), (1, 20)], 70),
+])
+@pytest.mark.parametrize("value", [0.5, float("nan"), float("inf")])
+def test_out_may_be_the_queries(torch, kind, G, D, lengths, prefix, value):
+    """out = q gives the bits of an output of its own, where masked values make rows be done again too."""
+    c = Case(torch, kind, 2, G, D, lengths, prefix=prefix, seed=8, padded_q=True)
+    for b, (_, n) in enumerate(lengths):
+        for x in c.kv:
+            x[c.begin[b] + n - 1] = value
+    want, want_lse = c.call()
+    x = c.dev()
+    out, lse = c.call(x, out=x["q"])
+    torch.cuda.synchronize()
+    assert out.data_ptr() == x["q"].data_ptr()
+    assert (bits(out) == bits(want)).all() and (bits(lse) == bits(want_lse)).all()
