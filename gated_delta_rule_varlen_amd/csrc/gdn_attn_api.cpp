@@ -69,6 +69,7 @@ gdn_status check_attn_desc(const gdn_attn_desc* d, gdn::AttnLaunch* a) {
     a->HK = d->HK;
     a->D = d->D;
     a->max_q = d->max_q < d->N ? d->max_q : d->N;
+    if (a->max_q < 0) a->max_q = 0;  // N == 0 takes any
     a->prefix_len = d->prefix_len;
     a->kv_rows = d->kv_rows;
     a->dtype = d->dtype;

@@ -348,3 +348,12 @@ def test_out_may_be_the_queries(torch, kind, G, D, lengths, prefix, value):
     torch.cuda.synchronize()
     assert out.data_ptr() == x["q"].data_ptr()
     assert (bits(out) == bits(want)).all() and (bits(lse) == bits(want_lse)).all()
+
+
+@pytest.mark.parametrize("max_q", [3, 0, -1, -1000])
+def test_calls_without_tokens_take_any_max_q(torch, max_q):
+    c = Case(torch, "bf16", 2, 2, 64, [(0, 5), (0, 0)], seed=2)
+    st = torch.ones(1, dtype=torch.int32, device="cuda")
+    c.call(dev_status=st, max_q=max_q)
+    torch.cuda.synchronize()
+    assert st.item() == 0
