@@ -44,7 +44,8 @@ gdn_status head_rows(const void* p, const int64_t stride[2], long long rows, int
 gdn_status check_sizes(int B, int N, int H, int HK, int D, int dtype) {
     if (B < 1 || N < 0 || H < 1 || HK < 1 || D < 1 || D > 256) return GDN_ERR_SHAPE;
     if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
-    if ((long long)N * H > INT_MAX || (long long)B * H > INT_MAX) return GDN_ERR_OVERFLOW;
+    // an index past the last tile of rows or tokens still fits 32 bits
+    if ((long long)N * H > INT_MAX - 4096 || (long long)B * H > INT_MAX) return GDN_ERR_OVERFLOW;
     return GDN_OK;
 }
 

@@ -1,7 +1,7 @@
 """Refusals of lengths past what the attention's index arithmetic holds, on the host."""
 import pytest
 
-from test_attn_host import P, abi, attn_desc, attention  # noqa: F401
+from test_attn_host import P, abi, attn_desc, attention, rope_desc  # noqa: F401
 
 
 @pytest.mark.parametrize("prefix_len", [2**31 - 1, 2**31 - 4096])
@@ -44,3 +44,23 @@ def test_numbers_that_are_none(abi, call):  # noqa: F811
             gdn.qk_norm_rope_varlen(x, x, x, off, inv_freq=torch.ones(32), eps="small")
         else:
             gdn.attention_varlen(x, x, x, off, **{call: "one"})
+
+
+@pytest.mark.parametrize("fields", [dict(N=2**31 - 100, H=1, HK=1), dict(N=(2**31 - 1) // 16, H=16, HK=1)])
+def test_rows_past_the_last_index(abi, fields):  # noqa: F811
+    """A row tile past the last row still has an index of 32 bits."""
+    import ctypes
+
+    n = ctypes.c_size_t()
+    for max_q in (1, fields["N"]):
+        d = attn_desc(abi, **fields, max_q=max_q)
+        assert attention(abi, d) == abi.ERR_OVERFLOW
+        assert abi.lib().gdn_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)) == abi.ERR_OVERFLOW
+
+
+@pytest.mark.parametrize("N", [2**31 - 1, 2**31 - 4096])
+def test_tokens_past_the_last_index(abi, N):  # noqa: F811
+    import ctypes
+
+    d = rope_desc(abi, N=N, H=1, HK=1, cache_rows=N)
+    assert abi.lib().gdn_qk_norm_rope_varlen(ctypes.byref(d), *([P] * 13), None, None) == abi.ERR_OVERFLOW
