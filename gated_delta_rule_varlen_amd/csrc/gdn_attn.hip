@@ -100,10 +100,11 @@ __global__ __launch_bounds__(256) void join_few_kernel(Args a, int bm, int local
 }
 
 // Many rows: `lanes` (16, 32 or 64) of a wave hold a row's elements, its other groups of so many share the parts.
+// A block takes four rows; the grid's second axis is there for more rows than one axis counts threads for.
 template <typename T, int LANES>
 __global__ __launch_bounds__(256) void join_rows_kernel(Args a, int bm, int local_set) {
     const int status = *a.status;
-    const long long row = blockIdx.x * 4ll + (threadIdx.x >> 6);
+    const long long row = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
     if (row >= a.set_rows) return;
     const int t = (int)(row / a.c.H), h = (int)(row - (long long)t * a.c.H);
     Parts parts;
@@ -143,7 +144,7 @@ struct Plan {
     Args a;
     bool is_short, join, both;
     int dp, wr, bm;
-    int lds, long_lds;
+    int lds, long_lds, threads, long_threads;
     long long blocks;
     size_t bytes;
 };
@@ -173,6 +174,7 @@ Plan plan(const AttnLaunch& c) {
     const long double q_span = ((long double)c.max_q * c.q.row + (long double)a.G * c.q.head) * es;
     p.is_short = rows <= kShortRows && s.ring + q_lds <= kMaxLds && q_span < kOutside;
     p.long_lds = whole.ring;
+    p.threads = p.long_threads = whole.threads;
     // key parts of the long form: enough blocks for two a CU, each of 128 keys at least
     auto parts = [&](long long tiles, long long keys) {
         const long long want = (2 * kCUs + tiles - 1) / std::max(1ll, tiles), most = keys / 128;
@@ -182,6 +184,7 @@ Plan plan(const AttnLaunch& c) {
     bool by_rows = true;
     if (p.is_short) {
         p.bm = s.bm;
+        p.threads = s.threads;
         p.lds = (int)(s.ring + q_lds);
         if (c.prefix_len > 0 && c.N > 0) {
             const long long tiles = (all_rows + whole.bm - 1) / whole.bm;
@@ -201,6 +204,7 @@ Plan plan(const AttnLaunch& c) {
         p.both = a.prefix_blocks > 0 && a.prefix_blocks + a.workers <= 2 * kCUs && p.wr <= 4 && joint(whole.ring, p.lds);
         if (p.both) {
             p.lds = std::max(p.lds, whole.ring);
+            p.threads = p.long_threads;
             p.blocks = ((a.prefix_blocks + kCUs - 1) / kCUs + (a.workers + kCUs - 1) / kCUs) * kCUs;  // whole turns
         }
         p.join = c.N > 0 && (a.workers > 1 || a.sets > 0);
@@ -246,7 +250,7 @@ Plan plan(const AttnLaunch& c) {
 template <typename T>
 hipError_t launch(const AttnLaunch& c, hipStream_t stream) {
     Plan p = plan<T>(c);
-    if (p.blocks > kMaxBlocks || p.a.prefix_blocks > kMaxBlocks || (p.join && p.a.set_rows > kMaxBlocks))
+    if (p.blocks * p.threads > kMaxThreads || p.a.prefix_blocks * p.long_threads > kMaxThreads)
         return hipErrorInvalidConfiguration;
     hipError_t e;
     if (p.is_short) {
@@ -263,12 +267,13 @@ hipError_t launch(const AttnLaunch& c, hipStream_t stream) {
     }
     if (e != hipSuccess || !p.join) return e;
     const int local = p.is_short && p.a.sets > 0 ? p.a.local_set : -1;
-    const unsigned rows = (unsigned)p.a.set_rows, fours = (unsigned)((p.a.set_rows + 3) / 4);
+    const long long blocks = (p.a.set_rows + 3) / 4, most_x = kMaxThreads / 256;
+    const dim3 fours((unsigned)std::min(blocks, most_x), (unsigned)((blocks + most_x - 1) / most_x));
     if (p.a.cut != nullptr) {
         const unsigned most = (unsigned)(c.max_q * p.a.G + 3) / 4;
         join_cut_kernel<T><<<dim3((unsigned)p.a.workers, most), 256, 0, stream>>>(p.a, p.bm);
     } else if (few_rows(p.a)) {
-        join_few_kernel<T><<<dim3(rows, (c.D + 63) / 64), 256, 0, stream>>>(p.a, p.bm, local);
+        join_few_kernel<T><<<dim3((unsigned)p.a.set_rows, (c.D + 63) / 64), 256, 0, stream>>>(p.a, p.bm, local);
     } else if (c.D <= 64) {
         join_rows_kernel<T, 16><<<fours, 256, 0, stream>>>(p.a, p.bm, local);
     } else if (c.D <= 128) {

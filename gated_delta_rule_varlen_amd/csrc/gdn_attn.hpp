@@ -1252,13 +1252,13 @@ struct Long {
     using C = Cfg<T, 32, DP, RB == 512 && sizeof(typename T::storage) == 2 ? 8 : 4, RB <= 256 ? 2 : 1, 2, RB <= 512 ? 2 : 1>;
 };
 
-// What the host needs to know of a configuration: tile sizes, bytes of the ring and of a row in LDS.
+// What the host needs to know of a configuration: tile sizes, bytes of the ring and of a row in LDS, threads.
 struct Shape {
-    int bm, bn, ring, row;
+    int bm, bn, ring, row, threads;
 };
 template <typename C>
 constexpr Shape shape_of() {
-    return Shape{C::BM, C::BN, C::LDS, C::RB};
+    return Shape{C::BM, C::BN, C::LDS, C::RB, C::NT};
 }
 
 constexpr int kMaxLds = 159 * 1024;  // of the 160 KB, less the kernels' own few words
@@ -1298,7 +1298,7 @@ hipError_t start_both(const Args& a, int dp, int wr, long long blocks, int lds, 
 template <typename F>
 hipError_t start_kernel(F* f, std::atomic<uint64_t>& asked, const Args& a, long long blocks, int threads, int lds,
                         hipStream_t stream) {
-    if (blocks > kMaxBlocks || lds > kMaxLds) return hipErrorInvalidConfiguration;
+    if (blocks * threads > kMaxThreads || lds > kMaxLds) return hipErrorInvalidConfiguration;
     if (lds > 64 * 1024) {
         int dev = 0;
         hipError_t e = hipGetDevice(&dev);

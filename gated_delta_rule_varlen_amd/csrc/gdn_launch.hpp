@@ -168,5 +168,6 @@ constexpr int kChunkTokens = 64;
 
 // Limits of the launch grids (checked by the entry points before launching).
 constexpr long long kMaxBlocks = (1ll << 31) - 1;
+constexpr long long kMaxThreads = (1ll << 32) - 1;  // of a grid: a launch counts them in 32 bits
 
 }  // namespace gdn

@@ -286,6 +286,7 @@ hipError_t launch(const RopeLaunch& a, hipStream_t stream) {
     if (!a.interleaved && a.rot / 2 % VEC != 0) {
         const int tpb = a.N > 1024 ? 4 : 1;
         const int blocks = a.N > 0 ? (a.N + tpb - 1) / tpb : 1;
+        if ((long long)blocks * NT > kMaxThreads) return hipErrorInvalidConfiguration;
         rope_kernel<T><<<blocks, NT, 0, stream>>>(a, tpb, log2_pieces);
         return hipGetLastError();
     }
@@ -295,6 +296,7 @@ hipError_t launch(const RopeLaunch& a, hipStream_t stream) {
     const bool few = a.N <= 1024;
     const int wpt = few ? 4 : 1, tpb = few ? 1 : a.N <= 12288 ? 4 * ((a.N + 4095) / 4096) : 4;
     const int blocks = a.N > 0 ? (a.N + tpb - 1) / tpb : 1;
+    if ((long long)blocks * NT > kMaxThreads) return hipErrorInvalidConfiguration;
     auto go = [&](auto kernel) {
         kernel<<<blocks, NT, 0, stream>>>(a, tpb, wpt);
         return hipGetLastError();

@@ -378,8 +378,9 @@ gdn_status gdn_scan_workspace_bytes(const gdn_scan_desc *desc, size_t *bytes);
  *   past, positions [B] int32                NULL = zeros; positions NULL = past
  *   kv_begin  [B] int64                      NULL = rows are token indices (past moves positions only)
  * Constraints: B >= 1, N >= 0, H, HK >= 1, 1 <= D <= 256, 0 <= rot <= D even, D, every stride and
- * every base a multiple of 16 bytes (GDN_ERR_ALIGN), strides not negative, N*H at most 2^31 - 4097 and
- * N*HK and B*H at most 2^31 - 1 (GDN_ERR_OVERFLOW).  q_out, k_out and v_out do not overlap each other or (q_out = q aside) the inputs, and no two tokens name one row.
+ * every base a multiple of 16 bytes (GDN_ERR_ALIGN), strides not negative, N at most 2^26 - 4, N*H at
+ * most 2^31 - 4097, N*HK and B*H at most 2^31 - 1 (GDN_ERR_OVERFLOW).  q_out, k_out and v_out do not
+ * overlap each other or (q_out = q aside) the inputs, and no two tokens name one row.
  * Malformed offsets, and rows outside [0, cache_rows) of a sequence with tokens, write nothing
  * (GDN_ERR_OFFSETS in *dev_status).
  * ---------------------------------------------------------------------------------------------- */
@@ -430,7 +431,8 @@ gdn_status gdn_qk_norm_rope_varlen(const gdn_rope_desc *desc, const void *q, con
  * Constraints: B >= 1, N >= 0, H, HK >= 1, H % HK == 0, 1 <= D <= 256, D, every stride and every base a
  * multiple of 16 bytes (GDN_ERR_ALIGN), strides not negative, rows of k and v at most 4 MiB apart
  * (GDN_ERR_OVERFLOW), N*H and prefix_len at most 2^31 - 4097 and B*H at most 2^31 - 1 (GDN_ERR_OVERFLOW),
- * max_q >= 1 unless N == 0.
+ * max_q >= 1 unless N == 0.  A call with more than 128 rows max_q*H/HK a sequence, or a prefix, may also be refused
+ * (GDN_ERR_OVERFLOW) where its row tiles pass one launch, which takes N*H >= 2^30 or B*HK >= 2^22.
  * out, lse and workspace do not overlap each other or (out = q aside) the inputs, and no two elements of out
  * share memory.  scale == 0 selects 1/sqrt(D); any other value is applied as given.  Malformed offsets, a sequence of
  * more than max_q tokens or 2^31 - 4097 keys and a key run outside [0, kv_rows) write nothing

@@ -64,3 +64,17 @@ def test_tokens_past_the_last_index(abi, N):  # noqa: F811
 
     d = rope_desc(abi, N=N, H=1, HK=1, cache_rows=N)
     assert abi.lib().gdn_qk_norm_rope_varlen(ctypes.byref(d), *([P] * 13), None, None) == abi.ERR_OVERFLOW
+
+
+@pytest.mark.parametrize("fields", [dict(B=2**24, N=2**10, max_q=2**10), dict(B=2**27, N=2**7, max_q=2**7)])
+def test_more_row_tiles_than_a_launch_holds(abi, fields):  # noqa: F811
+    assert attention(abi, attn_desc(abi, **fields)) == abi.ERR_OVERFLOW
+
+
+@pytest.mark.parametrize("N", [2**26, 2**30])
+def test_more_tokens_than_a_launch_holds(abi, N):  # noqa: F811
+    import ctypes
+
+    for rot in (64, 50):
+        d = rope_desc(abi, N=N, H=1, HK=1, cache_rows=N, rot=rot)
+        assert abi.lib().gdn_qk_norm_rope_varlen(ctypes.byref(d), *([P] * 13), None, None) == abi.ERR_OVERFLOW

@@ -357,3 +357,24 @@ def test_calls_without_tokens_take_any_max_q(torch, max_q):
     c.call(dev_status=st, max_q=max_q)
     torch.cuda.synchronize()
     assert st.item() == 0
+
+
+def test_more_rows_behind_a_prefix_than_one_axis_of_a_grid(torch):
+    """2^26 rows and more joined with a prefix; sequences read the same rows of the cache."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    H, D, T, n, P = 32, 8, 128, 130, 40
+    B = (1 << 26) // (H * T) + 1
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.bfloat16)
+    q, k, v, pk, pv = normal(B * T, H, D), normal(n, H, D), normal(n, H, D), normal(P, H, D), normal(P, H, D)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out, lse = gdn.attention_prefix_varlen(q, pk, pv, k, v, torch.arange(B + 1, device="cuda", dtype=torch.int32) * T,
+                                           kv_len=i32([n] * B), kv_begin=torch.zeros(B, dtype=torch.int64, device="cuda"),
+                                           max_q=T, return_lse=True)
+    for b in (0, B // 2, B - 1):
+        at = slice(b * T, (b + 1) * T)
+        o, l, ot, lt = attention_ref(q[at].cpu(), k.cpu(), v.cpu(), [T], [0], [n], kind="bf16", prefix_k=pk.cpu(),
+                                     prefix_v=pv.cpu())
+        assert_within(out[at], o, ot, f"sequence {b} out")
+        assert_within(lse[at], l, lt, f"sequence {b} lse")
