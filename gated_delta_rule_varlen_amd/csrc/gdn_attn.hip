@@ -161,7 +161,6 @@ Plan plan(const AttnLaunch& c) {
     a.s2 = fabsf(c.scale) * kLog2e;
     a.negate = c.scale < 0.0f;
     a.splits = 1;
-    a.chunk = 1;
     a.set_rows = (long long)c.N * c.H;
     p.dp = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
     const long long rows = (long long)c.max_q * a.G, es = sizeof(typename T::storage);
@@ -210,14 +209,13 @@ Plan plan(const AttnLaunch& c) {
         p.join = c.N > 0 && (a.workers > 1 || a.sets > 0);
         by_rows = a.sets > 0 || few_rows(a);
     } else {
-        const long long most = (rows + whole.bm - 1) / whole.bm;  // tiles of the longest sequence
-        a.splits = parts(std::min(most * c.B, all_rows / whole.bm + c.B) * c.HK, c.kv_rows + c.prefix_len);
-        // 16 tiles of a sequence follow one another and find its keys in the L2 (prefill batch of 24748 tokens: 670 us
-        // against 730 at one).  More sequences than the kernel sorts by length do so only where blocks come in
-        // many rounds; in few the even end counts, which one tile of each, the last ones first, gives.
-        const long long real = std::min(most * c.B, all_rows / whole.bm + c.B) * c.HK * a.splits;
-        a.chunk = c.B <= 64 || real >= 8 * 2 * kCUs ? 16 : 1;
-        p.blocks = (most + a.chunk - 1) / a.chunk * a.chunk * c.B * c.HK * a.splits;
+        // One block for every slot that a row tile can have, however long max_q says that one sequence may be: with
+        // blocks for each sequence's longest, longest first, eight prompts of 24748 tokens took 667 us instead of 658, 64
+        // fp32 prompts of up to 300 tokens 317 instead of 323, one prompt of 8192 tokens among 63 of up to 200 1250
+        // instead of 537, and max_q = N for the eight prompts 756 instead of 659.
+        const long long most = (rows + whole.bm - 1) / whole.bm, slots = all_rows / whole.bm + c.B;
+        a.splits = parts(std::min(most * c.B, slots) * c.HK, c.kv_rows + c.prefix_len);
+        p.blocks = slots * c.HK * a.splits;
         if (a.splits > 1) {
             a.sets = a.splits;
             a.to_sets = true;

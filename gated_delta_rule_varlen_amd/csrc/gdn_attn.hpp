@@ -57,7 +57,6 @@ struct Args {
     float s2;       // |scale| * log2(e); the sign goes to the queries
     bool negate;
     int splits;     // key parts of the long form
-    int chunk;      // row tiles of a sequence that follow one another
     int workers;    // blocks of the short form
     bool to_sets;   // results go to the workspace, for the joining kernel
     int local_set;  // the set of a sequence's own keys, behind the prefix's key parts
@@ -204,16 +203,26 @@ __device__ __forceinline__ Sequence sequence(const AttnLaunch& c, int i) {
     return s;
 }
 
-// The sequence of rank `place` by its keys, of 2 to 64: a sequence a lane.
-__device__ __forceinline__ int by_length(const AttnLaunch& c, int place) {
-    const int lane = threadIdx.x & 63, i = min(lane, c.B - 1);
-    const int n = c.kv_len != nullptr ? c.kv_len[i] : c.offsets[i + 1] - c.offsets[i];
-    int rank = 0;
-    for (int j = 0; j < c.B; ++j) {
-        const int other = __builtin_amdgcn_readlane(n, j);
-        rank += (other > n) | (other == n && j < lane);
+// Row tiles end to end without a sum over the sequences: those of sequence b start at slot offsets[b] * G / BM + b.
+// ceil(T * G / BM) is at most one more than the difference of two neighbours' quotients, so the next sequence's slots
+// begin behind them, and N * G / BM + B slots hold all.
+template <int BM>
+__device__ __forceinline__ unsigned slot_of(const AttnLaunch& c, int G, int offset, int b) {
+    return (unsigned)(min(max(offset, 0), c.N) * G) / BM + (unsigned)b;
+}
+// The last sequence that starts at `slot` or before it: 64 candidates a step, a sequence of the call whatever its
+// offsets hold.
+template <int BM>
+__device__ __forceinline__ int sequence_at(const AttnLaunch& c, int G, unsigned slot) {
+    int lo = 0, hi = c.B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo - 1) / 64 + 1, i = lo + min((int)(threadIdx.x & 63), (hi - lo - 1) / step) * step;
+        const uint64_t here = __builtin_amdgcn_ballot_w64(slot_of<BM>(c, G, c.offsets[i], i) <= slot);
+        const int at = here == 0 ? 0 : 63 - __builtin_clzll(here);
+        lo = uniform(lo + min(at, (hi - lo - 1) / step) * step);
+        hi = min(hi, lo + step);
     }
-    return uniform(__ffsll((unsigned long long)__builtin_amdgcn_ballot_w64(lane < c.B && rank == place)) - 1);
+    return lo;
 }
 
 // Sequence i as the arrays have it, and whether it is malformed.
@@ -1004,22 +1013,19 @@ __device__ __forceinline__ void report(const Args& a, bool malformed, unsigned b
     }
 }
 
-// The long form: one block per key head, sequence, tile of BM rows and key part; the last tiles of a
-// sequence (which see most keys) come first, `chunk` of them before the next sequence's, and up to 64 sequences go
-// by their keys, the longest first, so that the last blocks are short ones.  Key heads are the fastest index, so
-// the blocks that read one head's keys at a time lie on few XCDs.  With prefix_rows the rows
+// The long form: one block per key head, key part and tile of BM rows.  The row tiles of all sequences lie end to
+// end (a few blocks find none and end), those of a sequence from its last, which sees most keys.  Key heads are the
+// fastest index, so the blocks that read one head's keys at a time lie on few XCDs.  With prefix_rows the rows
 // are all tokens' and the keys the prefix alone.
 template <typename C>
 __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsigned block, const bool prefix_rows) {
     unsigned x = block;
     const int hk = x % a.c.HK;
     x /= a.c.HK;
-    const int lo = x % a.chunk;
-    x /= a.chunk;
-    const int B = prefix_rows ? 1 : a.c.B, place = x % B, b = B > 1 && B <= 64 ? by_length(a.c, place) : place;
-    x /= B;
-    // a chunk's order differs by sequence: else an XCD (every eighth block) would get the same few tiles of all
-    const int part = x % a.splits, back = x / a.splits * a.chunk + (a.chunk > 1 ? lo ^ (place & 7) : lo);
+    const int part = x % a.splits;
+    x /= a.splits;
+    const int b = prefix_rows ? 0 : sequence_at<C::BM>(a.c, a.G, x);
+    const unsigned back = prefix_rows ? x : x - slot_of<C::BM>(a.c, a.G, uniform(entry(a.c.offsets, b)), b);  // tiles behind
     // Queries and the first keys are on their way while the call is checked.
     const Sequence seq = prefix_rows ? Sequence{0, a.c.N, 0, 0} : sequence(a.c, b);
     const int first = seq.first, T = seq.T, n = seq.n;
@@ -1030,11 +1036,12 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
         if (malformed) wait_and_meet<0>();
         return malformed;
     };
-    const int rows = T * a.G, tiles = (rows + C::BM - 1) / C::BM, row0 = (tiles - 1 - back) * C::BM;
-    if (row0 < 0 || rows == 0) {
+    const int rows = T * a.G, tiles = (rows + C::BM - 1) / C::BM;
+    if (back >= (unsigned)tiles) {
         if (block == 0) stop();  // the block that reports
         return;
     }
+    const int row0 = (tiles - 1 - (int)back) * C::BM;
     const int seen0 = n - T + 1;
     const int last_token = min(row0 + C::BM, rows) - 1;
     const int reach = uniform(max(0, min(n, seen0 + last_token / a.G)));  // keys the last row sees

@@ -378,3 +378,50 @@ def test_more_rows_behind_a_prefix_than_one_axis_of_a_grid(torch):
                                      prefix_v=pv.cpu())
         assert_within(out[at], o, ot, f"sequence {b} out")
         assert_within(lse[at], l, lt, f"sequence {b} lse")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("HK,G,D,lengths,prefix", [
+    (2, 4, 64, [(i % 5 != 2, 1 + (37 * i) % 90) for i in range(300)], 0),  # single tokens
+    (1, 3, 128, [(700, 900)] + [(i % 4, 3 + i % 60) for i in range(70)], 0),  # a token's rows in two tiles
+    (1, 8, 256, [(i % 6, 2 + i % 7) for i in range(200)] + [(0, 0), (400, 450)], 77),
+    (1, 2, 64, [(i % 3, 1 + i % 4) for i in range(5000)], 0),  # more than 64 * 64 sequences
+])
+def test_default_max_q(torch, kind, HK, G, D, lengths, prefix):
+    c = Case(torch, kind, HK, G, D, lengths, prefix=prefix, seed=D)
+    out, lse = c.call(max_q=None)
+    o, l, ot, lt = c.ref()
+    assert_within(out, o, ot, "default max_q out")
+    assert_within(lse, l, lt, "default max_q lse")
+
+
+def test_default_max_q_of_a_large_batch(torch):
+    """8192 single tokens of 32 heads: as many row tiles for each as for a sequence of all tokens would pass the
+    threads of one launch."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    B, H, HK, D = 8192, 32, 8, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()
+    n = 1 + torch.arange(B) % 3
+    begin = torch.nn.functional.pad(n.cumsum(0), (1, 0))
+    q, k, v = normal(B, H, D), normal(int(begin[-1]), HK, D), normal(int(begin[-1]), HK, D)
+    out, lse = gdn.attention_varlen(q, k, v, torch.arange(B + 1, dtype=torch.int32).cuda(), kv_len=n.int().cuda(),
+                                    kv_begin=begin[:-1].cuda(), return_lse=True, out=sentinel((B, H, D), "bf16"))
+    pick = [0, 1, 2, 63, 64, 127, 128, 4095, 4096, B - 2, B - 1]
+    o, l, ot, lt = attention_ref(q[pick].cpu(), k.cpu(), v.cpu(), [1] * len(pick), begin[pick].tolist(), n[pick].tolist(),
+                                 kind="bf16")
+    assert_within(out[pick], o, ot, "large batch out")
+    assert_within(lse[pick], l, lt, "large batch lse")
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+    one = n == 1  # a token that sees one key has its value
+    want = v[begin[:-1][one].cuda()].repeat_interleave(H // HK, dim=1)
+    assert (bits(out[one.cuda()]) == bits(want)).all()
+
+
+@pytest.mark.parametrize("what", ["ok", "start", "end", "falling", "far", "length"])
+def test_default_max_q_malformed(torch, what):
+    c = Case(torch, "bf16", 2, 4, 64, [(1 + i % 3, 20 + i) for i in range(150)], seed=2)
+    spoil = dict(ok=[], start=[("offsets", 0, 1)], end=[("offsets", 150, c.N + 1)], falling=[("offsets", 70, 1 << 30)],
+                 far=[("offsets", 64, -(1 << 31))], length=[("kv_len", 0, -1)])[what]
+    _expect_untouched(torch, c, status=0 if what == "ok" else -9, spoil=spoil, max_q=None)
