@@ -56,7 +56,7 @@ struct Parts {
             }
         }
         // a cut run left its own set (the last) unused; a run that was not, without sets, is written already
-        all = pieces + a.sets - (worker >= 0 && local_set >= 0 ? 1 : 0);
+        all = pieces + (a.live != nullptr ? a.live[t] : a.sets) - (worker >= 0 && local_set >= 0 ? 1 : 0);
     }
     // Adds part p to the running (top, l, o) of elements e .. e + 3.
     __device__ __forceinline__ void add(const Args& a, int bm, int p, int e, float& top, float& l, f32x4& o) const {
@@ -174,9 +174,10 @@ Plan plan(const AttnLaunch& c) {
     p.is_short = rows <= kShortRows && s.ring + q_lds <= kMaxLds && q_span < kOutside;
     p.long_lds = whole.ring;
     p.threads = p.long_threads = whole.threads;
-    // key parts of the long form: enough blocks for two a CU, each of 128 keys at least
+    // Key parts of the long form: enough blocks for two a CU, each of kPartKeys keys at least.  The sequences' own
+    // lengths are on the device: there a sequence takes as many of the parts as its keys fill.
     auto parts = [&](long long tiles, long long keys) {
-        const long long want = (2 * kCUs + tiles - 1) / std::max(1ll, tiles), most = keys / 128;
+        const long long want = (2 * kCUs + tiles - 1) / std::max(1ll, tiles), most = keys / kPartKeys;
         return (int)std::max(1ll, std::min(std::min(want, most), 64ll));
     };
     const long long N = c.N, all_rows = N * a.G;
@@ -239,6 +240,7 @@ Plan plan(const AttnLaunch& c) {
         if (a.sets > 0) {
             a.set_ml = reinterpret_cast<float2*>(take((size_t)a.sets * a.set_rows * 8));
             a.set_o = reinterpret_cast<float*>(take((size_t)a.sets * a.set_rows * c.D * 4));
+            if (!p.is_short) a.live = reinterpret_cast<int*>(take(N * 4));
         }
     }
     p.bytes = at;

@@ -47,6 +47,7 @@ typedef short v4i16 __attribute__((ext_vector_type(4)));
 constexpr int kRsrc = 0x00020000;     // raw buffer, range checked
 constexpr int kOutside = 0x40000000;  // a byte offset past every tile's range
 constexpr int kMostKeys = INT_MAX - 4096;  // of a sequence: an index past its last tile still fits
+constexpr int kPartKeys = 128;  // of a key part of the long form at least
 constexpr float kNoMax = -3.0e38f;    // running maximum before the first key: below every score
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -56,7 +57,7 @@ struct Args {
     int G;          // heads per key head
     float s2;       // |scale| * log2(e); the sign goes to the queries
     bool negate;
-    int splits;     // key parts of the long form
+    int splits;     // key parts of the long form at most: a sequence has one for every kPartKeys of its keys
     int workers;    // blocks of the short form
     bool to_sets;   // results go to the workspace, for the joining kernel
     int local_set;  // the set of a sequence's own keys, behind the prefix's key parts
@@ -71,6 +72,7 @@ struct Args {
     float2* set_ml;    // [sets][N*H]
     int sets;
     long long set_rows;  // N*H
+    int* live;         // [N]: sets that the long form wrote of a token's rows
 };
 
 // Accumulators of an M x M tile, and one step of its product: 16 bytes of each operand's rows a lane.
@@ -1022,8 +1024,16 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
     unsigned x = block;
     const int hk = x % a.c.HK;
     x /= a.c.HK;
-    const int part = x % a.splits;
-    x /= a.splits;
+    const unsigned slots = prefix_rows ? (a.c.N * a.G + C::BM - 1) / C::BM : a.c.N * a.G / C::BM + a.c.B;
+    // Four parts of a tile follow one another, so that blocks go from the longest down; parts that short sequences do
+    // not have come last (512 tokens in a cache of 2^20 rows, 16 parts: 34 us, with all of a tile in a row 49).
+    int part = 0;
+    if (a.splits > 1) {
+        const int four = x / (4 * slots), of = min(4, a.splits - 4 * four);
+        x -= four * 4 * slots;
+        part = 4 * four + x % of;
+        x /= of;
+    }
     const int b = prefix_rows ? 0 : sequence_at<C::BM>(a.c, a.G, x);
     const unsigned back = prefix_rows ? x : x - slot_of<C::BM>(a.c, a.G, uniform(entry(a.c.offsets, b)), b);  // tiles behind
     // Queries and the first keys are on their way while the call is checked.
@@ -1037,7 +1047,8 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
         return malformed;
     };
     const int rows = T * a.G, tiles = (rows + C::BM - 1) / C::BM;
-    if (back >= (unsigned)tiles) {
+    const int parts = min(a.splits, max(1, (int)(((unsigned)a.c.prefix_len + (unsigned)n) / kPartKeys)));
+    if (back >= (unsigned)tiles || part >= parts) {
         if (block == 0) stop();  // the block that reports
         return;
     }
@@ -1046,7 +1057,7 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
     const int last_token = min(row0 + C::BM, rows) - 1;
     const int reach = uniform(max(0, min(n, seen0 + last_token / a.G)));  // keys the last row sees
     const int ptiles = (a.c.prefix_len + C::BN - 1) / C::BN, all = ptiles + (reach + C::BN - 1) / C::BN;
-    const int t0 = uniform((int)((long long)all * part / a.splits)), t1 = uniform((int)((long long)all * (part + 1) / a.splits));
+    const int t0 = uniform((int)((long long)all * part / parts)), t1 = uniform((int)((long long)all * (part + 1) / parts));
 
     Block<C> blk(a, lds);
     blk.load_rows(row0, rows, first, hk);
@@ -1067,6 +1078,8 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
         if (!blk.run(own, k0, k1, full, [&] { return t0 < p1 ? false : stop(); })) return;
     }
     if (t0 >= p1 && k0 >= k1 && stop()) return;  // no keys at all
+    if (a.live != nullptr && part == 0 && hk == 0)
+        for (int i = row0 / a.G + (int)threadIdx.x; i <= last_token / a.G; i += C::NT) a.live[first + i] = parts;
     blk.sum_rows();
     const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? part : -1, -1};
     // one or the other: redo() reads the queries, which may be where the results go

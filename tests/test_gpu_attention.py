@@ -425,3 +425,34 @@ def test_default_max_q_malformed(torch, what):
     spoil = dict(ok=[], start=[("offsets", 0, 1)], end=[("offsets", 150, c.N + 1)], falling=[("offsets", 70, 1 << 30)],
                  far=[("offsets", 64, -(1 << 31))], length=[("kv_len", 0, -1)])[what]
     _expect_untouched(torch, c, status=0 if what == "ok" else -9, spoil=spoil, max_q=None)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("HK,G,lengths,prefix", [
+    (1, 8, [(300, 300)], 0),
+    (2, 3, [(90, 90), (0, 5), (130, 400), (3, 0)], 0),  # a token's rows in two tiles
+    (1, 4, [(150, 150), (60, 20)], 500),
+])
+def test_a_large_cache_is_not_cut_finer(torch, kind, HK, G, lengths, prefix):
+    """Key parts are of the sequences' own keys, however many rows the cache has: no part of less than 128 keys
+    is written to the workspace."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    D = 64
+    c = Case(torch, kind, HK, G, D, lengths, prefix=prefix, seed=21)
+    x = c.dev()
+    for n in ("k", "v"):
+        large = torch.full((1 << 17, HK, D), float("nan"), dtype=DT[kind], device="cuda")
+        large[:len(x[n])] = x[n]
+        x[n] = large
+    need = gdn.attention_workspace_bytes(x["q"], len(lengths), HK=HK, max_q=x["max_q"], kv_rows=1 << 17, prefix_len=prefix)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = c.call(x, workspace=ws)
+    torch.cuda.synchronize()
+    parts = [max(1, (prefix + n) // 128) for _, n in lengths]
+    most = sum(p * t for p, (t, _) in zip(parts, lengths)) * c.H * (D + 2) + c.N + 1
+    written = (ws[:need // 4 * 4].view(torch.int32) != torch.tensor(0xA5A5A5A5 - (1 << 32), dtype=torch.int32, device="cuda")).sum().item()
+    o, l, ot, lt = c.ref()
+    assert_within(out, o, ot, "large cache out")
+    assert_within(lse, l, lt, "large cache lse")
+    assert written <= most, (written, most)
