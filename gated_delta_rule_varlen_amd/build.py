@@ -68,13 +68,13 @@ def _build_bind() -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link libgdn.so, and the binding beside it; returns the library path."""
+    """Compile every HIP source and link libgdn.so, and the binding beside it; returns the library path.  Where the
+    binding does not compile libgdn.so is linked all the same, and then the error is raised."""
     os.makedirs(BUILD, exist_ok=True)
     jobs = min(len(SOURCES), int(os.environ.get("MAX_JOBS", os.cpu_count() or 4)))
     with ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
         bind = ex.submit(_build_bind)
         objs = list(ex.map(_compile, SOURCES))
-        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -82,7 +82,8 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}", flush=True)
+    bind.result()  # only now: the library needs neither a host compiler nor torch's headers
     return LIB
 
 

@@ -320,3 +320,26 @@ def test_scan_noalloc_host_validation(abi, fields, kw, want):
     st = abi.lib().gdn_scan_varlen_noalloc(ctypes.byref(d), a["qkv"], None, None, a["a"], None, a["alog"], a["dtb"],
                                            None, a["out"], None, a["off"], None, None, None)
     assert st == getattr(abi, want)
+
+
+def test_the_library_is_linked_where_the_binding_does_not_compile(monkeypatch, tmp_path):
+    """A host without g++ or torch's headers still gets libgdn.so, and is told about the binding."""
+    from gated_delta_rule_varlen_amd import build
+
+    linked = []
+
+    def no_compiler():
+        raise RuntimeError("no C++ compiler")
+
+    def link(cmd, **kw):
+        linked.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return type("Done", (), dict(returncode=0, stderr=""))
+
+    monkeypatch.setattr(build, "_build_bind", no_compiler)
+    monkeypatch.setattr(build, "_compile", lambda src: src + ".o")
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libgdn.so"))
+    monkeypatch.setattr(build.subprocess, "run", link)
+    with pytest.raises(RuntimeError, match="no C.. compiler"):
+        build.build()
+    assert len(linked) == 1 and (tmp_path / "libgdn.so").exists()
