@@ -166,7 +166,7 @@ Plan plan(const AttnLaunch& c) {
     const long long rows = (long long)c.max_q * a.G, es = sizeof(typename T::storage);
     p.wr = rows <= 64 ? (int)(rows + 15) / 16 : 8;
     if (p.wr < 1) p.wr = 1;
-    const Shape s = with_short<T>(p.dp, p.wr, [](auto x) { return shape_of<typename decltype(x)::C>(); });
+    const Shape s = with_short<T>(p.dp, p.wr, Shape{0, 0, kMaxLds + 1, 0, 0}, [](auto x) { return shape_of<typename decltype(x)::C>(); });
     const Shape whole = with_long<T>(p.dp, [](auto x) { return shape_of<typename decltype(x)::C>(); });
     // the short form's queries lie in LDS beside the ring, and a run's span a 32-bit range
     const long long q_lds = (rows + 7) / 8 * 8 * s.row;
@@ -194,7 +194,7 @@ Plan plan(const AttnLaunch& c) {
             a.to_sets = true;
             a.local_set = a.splits;
         }
-        const int per_cu = std::min(8, (int)(160 * 1024 / (p.lds + 256)));
+        const int per_cu = std::min(8, kCULds / ((p.lds + 1279) / 1280 * 1280));  // LDS is handed out in 1280 bytes
         const long long units = c.HK * (c.kv_rows / s.bn + c.B);  // fewer blocks than that have work, bar overlapping runs
         a.workers = (int)std::max(1ll, std::min((long long)kCUs * per_cu, units));
         p.blocks = a.workers;

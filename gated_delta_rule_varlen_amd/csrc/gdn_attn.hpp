@@ -1252,16 +1252,30 @@ __global__ __launch_bounds__(CL::NT, CL::WAVES) void both_kernel(Args a) {
     }
 }
 
+constexpr int kCULds = 160 * 1024;   // of a CU
+constexpr int kMaxLds = 159 * 1024;  // of a block: less the kernels' own few words
+
 // ---- which tile for which call -------------------------------------------------------------------
 // Head widths are compiled for 64, 128 and 256.
 //
-// Short form, 16 x 16 tiles, one wave for every 16 rows (1, 2, 3, 4 or 8 waves): what counts is bytes on their way,
-// 64 to 96 KB a CU over its blocks.
+// Short form, 16 x 16 tiles, one wave for every 16 rows (1, 2, 3, 4 or 8 waves).  What counts is bytes on their way:
+// the ring is the deepest with which two blocks and all their rows' queries fit a CU, or where none does the deepest
+// with which one does, of 4 stages at most.  That is 64 to 96 KB on their way a CU, and 32 KB with eight waves at
+// 512-byte rows.  (64 sequences over 613 MB, 32 rows of D 256: 120 us, with one block a CU 137; 64 rows of D 128 over
+// 1.2 GB: 257 and 342.)  A depth of 0: no such call, not even the fewest rows of so many waves fit beside two stages.
 template <typename T, int DP, int WR>
 struct Short {
     static constexpr int WIDTH = DP;
     static constexpr int RB = DP * (int)sizeof(typename T::storage);
-    static constexpr int NS = RB <= 256 ? 4 : RB <= 512 && WR == 3 ? 4 : RB <= 512 && WR == 4 ? 3 : 2;
+    static constexpr int lds(int stages, int rows) { return stages * 64 * RB + rows * RB; }
+    static constexpr int depth() {
+        for (int blocks = 2; blocks >= 1; --blocks)
+            for (int ns = 4; ns >= 2; --ns)
+                if (lds(ns, 16 * WR) <= (blocks == 2 ? kCULds / 2 : kMaxLds)) return ns;
+        constexpr int fewest = WR == 8 ? 65 : 16 * (WR - 1) + 1;
+        return lds(2, (fewest + 7) / 8 * 8) <= kMaxLds ? 2 : 0;
+    }
+    static constexpr int NS = depth();
     using C = Cfg<T, 16, DP, WR, 1, NS, 1>;
 };
 // Long form, 32 x 32 tiles, four waves (eight at width 256 in half precision, where they share the queries' place).
@@ -1281,22 +1295,25 @@ constexpr Shape shape_of() {
     return Shape{C::BM, C::BN, C::LDS, C::RB, C::NT};
 }
 
-constexpr int kMaxLds = 159 * 1024;  // of the 160 KB, less the kernels' own few words
 
-// dp 64, 128 or 256; wr 1, 2, 3, 4 or 8.
-template <typename T, int DP, typename F>
-auto with_waves(int wr, F f) {
+// dp 64, 128 or 256; wr 1, 2, 3, 4 or 8.  `none` where there is no short form of so many rows.
+template <typename T, int DP, typename R, typename F>
+R with_waves(int wr, R none, F f) {
+    auto go = [&](auto s) -> R {
+        if constexpr (decltype(s)::NS > 0) return f(s);
+        else return none;
+    };
     switch (wr) {
-        case 1: return f(Short<T, DP, 1>{});
-        case 2: return f(Short<T, DP, 2>{});
-        case 3: return f(Short<T, DP, 3>{});
-        case 4: return f(Short<T, DP, 4>{});
-        default: return f(Short<T, DP, 8>{});
+        case 1: return go(Short<T, DP, 1>{});
+        case 2: return go(Short<T, DP, 2>{});
+        case 3: return go(Short<T, DP, 3>{});
+        case 4: return go(Short<T, DP, 4>{});
+        default: return go(Short<T, DP, 8>{});
     }
 }
-template <typename T, typename F>
-auto with_short(int dp, int wr, F f) {
-    return dp == 64 ? with_waves<T, 64>(wr, f) : dp == 128 ? with_waves<T, 128>(wr, f) : with_waves<T, 256>(wr, f);
+template <typename T, typename R, typename F>
+R with_short(int dp, int wr, R none, F f) {
+    return dp == 64 ? with_waves<T, 64>(wr, none, f) : dp == 128 ? with_waves<T, 128>(wr, none, f) : with_waves<T, 256>(wr, none, f);
 }
 template <typename T, typename F>
 auto with_long(int dp, F f) {
@@ -1355,7 +1372,7 @@ hipError_t start_one_both(const Args& a, long long blocks, int lds, hipStream_t 
 #define GDN_ATTN_INSTANCES(T)                                                                                           \
     template <>                                                                                                         \
     hipError_t start_short<T>(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream) {           \
-        return with_short<T>(dp, wr, [&](auto p) { return start_one_short<typename decltype(p)::C>(a, blocks, lds, stream); }); \
+        return with_short<T>(dp, wr, hipErrorInvalidConfiguration, [&](auto p) { return start_one_short<typename decltype(p)::C>(a, blocks, lds, stream); }); \
     }                                                                                                                   \
     template <>                                                                                                         \
     hipError_t start_long<T>(const Args& a, int dp, long long blocks, int lds, hipStream_t stream) {                    \
@@ -1364,7 +1381,7 @@ hipError_t start_one_both(const Args& a, long long blocks, int lds, hipStream_t 
     template <>                                                                                                         \
     hipError_t start_both<T>(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream) {            \
         return with_long<T>(dp, [&](auto l) {                                                                           \
-            return with_short<T>(dp, wr, [&](auto p) {                                                                  \
+            return with_short<T>(dp, wr, hipErrorInvalidConfiguration, [&](auto p) {                                                                  \
                 using L = decltype(l);                                                                                  \
                 using P = decltype(p);                                                                                  \
                 if constexpr (L::WIDTH == P::WIDTH) return start_one_both<typename L::C, typename P::C>(a, blocks, lds, stream); \

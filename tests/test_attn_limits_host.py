@@ -78,3 +78,20 @@ def test_more_tokens_than_a_launch_holds(abi, N):  # noqa: F811
     for rot in (64, 50):
         d = rope_desc(abi, N=N, H=1, HK=1, cache_rows=N, rot=rot)
         assert abi.lib().gdn_qk_norm_rope_varlen(ctypes.byref(d), *([P] * 13), None, None) == abi.ERR_OVERFLOW
+
+
+@pytest.mark.parametrize("fields,rows", [(dict(H=16, HK=2, D=256, max_q=4), 32), (dict(H=8, HK=2, D=128, max_q=16), 64),
+                                         (dict(H=8, HK=2, D=128, max_q=16, dtype=0), 64)])
+def test_two_blocks_a_cu_where_they_fit(abi, fields, rows):  # noqa: F811
+    """Rings and queries of exactly half a CU's LDS (80 KB): the workspace has slots for two blocks on each of 256
+    CUs.  At fp32 and D 128 the 64 rows leave one."""
+    import ctypes
+
+    n = ctypes.c_size_t()
+    D, H = fields["D"], fields["H"]
+    wide = dict(q_stride=(H * D, D), out_stride=(H * D, D), k_stride=(2 * D, D), v_stride=(2 * D, D))
+    d = attn_desc(abi, B=64, N=64 * fields["max_q"], kv_rows=1 << 20, **fields, **wide)
+    assert abi.lib().gdn_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)) == abi.OK
+    blocks = 256 if fields.get("dtype") == 0 else 512
+    slots = 2 * blocks * rows * (4 * D + 8)
+    assert slots <= n.value < slots + slots // 8

@@ -456,3 +456,13 @@ def test_a_large_cache_is_not_cut_finer(torch, kind, HK, G, lengths, prefix):
     assert_within(out, o, ot, "large cache out")
     assert_within(lse, l, lt, "large cache lse")
     assert written <= most, (written, most)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [16, 24, 32, 40, 48, 56, 64, 72, 128])
+@pytest.mark.parametrize("prefix", [0, 90])
+def test_rows_of_every_number_of_waves(torch, kind, D, rows, prefix):
+    """Every number of waves (16 rows each) of the short form, at every width, whole runs and cut ones."""
+    Case(torch, kind, 2, 8, D, [(rows // 8, 400), (1, 33), (0, 4), (rows // 8, rows // 8), (2, 1)], prefix=prefix,
+         seed=rows + D).check(f"{rows} rows D{D}")
