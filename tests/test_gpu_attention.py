@@ -466,3 +466,93 @@ def test_rows_of_every_number_of_waves(torch, kind, D, rows, prefix):
     """Every number of waves (16 rows each) of the short form, at every width, whole runs and cut ones."""
     Case(torch, kind, 2, 8, D, [(rows // 8, 400), (1, 33), (0, 4), (rows // 8, rows // 8), (2, 1)], prefix=prefix,
          seed=rows + D).check(f"{rows} rows D{D}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,B", [(1, 150), (5, 30)])
+def test_many_rows_of_cut_runs(torch, kind, D, T, B):
+    """More rows than are joined a block each: single tokens and drafts of 32 heads, empty sequences, rows without
+    keys and a run over many blocks among them."""
+    lengths = [(0 if i % 11 == 5 else T, (T - 2 if T > 2 and i % 13 == 7 else T + (37 * i) % 90)) for i in range(B)]
+    lengths[B // 2] = (T, 3000)
+    c = Case(torch, kind, 8, 4, D, lengths, seed=D + T)
+    assert c.N * c.H > 2048
+    c.check(f"cut runs D{D} T{T}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_rows_of_cut_runs_masked_values(torch, kind):
+    """The last token's value of every sequence is not finite; cut runs join rows done again and rows that are not."""
+    c = Case(torch, kind, 8, 4, 64, [(5, 40 + 61 * i % 700) for i in range(20)], seed=3)
+    last = torch.zeros(c.N, dtype=torch.bool)
+    last[4::5] = True
+    for b, (_, n) in enumerate(c.lengths):
+        for x in c.kv:
+            x[c.begin[b] + n - 1] = float("nan")
+    out, lse = c.call()
+    o, l, ot, lt = c.ref()
+    assert_within(out[~last.cuda()], o[~last], ot[~last], "cut masked out")
+    assert_within(lse[~last.cuda()], l[~last], lt[~last], "cut masked lse")
+
+
+@pytest.mark.parametrize("what", ["ok", "falling", "run", "length"])
+def test_many_rows_malformed(torch, what):
+    c = Case(torch, "bf16", 8, 4, 64, [(1, 20 + i) for i in range(100)], seed=2)
+    rows = c.kv[0].shape[0]
+    spoil = dict(ok=[], falling=[("offsets", 1, c.N + 5)], run=[("kv_begin", 2, rows - c.n[2] + 1)],
+                 length=[("kv_len", 0, -1)])[what]
+    _expect_untouched(torch, c, status=0 if what == "ok" else -9, spoil=spoil)
+
+
+def test_many_rows_from_a_graph(torch):
+    """Replays whose lengths change between them: other runs are cut than when the call was captured."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    c = Case(torch, "bf16", 8, 4, 128, [(1, 60 + 13 * i % 200) for i in range(100)], seed=6)
+    x = c.dev()
+    kw = {n: x[n] for n in ("kv_begin", "kv_len", "max_q")}
+    args = [x[n] for n in ("q", "k", "v", "offsets")]
+    out, lse = (torch.empty_like(t) for t in gdn.attention_varlen(*args, **kw, return_lse=True))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.attention_varlen(*args, **kw, out=out, lse=lse)
+    for turn in range(4):
+        x["kv_len"].copy_(torch.tensor([max(1, n - turn * (i % 3) * 20) for i, n in enumerate(c.n)], dtype=torch.int32))
+        want = gdn.attention_varlen(*args, **kw, return_lse=True)
+        torch.cuda.synchronize()
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (bits(out) == bits(want[0])).all() and (bits(lse) == bits(want[1])).all(), turn
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("lengths", [[(3, 50), (1, 200)], [(70, 90), (3, 50)]])
+def test_negative_scale(torch, kind, lengths):
+    c = Case(torch, kind, 2, 4, 128, lengths, seed=14)
+    out, lse = c.call(scale=-0.2)
+    o, l, ot, lt = c.ref(scale=-0.2)
+    assert_within(out, o, ot, "scaled out")
+    assert_within(lse, l, lt, "scaled lse")
+
+
+@pytest.mark.parametrize("T", [[3, 1], [200, 5]])
+def test_a_cache_without_rows(torch, T):
+    """No keys anywhere: zeros and -inf; and a prefix without rows is no prefix."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    N, dev = sum(T), "cuda"
+    q = torch.randn(N, 4, 64, device=dev, dtype=torch.bfloat16)
+    none = torch.empty(0, 2, 64, device=dev, dtype=torch.bfloat16)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)
+    kw = dict(kv_begin=torch.zeros(2, dtype=torch.int64, device=dev), max_q=max(T), return_lse=True)
+    off = i32(0, T[0], N)
+    out, lse = gdn.attention_varlen(q, none, none, off, kv_len=i32(0, 0), **kw)
+    assert (out == 0).all() and (lse == -float("inf")).all()
+    k, v = (torch.randn(9, 2, 64, device=dev, dtype=torch.bfloat16) for _ in range(2))
+    want = gdn.attention_varlen(q, k, v, off, kv_len=i32(4, 9), **kw)
+    got = gdn.attention_prefix_varlen(q, none, none, k, v, off, kv_len=i32(4, 9), **kw)
+    for a, b in zip(got, want):
+        assert (bits(a) == bits(b)).all()
