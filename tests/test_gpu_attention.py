@@ -556,3 +556,30 @@ def test_a_cache_without_rows(torch, T):
     got = gdn.attention_prefix_varlen(q, none, none, k, v, off, kv_len=i32(4, 9), **kw)
     for a, b in zip(got, want):
         assert (bits(a) == bits(b)).all()
+
+
+def test_binding_names_what_it_refuses(torch):
+    """With device tensors that are right otherwise: the number or tensor that is none is what the error names."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    c = Case(torch, "bf16", 2, 4, 64, [(1, 9), (2, 5)], seed=2)
+    x = c.dev()
+    c.call(x)
+    for bad, err, match in ((dict(k=3), TypeError, "k must be a tensor"), (dict(v="v"), TypeError, "v must be a tensor"),
+                            (dict(offsets=3), TypeError, "offsets must be a tensor"),
+                            (dict(q=None), TypeError, "q must be a tensor"),
+                            (dict(out=3), TypeError, "out must be a tensor"),
+                            (dict(workspace=3), TypeError, "workspace must be a tensor"),
+                            (dict(scale="one"), TypeError, "real number"), (dict(max_q="one"), TypeError, "integer"),
+                            (dict(max_q=1 << 70), OverflowError, "int too")):
+        with pytest.raises(err, match=match):
+            c.call({**x, **bad})
+    k = torch.randn(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    rope = dict(inv_freq=torch.ones(32, device="cuda"))
+    gdn.qk_norm_rope_varlen(x["q"], k, k, x["offsets"], **rope)
+    for args, kw, match in (((x["q"], 3, k, x["offsets"]), {}, "k must be a tensor"),
+                            ((x["q"], k, k, None), {}, "offsets must be a tensor"),
+                            ((x["q"], k, k, x["offsets"]), dict(eps="small"), "real number"),
+                            ((x["q"], k, k, x["offsets"]), dict(inv_freq=None), "inv_freq must be a tensor")):
+        with pytest.raises(TypeError, match=match):
+            gdn.qk_norm_rope_varlen(*args, **{**rope, **kw})
