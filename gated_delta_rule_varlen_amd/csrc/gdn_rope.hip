@@ -273,8 +273,10 @@ __global__ __launch_bounds__(NT) void rope_kernel(RopeLaunch a, int tpb, int log
                 }
                 raw.e[i] = from_f32<T>(v);
             }
-            *reinterpret_cast<u32x4*>(y + e0) = raw.v;
         }
+        // in place: all lanes have read their partners before one writes (a row lies in one wave)
+        __builtin_amdgcn_wave_barrier();
+        if (in) *reinterpret_cast<u32x4*>(y + e0) = raw.v;
     }
 }
 

@@ -182,3 +182,15 @@ def test_graph_replays(torch):
         graph.replay()
         torch.cuda.synchronize()
         assert (bits(x["q_out"]) == bits(want)).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,rot", [(64, 50), (256, 254), (72, 72), (8, 6)])
+@pytest.mark.parametrize("T", [[3, 0, 9], [700, 613]])
+def test_in_place_where_halves_are_no_pieces(torch, kind, D, rot, T):
+    """q_out = q where an element's partner lies in another lane's piece."""
+    c = Case(torch, kind, 5, 2, D, rot, T, [i % 3 for i in range(len(T))], seed=rot)
+    q, _, _ = c.call(c.dev())
+    x = c.dev()
+    in_place, _, _ = c.call(x, q_out=x["q"])
+    assert in_place.data_ptr() == x["q"].data_ptr() and (bits(in_place) == bits(q)).all()
