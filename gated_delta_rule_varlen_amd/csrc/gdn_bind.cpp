@@ -155,6 +155,10 @@ PyObject* rope(PyObject*, PyObject* const* x, Py_ssize_t count) {
         PyErr_SetString(PyExc_ValueError, "k_out and v_out are required with kv_begin");
         return nullptr;
     }
+    if (!has_v && x[14] != Py_None) {
+        PyErr_SetString(PyExc_ValueError, "v_out without v");
+        return nullptr;
+    }
     gdn_rope_desc d{};
     const int64_t N = q->size(0), H = q->size(1), HK = k->size(1), B = off->numel() - 1;
     Made q_out(x[12], {N, H, c.D}, *q, c.dtype), k_out(x[13], {N, HK, c.D}, *q, c.dtype);

@@ -583,3 +583,11 @@ def test_binding_names_what_it_refuses(torch):
                             ((x["q"], k, k, x["offsets"]), dict(inv_freq=None), "inv_freq must be a tensor")):
         with pytest.raises(TypeError, match=match):
             gdn.qk_norm_rope_varlen(*args, **{**rope, **kw})
+
+
+def test_binding_refuses_v_out_without_v(torch):
+    import gated_delta_rule_varlen_amd as gdn
+
+    k, off = torch.randn(3, 2, 64, device="cuda"), torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="v_out without v"):
+        gdn.qk_norm_rope_varlen(k, k, None, off, inv_freq=torch.ones(32, device="cuda"), v_out=torch.empty_like(k))
