@@ -257,7 +257,9 @@ PyObject* attention(PyObject*, PyObject* const* x, Py_ssize_t count) {
     Made out(x[10], {N, H, c.D}, *q, c.dtype);
     const auto o = c.head_rows(c.tensor(out.object, "out"), H, d.out_stride, "out");
     c.rows_are(o.rows == N, "out must have one row per token");
-    const bool with_lse = x[11] != Py_None || PyObject_IsTrue(x[12]) == 1;
+    const int asked = PyObject_IsTrue(x[12]);
+    if (c.failed || asked < 0) return nullptr;
+    const bool with_lse = x[11] != Py_None || asked == 1;
     Made lse(with_lse ? x[11] : Py_True, {N, H}, *q, at::kFloat);
     auto stats = with_lse ? (float*)c.flat(lse.object, N * H, at::kFloat, "lse") : nullptr;
     at::Tensor scratch;

@@ -591,3 +591,9 @@ def test_binding_refuses_v_out_without_v(torch):
     k, off = torch.randn(3, 2, 64, device="cuda"), torch.tensor([0, 3], dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError, match="v_out without v"):
         gdn.qk_norm_rope_varlen(k, k, None, off, inv_freq=torch.ones(32, device="cuda"), v_out=torch.empty_like(k))
+
+
+def test_binding_refuses_a_truth_value_that_has_none(torch):
+    c = Case(torch, "bf16", 2, 4, 64, [(1, 9), (2, 5)], seed=2)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        c.call({**c.dev(), "return_lse": torch.ones(2)})
