@@ -267,8 +267,8 @@ PyObject* attention(PyObject*, PyObject* const* x, Py_ssize_t count) {
     size_t ws_bytes = 0;
     if (x[13] != Py_None) {
         const at::Tensor* t = c.tensor(x[13], "workspace");
-        if (t != nullptr && (!t->is_cuda() || !t->is_contiguous()))
-            c.refuse(PyExc_ValueError, "workspace must be a contiguous device tensor");
+        if (t != nullptr && (!t->is_cuda() || t->get_device() != c.dev || !t->is_contiguous()))
+            c.refuse(PyExc_ValueError, "workspace must be a contiguous tensor on device cuda:%d", c.dev);
         if (c.failed) return nullptr;
         ws = t->data_ptr();
         ws_bytes = t->nbytes();

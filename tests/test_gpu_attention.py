@@ -597,3 +597,9 @@ def test_binding_refuses_a_truth_value_that_has_none(torch):
     c = Case(torch, "bf16", 2, 4, 64, [(1, 9), (2, 5)], seed=2)
     with pytest.raises(RuntimeError, match="ambiguous"):
         c.call({**c.dev(), "return_lse": torch.ones(2)})
+
+
+def test_binding_refuses_a_workspace_elsewhere(torch):
+    c = Case(torch, "bf16", 2, 4, 64, [(1, 9), (2, 5)], seed=2)
+    with pytest.raises(ValueError, match="workspace .* cuda:0"):
+        c.call({**c.dev(), "workspace": torch.empty(1 << 20, dtype=torch.uint8)})
