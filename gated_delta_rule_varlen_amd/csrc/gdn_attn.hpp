@@ -922,10 +922,11 @@ struct Block {
         return y;
     }
 
-    // The accumulators of the wave's rows.
+    // The accumulators of the wave's rows, unless redo() is to follow: it reads the queries, which may be where the
+    // results go.
     __device__ __forceinline__ void store(const To& to) {
         const int r = to.row0 + wave * M + col;
-        if (r >= to.rows) return;
+        if (r >= to.rows || spoiled) return;
         const Row y = row_at(to, r, ref, l, grp == 0);
         if (y.sums != nullptr) {
             float* p = y.sums + 4 * grp;
@@ -1082,9 +1083,8 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
         for (int i = row0 / a.G + (int)threadIdx.x; i <= last_token / a.G; i += C::NT) a.live[first + i] = parts;
     blk.sum_rows();
     const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? part : -1, -1};
-    // one or the other: redo() reads the queries, which may be where the results go
-    if (!blk.spoiled) blk.store(to);
-    else
+    blk.store(to);
+    if (blk.spoiled)
         blk.redo(to, prefix, t0 * C::BN, min(p1 * C::BN, a.c.prefix_len), own, k0 * C::BN, max(0, min(k1 * C::BN, n)), seen0);
 }
 
@@ -1181,9 +1181,8 @@ __device__ __forceinline__ void short_form(const Args& a, char* lds, const int w
             // a worker's slot 0: a run cut at the front; slot 1: a run that starts here and goes on in the next worker
             const typename Block<C>::To to{0, rows, run.first, run.hk, whole && a.to_sets ? a.local_set : -1,
                                            whole ? -1 : w * 2ll + (run.t0 == 0 ? 1 : 0)};
-            if (!blk.spoiled) {
-                blk.store(to);
-            } else {
+            blk.store(to);
+            if (blk.spoiled) {
                 const Keys own{static_cast<const char*>(a.c.k.p) + (run.begin * a.c.k.row + run.hk * a.c.k.head) * C::ES,
                                static_cast<const char*>(a.c.v.p) + (run.begin * a.c.v.row + run.hk * a.c.v.head) * C::ES,
                                run.n};
