@@ -210,10 +210,10 @@ Plan plan(const AttnLaunch& c) {
         p.join = c.N > 0 && (a.workers > 1 || a.sets > 0);
         by_rows = a.sets > 0 || few_rows(a);
     } else {
-        // One block for every slot that a row tile can have, however long max_q says that one sequence may be: with
-        // blocks for each sequence's longest, longest first, eight prompts of 24748 tokens took 667 us instead of 658, 64
-        // fp32 prompts of up to 300 tokens 317 instead of 323, one prompt of 8192 tokens among 63 of up to 200 1250
-        // instead of 537, and max_q = N for the eight prompts 756 instead of 659.
+        // One block for every slot that a row tile can have, however long max_q says that one sequence may be.  (With
+        // blocks for each sequence as for the longest, one prompt of 8192 tokens among 63 of up to 200 took 1220 us,
+        // so 545; max_q = N for eight prompts 756 and 660.  In the order of their keys 64 fp32 prompts of up to
+        // 300 tokens take 276 us, as they come 326.)
         const long long most = (rows + whole.bm - 1) / whole.bm, slots = all_rows / whole.bm + c.B;
         a.splits = parts(std::min(most * c.B, slots) * c.HK, c.kv_rows + c.prefix_len);
         p.blocks = slots * c.HK * a.splits;

@@ -227,6 +227,25 @@ __device__ __forceinline__ int sequence_at(const AttnLaunch& c, int G, unsigned 
     return lo;
 }
 
+// Up to 64 sequences, one a lane: their row tiles end to end without gaps, those of the one with most keys first, so that
+// the last blocks are short ones.  The tile's place from the end of its sequence b; past all tiles a large number.
+template <int BM>
+__device__ __forceinline__ unsigned by_keys(const AttnLaunch& c, int G, unsigned slot, int* b) {
+    const int lane = threadIdx.x & 63, i = min(lane, c.B - 1);
+    const int o = min(max(c.offsets[i], 0), c.N), T = min(max(c.offsets[i + 1], o), c.N) - o;
+    const int n = c.kv_len != nullptr ? c.kv_len[i] : T;
+    const int tiles = lane < c.B ? (T * G + BM - 1) / BM : 0;
+    unsigned start = 0;
+    for (int j = 0; j < c.B; ++j) {
+        const int other = __builtin_amdgcn_readlane(n, j), t = __builtin_amdgcn_readlane(tiles, j);
+        start += (other > n) | (other == n && j < lane) ? t : 0;
+    }
+    const uint64_t here = __builtin_amdgcn_ballot_w64(slot - start < (unsigned)tiles);
+    if (here == 0) return ~0u;
+    *b = uniform((int)__builtin_ctzll(here));
+    return slot - (unsigned)__builtin_amdgcn_readlane((int)start, *b);
+}
+
 // Sequence i as the arrays have it, and whether it is malformed.
 struct Entry {
     int o, e, n;
@@ -1017,9 +1036,9 @@ __device__ __forceinline__ void report(const Args& a, bool malformed, unsigned b
 }
 
 // The long form: one block per key head, key part and tile of BM rows.  The row tiles of all sequences lie end to
-// end (a few blocks find none and end), those of a sequence from its last, which sees most keys.  Key heads are the
-// fastest index, so the blocks that read one head's keys at a time lie on few XCDs.  With prefix_rows the rows
-// are all tokens' and the keys the prefix alone.
+// end (a few blocks find none and end), up to 64 sequences by their keys, those of a sequence from its last, which sees
+// most keys.  Key heads are the fastest index, so the blocks that read one head's keys at a time lie on few XCDs.  With
+// prefix_rows the rows are all tokens' and the keys the prefix alone.
 template <typename C>
 __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsigned block, const bool prefix_rows) {
     unsigned x = block;
@@ -1035,8 +1054,16 @@ __device__ __forceinline__ void long_form(const Args& a, char* lds, const unsign
         part = 4 * four + x % of;
         x /= of;
     }
-    const int b = prefix_rows ? 0 : sequence_at<C::BM>(a.c, a.G, x);
-    const unsigned back = prefix_rows ? x : x - slot_of<C::BM>(a.c, a.G, uniform(entry(a.c.offsets, b)), b);  // tiles behind
+    int b = 0;
+    unsigned back = x;  // tiles of the sequence behind this one
+    if (!prefix_rows) {
+        if (a.c.B <= 64) {
+            back = by_keys<C::BM>(a.c, a.G, x, &b);
+        } else {
+            b = sequence_at<C::BM>(a.c, a.G, x);
+            back = x - slot_of<C::BM>(a.c, a.G, uniform(entry(a.c.offsets, b)), b);
+        }
+    }
     // Queries and the first keys are on their way while the call is checked.
     const Sequence seq = prefix_rows ? Sequence{0, a.c.N, 0, 0} : sequence(a.c, b);
     const int first = seq.first, T = seq.T, n = seq.n;
