@@ -198,9 +198,9 @@ Plan plan(const AttnLaunch& c) {
         const long long units = c.HK * (c.kv_rows / s.bn + c.B);  // fewer blocks than that have work, bar overlapping runs
         a.workers = (int)std::max(1ll, std::min((long long)kCUs * per_cu, units));
         p.blocks = a.workers;
-        // Both forms in one launch where all blocks run at once (8 drafts behind 1001 shared keys: 12.8 us, in two
-        // launches 19.2).  In more rounds the short form's blocks are too few on a CU beside the long form's
-        // (256 sequences behind 8192 keys: 138 us, in two launches 127).
+        // Both forms in one launch where all blocks run at once (8 drafts behind 1001 shared keys: 12.4 us, in two
+        // launches 18.7).  In more rounds the short form's blocks are too few on a CU beside the long form's
+        // (256 sequences behind 8192 keys: 136 us, in two launches 130).
         p.both = a.prefix_blocks > 0 && a.prefix_blocks + a.workers <= 2 * kCUs && p.wr <= 4 && joint(whole.ring, p.lds);
         if (p.both) {
             p.lds = std::max(p.lds, whole.ring);
@@ -212,8 +212,8 @@ Plan plan(const AttnLaunch& c) {
     } else {
         // One block for every slot that a row tile can have, however long max_q says that one sequence may be.  (With
         // blocks for each sequence as for the longest, one prompt of 8192 tokens among 63 of up to 200 took 1220 us,
-        // so 545; max_q = N for eight prompts 756 and 660.  In the order of their keys 64 fp32 prompts of up to
-        // 300 tokens take 276 us, as they come 326.)
+        // so 557; max_q = N for eight prompts 756 and 680.  In the order of their keys 64 fp32 prompts of up to
+        // 300 tokens take 275 us, as they come 326.)
         const long long most = (rows + whole.bm - 1) / whole.bm, slots = all_rows / whole.bm + c.B;
         a.splits = parts(std::min(most * c.B, slots) * c.HK, c.kv_rows + c.prefix_len);
         p.blocks = slots * c.HK * a.splits;

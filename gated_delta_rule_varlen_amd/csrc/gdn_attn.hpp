@@ -21,9 +21,9 @@
 // Softmax in base 2: p = 2^(s*c - ref), c = scale*log2(e).  ref follows the running maximum only when
 // that has grown by more than 2^8 (P stays in range, the quotient O / l is the same), so O is hardly ever rescaled.
 //
-// On one MI355X: a prompt of 16384 tokens (H 16, HK 2, D 256, bf16) takes 1747 us = 1.26 PFLOP/s, the matrix cores
-// busy in 71% of the cycles; eight prompts of 24748 tokens (H 32, HK 8, D 128) 663 us = 1.0 PFLOP/s; decode of 256
-// sequences over 2.26 GB of cache 360 us = 6.3 TB/s.
+// On the MI355X, by card: a prompt of 16384 tokens (H 16, HK 2, D 256, bf16) takes 1747 to 1867 us = 1.18 to 1.26 PFLOP/s,
+// the matrix cores busy in 71% of the cycles; eight prompts of 24748 tokens (H 32, HK 8, D 128) 663 to 700 us = 0.95 to
+// 1.0 PFLOP/s, busy in 54%; decode of 256 sequences over 2.26 GB of cache 357 to 363 us = 6.2 to 6.3 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -173,7 +173,7 @@ struct Range {
         r = u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)bytes, (uint32_t)kRsrc};
     }
 };
-// STREAM: the bytes are read by this block alone (decode of 256 sequences: 357 us, without the hint 410).
+// STREAM: the bytes are read by this block alone (decode of 256 sequences: 357 us, without the hint 408).
 template <bool STREAM>
 __device__ __forceinline__ void load_to_lds(const Range& s, uint32_t at, int voff, int soff) {
     if constexpr (STREAM)
@@ -401,7 +401,7 @@ struct Cfg {
     static constexpr int RPI = LW * 64 / CPR;      // rows one load of all of them covers
     static constexpr int PRE = RPI >= 16 ? 1 : 16 / RPI;  // after which the places of a row's pieces repeat
     // Operand steps of the queries that lie in LDS, behind the ring: at width 256 eight waves' share of the CU's
-    // registers holds six (with ten in LDS a 16384-token prompt takes 1757 us, with seven and spills 2170)
+    // registers holds six (with ten in LDS a 16384-token prompt takes 1785 us, with seven and spills 2195)
     static constexpr int QL = PADDED ? 10 : 0;
     static constexpr int RING = NS * STAGE, LDS = RING + QL * NW * 1024;
     static constexpr bool PIPE = RB <= 256;       // the registers hold two tiles' scores (long form)

@@ -1,9 +1,9 @@
 // gdn_bind.cpp -- argument marshalling of the softmax-attention operators as a CPython extension (_bind.so): from
 // tensors to descriptors and addresses, with the checks of the Python binding's other functions.
 //
-// These operators are called once a layer and token, where the host's time per call is the operator's: in Python
-// the same checks took 7 us a call, more than the kernels of a small step.  The entry points of libgdn.so are handed
-// in as addresses (connect), so nothing here is linked against it.
+// These operators are called once a layer and token, where the host's time per call is the operator's: one token's
+// attention takes 6.2 us of it, and with the same checks in Python 11.6, more than the kernels of a small step.  The entry
+// points of libgdn.so are handed in as addresses (connect), so nothing here is linked against it.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
