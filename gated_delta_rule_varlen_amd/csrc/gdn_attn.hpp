@@ -562,6 +562,10 @@ struct Block {
     static constexpr int SN = C::SUB * C::EA;  // scores of 32 keys a lane
     using Scores = Acc<M>[KT][C::SUB];
 
+    // The fp32 products of a score in the short form are summed in four chains: one sum of 256 after the other was off by
+    // up to 2.7 times as much as one in a tree (outputs of a token over 63 keys of D 256: 7.8e-7, so 2.9e-7).  The long
+    // form keeps one, as a plain product does: it has no registers for more (D 256, 8192 tokens: 2.6 ms, with four 3.2).
+    static constexpr int CHAINS = C::HALF || M == 32 ? 1 : 4;
     // Scores of a stage's keys: element i of a lane's scores of 32 keys is key 4 NG (i / 4) + 4 grp + i % 4.
     template <bool GROUPED>
     __device__ __forceinline__ void scores(int stage, Scores& acc) {
@@ -570,6 +574,7 @@ struct Block {
         for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int u = 0; u < C::SUB; ++u) acc[k][u] = Acc<M>{};
+        Acc<M> more[CHAINS][KT][C::SUB] = {};  // of chains 1 to CHAINS - 1
         // operands are read in groups ahead of the products that use them
         constexpr int KG = C::CS < 8 ? C::CS : C::CS > 8 && C::WAVES > 1 ? 4 : 8;
 #pragma unroll
@@ -588,9 +593,16 @@ struct Block {
                 for (int x = 0; x < KG; ++x) {
                     const u32x4 y = x0 + x < C::CS - C::QL ? q[x0 + x] : *query_at(x0 + x);
 #pragma unroll
-                    for (int u = 0; u < C::SUB; ++u) multiply<T, M>(f[x][u], y, acc[k][u]);
+                    for (int u = 0; u < C::SUB; ++u)
+                        multiply<T, M>(f[x][u], y, (x0 + x) % CHAINS == 0 ? acc[k][u] : more[(x0 + x) % CHAINS][k][u]);
                 }
             }
+        if constexpr (CHAINS == 4) {
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int u = 0; u < C::SUB; ++u) acc[k][u] = (acc[k][u] + more[1][k][u]) + (more[2][k][u] + more[3][k][u]);
+        }
     }
     // Hides the keys a row does not see; base = index of the tile's first key in the run.
     __device__ __forceinline__ void hide(Scores& s, int base) {

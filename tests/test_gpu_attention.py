@@ -603,3 +603,19 @@ def test_binding_refuses_a_workspace_elsewhere(torch):
     c = Case(torch, "bf16", 2, 4, 64, [(1, 9), (2, 5)], seed=2)
     with pytest.raises(ValueError, match="workspace .* cuda:0"):
         c.call({**c.dev(), "workspace": torch.empty(1 << 20, dtype=torch.uint8)})
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("at", [0, 37, 100, 127])
+def test_scores_of_single_precision_are_sums_of_parts(torch, D, at):
+    """One large product among many that a running sum behind it would lose: of single tokens at most a quarter of them
+    may be.  With one key the lse is the score; e = 2^-24 of it is 1, and no more than eight roundings follow."""
+    import gated_delta_rule_varlen_amd as gdn
+
+    q = torch.full((3, 2, D), 0.5, device="cuda")
+    q[:, :, at] = 4096.0
+    one = torch.ones(3, dtype=torch.int32, device="cuda")
+    _, lse = gdn.attention_varlen(q, q, q, torch.arange(4, dtype=torch.int32, device="cuda"), kv_len=one,
+                                  kv_begin=torch.arange(3, device="cuda"), max_q=1, scale=1.0, return_lse=True)
+    exact = 2.0 ** 24 + 0.25 * (D - 1)
+    assert (lse.double() - exact).abs().max().item() <= 0.25 * D / 4 + 8
