@@ -26,10 +26,10 @@ SIZE = {"f32": 4, "bf16": 2, "f16": 2}
 EPS = 1e-6
 
 # The 4-bit values (bit 3 is the sign) and the shared powers of two: a block's largest element is at most 6 of them.
-# Those of fp16 are such that every value of a block is an fp16 number.
+# They are such that every value of a block is a number of its type (4 * 2^126 would not be).
 VALUES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 BLOCK = 32
-POWERS = {"f32": (-126, 126), "bf16": (-126, 126), "f16": (-23, 13)}
+POWERS = {"f32": (-126, 125), "bf16": (-126, 125), "f16": (-23, 13)}
 
 
 # ---- cases ---------------------------------------------------------------------------------------
