@@ -1,4 +1,5 @@
-"""MI355X (gfx950) varlen gated delta-rule hot path, and the softmax-attention operators beside it.
+"""MI355X (gfx950) varlen gated delta-rule hot path, and the softmax-attention operators, the 4-bit cache and the block's
+norms beside it.
 
 A thin binding over libgdn's C ABI (include/gdn.h).  These functions only marshal arguments: they
 check that tensors are device-resident and contiguous, allocate outputs with torch when the
@@ -8,7 +9,7 @@ library.  Every step of the computation runs in the library's HIP kernels; there
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -17,8 +18,9 @@ from ._abi import GdnError, PATH_NAMES, lib  # noqa: F401
 
 __all__ = ["conv1d_varlen", "conv1d_varlen_capture", "prepare_qk_gates", "prepare_qk_gates_strided", "scan_varlen",
            "scan_varlen_capture", "scan_varlen_strided", "scan_varlen_noalloc", "scan_workspace_bytes", "decode_step",
-           "qk_norm_rope_varlen", "attention_varlen", "attention_prefix_varlen", "attention_workspace_bytes", "GdnError",
-           "lib"]
+           "qk_norm_rope_varlen", "attention_varlen", "attention_prefix_varlen", "attention_workspace_bytes", "Fp4Cache",
+           "fp4_cache", "cache_write_fp4_varlen", "cache_read_fp4_varlen", "attention_fp4_varlen",
+           "attention_fp4_workspace_bytes", "residual_norm", "gated_norm", "GdnError", "lib"]
 
 _DTYPE = {torch.float32: _abi.F32, torch.bfloat16: _abi.BF16, torch.float16: _abi.F16}
 _TORCH = {v: k for k, v in _DTYPE.items()}
@@ -369,7 +371,9 @@ def _marshal():
             raise ImportError(f"_bind.so is missing or does not load ({e}): build it with "
                               "`python -m gated_delta_rule_varlen_amd.build`") from e
         _bind.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            L.gdn_qk_norm_rope_varlen, L.gdn_attention_varlen, L.gdn_attention_prefix_varlen, L.gdn_attention_workspace_bytes)))
+            L.gdn_qk_norm_rope_varlen, L.gdn_attention_varlen, L.gdn_attention_prefix_varlen, L.gdn_attention_workspace_bytes,
+            L.gdn_cache_write_fp4_varlen, L.gdn_cache_read_fp4_varlen, L.gdn_attention_fp4_varlen,
+            L.gdn_attention_fp4_workspace_bytes, L.gdn_residual_norm, L.gdn_gated_norm)))
         _native = _bind
     return _native
 
@@ -447,3 +451,126 @@ def attention_workspace_bytes(q: torch.Tensor, B: int, *, HK: int, max_q: int, k
     n = ctypes.c_size_t()
     _check(lib().gdn_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)), "gdn_attention_workspace_bytes")
     return n.value
+
+
+class Fp4Cache(NamedTuple):
+    """A cache in 4 bits (include/gdn.h, gdn_fp4_cache): codes [rows, HK, D/2] and scales [rows, HK, D/32], uint8, with any
+    row and head strides (those of codes multiples of 16 bytes).  Any four such tensors in this order will do as well."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def fp4_cache(rows: int, HK: int, D: int, device="cuda") -> Fp4Cache:
+    """An empty cache (all values zero) of `rows` rows.  A head's rows lie one after the other, which is how the attention
+    reads them."""
+    if rows < 0 or HK < 1 or not 32 <= D <= 256 or D % 32:
+        raise ValueError("rows must not be negative, HK at least 1 and D a multiple of 32 up to 256")
+    return Fp4Cache(*(torch.zeros((HK, rows, w), dtype=torch.uint8, device=device).transpose(0, 1)
+                      for w in (D // 2, D // 32, D // 2, D // 32)))
+
+
+def cache_write_fp4_varlen(k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, *, cache, past=None, kv_begin=None,
+                           dev_status=None):
+    """New keys and values into a cache in 4 bits (gdn_cache_write_fp4_varlen).
+
+    k, v [N, HK, D] with contiguous heads and any token and head strides; offsets int32 [B+1].  Token i of
+    sequence b goes to row kv_begin[b] + past[b] + i (int64 [B], int32 [B]; past defaults to zeros, and without kv_begin the
+    row is the token's index).  Returns the cache."""
+    st = (_native or _marshal()).fp4_rows(False, k, v, offsets, cache, past, kv_begin, dev_status, _raw_stream(k))
+    if st:
+        _check(st, "gdn_cache_write_fp4_varlen")
+    return cache
+
+
+def cache_read_fp4_varlen(cache, offsets: torch.Tensor, *, N: Optional[int] = None, past=None, kv_begin=None,
+                          dtype: torch.dtype = torch.bfloat16, k_out=None, v_out=None, dev_status=None):
+    """What a cache's rows stand for (gdn_cache_read_fp4_varlen): k, v [N, HK, D] of `dtype`, token i of sequence b from
+    row kv_begin[b] + past[b] + i as in cache_write_fp4_varlen.  N is the number of tokens, offsets' last entry; k_out and
+    v_out, if given, decide N and dtype.  Returns (k, v)."""
+    codes = cache[0]
+    given = k_out if k_out is not None else v_out
+    if not isinstance(codes, torch.Tensor) or not (given is None or isinstance(given, torch.Tensor)):
+        raise TypeError("cache, k_out and v_out must be tensors")
+    if given is None:
+        if N is None:
+            raise ValueError("N is required without k_out and v_out")
+        shape, like = (N, codes.shape[1], 2 * codes.shape[2]), dict(dtype=dtype, device=codes.device)
+    else:
+        shape, like = tuple(given.shape), dict(dtype=given.dtype, device=given.device)
+    if k_out is None:
+        k_out = torch.empty(shape, **like)
+    if v_out is None:
+        v_out = torch.empty(shape, **like)
+    st = (_native or _marshal()).fp4_rows(True, k_out, v_out, offsets, cache, past, kv_begin, dev_status, _raw_stream(k_out))
+    if st:
+        _check(st, "gdn_cache_read_fp4_varlen")
+    return k_out, v_out
+
+
+def attention_fp4_varlen(q: torch.Tensor, cache, offsets: torch.Tensor, *, kv_len: torch.Tensor, kv_begin: torch.Tensor,
+                         max_q: Optional[int] = None, scale: float = 0.0, out=None, lse=None, return_lse: bool = False,
+                         workspace=None, dev_status=None):
+    """attention_varlen over a cache in 4 bits (gdn_attention_fp4_varlen): q [N, H, D]; the keys and values of sequence b
+    are what rows kv_begin[b] .. kv_begin[b] + kv_len[b] - 1 of the cache stand for, its own new tokens last.  The other
+    arguments are attention_varlen's.  Returns (out [N, H, D], lse [N, H] fp32, or None unless asked for)."""
+    st, out, lse = (_native or _marshal()).attention_fp4(q, cache, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse,
+                                                         workspace, dev_status, _raw_stream(q))
+    if st:
+        _check(st, "gdn_attention_fp4_varlen")
+    return out, lse
+
+
+def attention_fp4_workspace_bytes(q: torch.Tensor, B: int, *, HK: int, max_q: int, kv_rows: int) -> int:
+    """Bytes of device scratch attention_fp4_varlen takes as `workspace` for queries like q over a cache of kv_rows rows;
+    it allocates them itself when the caller keeps none."""
+    N, H, D = q.shape
+    qr, qh, _ = q.stride()
+    pair = ctypes.c_int64 * 2
+    none = pair()
+    d = _abi.AttnDesc(B, N, H, HK, D, min(max_q, N), _code(q, "q"), 0, 0.0, 0, kv_rows,
+                      pair(qr if N > 1 else H * D, qh if H > 1 else D), none, none, none, none, none)
+    n = ctypes.c_size_t()
+    _check(lib().gdn_attention_fp4_workspace_bytes(ctypes.byref(d), ctypes.byref(n)), "gdn_attention_fp4_workspace_bytes")
+    return n.value
+
+
+def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, weight=None, post_weight=None,
+                  scale: float = 1.0, channel_scale=None, eps: float = 1e-6, out=None, residual_out=None,
+                  write_residual: bool = True):
+    """What stands between two blocks (gdn_residual_norm), in one pass:
+
+        t = x, or x * post_weight / sqrt(mean(x^2) + eps)
+        residual_out = residual + scale * channel_scale * t
+        out = residual_out * weight / sqrt(mean(residual_out^2) + eps)      (of the sum before it is rounded)
+
+    x, out [N, C]; residual, residual_out [N, C] of x's type or float32 (residual None: zeros); weight, post_weight,
+    channel_scale fp32 [C] or None (ones; no norm of x).  out may be x and residual_out may be residual.  Returns
+    (out, residual_out), the latter None with write_residual=False."""
+    st, out, residual_out = (_native or _marshal()).residual_norm(x, residual, weight, post_weight, scale, channel_scale, eps, out,
+                                                                  residual_out, write_residual, _raw_stream(x))
+    if st:
+        _check(st, "gdn_residual_norm")
+    return out, residual_out
+
+
+_ACTIVATIONS = {"silu": 0, "sigmoid": _abi.GATE_SIGMOID}
+
+
+def gated_norm(x: torch.Tensor, gate: torch.Tensor, *, weight=None, eps: float = 1e-6, activation: str = "silu",
+               gate_first: bool = False, norm: bool = True, out=None):
+    """Norm of every head of a recurrence's or an attention's output times its activated gate (gdn_gated_norm):
+
+        out = x * weight / sqrt(mean(x^2) + eps) * act(gate),  with gate_first the norm of x * act(gate),
+        with norm=False (then no weight) x * act(gate)
+
+    x, gate, out [N, H, V] with contiguous heads and any token and head strides; weight fp32 [V] or None (ones); activation
+    "silu" or "sigmoid".  out may be x or gate.  Returns out."""
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    flags = _ACTIVATIONS[activation] | (_abi.GATE_FIRST if gate_first else 0) | (0 if norm else _abi.GATE_NO_NORM)
+    st, out = (_native or _marshal()).gated_norm(x, gate, weight, eps, flags, out, _raw_stream(x))
+    if st:
+        _check(st, "gdn_gated_norm")
+    return out

@@ -19,6 +19,7 @@ F32, BF16, F16 = 0, 1, 2
 CONV_SILU = 1
 L2NORM, SOFTPLUS, SIGMOID, NO_RETRIEVE, GATE_PER_KEY = 1, 2, 4, 8, 16
 ROPE_INTERLEAVED = 1
+GATE_SIGMOID, GATE_FIRST, GATE_NO_NORM = 1, 2, 4
 # gdn_path
 PATH_AUTO, PATH_DECODE, PATH_SEQ, PATH_CHUNK = 0, 1, 2, 3
 PATH_NAMES = {PATH_AUTO: "auto", PATH_DECODE: "decode", PATH_SEQ: "seq", PATH_CHUNK: "chunk"}
@@ -40,6 +41,12 @@ EXPORTS = (
     "gdn_attention_varlen",
     "gdn_attention_prefix_varlen",
     "gdn_attention_workspace_bytes",
+    "gdn_cache_write_fp4_varlen",
+    "gdn_cache_read_fp4_varlen",
+    "gdn_attention_fp4_varlen",
+    "gdn_attention_fp4_workspace_bytes",
+    "gdn_residual_norm",
+    "gdn_gated_norm",
     "gdn_status_string",
     "gdn_abi_version",
 )
@@ -129,6 +136,62 @@ class AttnDesc(ctypes.Structure):
     ]
 
 
+class Fp4Cache(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("k_codes_stride", ctypes.c_int64 * 2),
+        ("k_scales_stride", ctypes.c_int64 * 2),
+        ("v_codes_stride", ctypes.c_int64 * 2),
+        ("v_scales_stride", ctypes.c_int64 * 2),
+    ]
+
+
+class Fp4RowsDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("HK", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("k_stride", ctypes.c_int64 * 2),
+        ("v_stride", ctypes.c_int64 * 2),
+    ]
+
+
+class ResidualNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int32),
+        ("C", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
+        ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("residual_out_stride", ctypes.c_int64),
+    ]
+
+
+class GatedNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("V", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("eps", ctypes.c_float),
+        ("x_stride", ctypes.c_int64 * 2),
+        ("gate_stride", ctypes.c_int64 * 2),
+        ("out_stride", ctypes.c_int64 * 2),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -176,6 +239,18 @@ def lib() -> ctypes.CDLL:
         L.gdn_attention_prefix_varlen.restype = st
         L.gdn_attention_workspace_bytes.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
         L.gdn_attention_workspace_bytes.restype = st
+        L.gdn_cache_write_fp4_varlen.argtypes = [vp] * 9
+        L.gdn_cache_write_fp4_varlen.restype = st
+        L.gdn_cache_read_fp4_varlen.argtypes = [vp] * 9
+        L.gdn_cache_read_fp4_varlen.restype = st
+        L.gdn_attention_fp4_varlen.argtypes = [vp] * 9 + [ctypes.c_size_t, vp, vp]
+        L.gdn_attention_fp4_varlen.restype = st
+        L.gdn_attention_fp4_workspace_bytes.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+        L.gdn_attention_fp4_workspace_bytes.restype = st
+        L.gdn_residual_norm.argtypes = [vp] * 9
+        L.gdn_residual_norm.restype = st
+        L.gdn_gated_norm.argtypes = [vp] * 6
+        L.gdn_gated_norm.restype = st
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_abi_version.argtypes = []

@@ -1,5 +1,5 @@
 """Build libgdn.so (the C-ABI library) in-tree with hipcc for gfx950, and _bind.so (host code only: the argument
-marshalling of the softmax-attention operators) against torch's headers.
+marshalling of the operators beside the recurrence) against torch's headers.
 
 Every source of libgdn.so under csrc/ is compiled to an object in _build/ (in parallel), then linked into
 gated_delta_rule_varlen_amd/libgdn.so.  Run as ``python -m gated_delta_rule_varlen_amd.build``.
@@ -21,7 +21,8 @@ BIND = os.path.join(PKG, "_bind.so")
 SOURCES = ["gdn_api.cpp", "gdn_conv.hip", "gdn_prepare.hip", "gdn_scan.hip", "gdn_seq.hip", "gdn_chunk.hip",
            "gdn_chunk_k64.hip", "gdn_chunk_k128.hip", "gdn_chunk_k256.hip",
            "gdn_decode.hip", "gdn_noalloc.hip", "gdn_attn_api.cpp", "gdn_rope.hip", "gdn_attn.hip",
-           "gdn_attn_bf16.hip", "gdn_attn_f16.hip", "gdn_attn_f32.hip"]
+           "gdn_attn_bf16.hip", "gdn_attn_f16.hip", "gdn_attn_f32.hip",
+           "gdn_fp4.hip", "gdn_attn_fp4.hip", "gdn_norm_api.cpp", "gdn_norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [

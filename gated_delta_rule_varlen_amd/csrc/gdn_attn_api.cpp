@@ -5,41 +5,14 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 
 #include "gdn.h"
+#include "gdn_check.hpp"
 #include "gdn_launch.hpp"
 
 namespace {
 
-constexpr long long kMaxRowBytes = 4ll << 20;  // between two rows of k or v: 32-bit offsets inside a key tile
-
-bool dtype_ok(int d) { return d == GDN_F32 || d == GDN_BF16 || d == GDN_F16; }
-long long dsize(int d) { return d == GDN_F32 ? 4 : 2; }
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-gdn_status from_hip(hipError_t e) {
-    if (e == hipSuccess) return GDN_OK;
-    if (e == hipErrorInvalidConfiguration) return GDN_ERR_OVERFLOW;
-    return GDN_ERR_HIP;
-}
-
-// A [rows, heads, D] tensor with free row and head strides; one without rows has no address to check.
-gdn_status head_rows(const void* p, const int64_t stride[2], long long rows, int heads, int D, int dtype,
-                     gdn::HeadRows* out) {
-    out->p = const_cast<void*>(p);
-    out->row = stride[0];
-    out->head = stride[1];
-    if (rows == 0) return GDN_OK;
-    if (p == nullptr) return GDN_ERR_NULL;
-    if (stride[0] < 0 || stride[1] < 0) return GDN_ERR_SHAPE;
-    const long long es = dsize(dtype);
-    // the last element's byte offset stays far inside 64 bits
-    if (stride[0] > (LLONG_MAX / 16) / rows || stride[1] > (LLONG_MAX / 16) / heads) return GDN_ERR_OVERFLOW;
-    if (misaligned(p) || (stride[0] * es) % 16 != 0 || (stride[1] * es) % 16 != 0 || (D * es) % 16 != 0)
-        return GDN_ERR_ALIGN;
-    return GDN_OK;
-}
+using namespace gdn;
 
 gdn_status check_sizes(int B, int N, int H, int HK, int D, int dtype) {
     if (B < 1 || N < 0 || H < 1 || HK < 1 || D < 1 || D > 256) return GDN_ERR_SHAPE;
@@ -109,6 +82,66 @@ gdn_status attention(const gdn_attn_desc* d, const void* q, const void* pk, cons
     a.workspace = workspace;
     a.dev_status = dev_status;
     return from_hip(gdn::launch_attention(a, stream));
+}
+
+// The four tensors of a 4-bit cache; one without rows has no addresses to check.
+gdn_status check_cache(const gdn_fp4_cache* c, int HK, int D, gdn::Fp4Cache* to) {
+    if (c == nullptr) return GDN_ERR_NULL;
+    if (c->rows < 0 || D < 32 || D > 256 || D % 32 != 0) return GDN_ERR_SHAPE;
+    if (c->rows > LLONG_MAX / 16) return GDN_ERR_OVERFLOW;
+    to->rows = c->rows;
+    struct {
+        const void* p;
+        const int64_t* stride;
+        int width, align;
+        gdn::HeadRows* to;
+    } t[4] = {{c->k_codes, c->k_codes_stride, D / 2, 16, &to->k.codes},
+              {c->k_scales, c->k_scales_stride, D / 32, 1, &to->k.scales},
+              {c->v_codes, c->v_codes_stride, D / 2, 16, &to->v.codes},
+              {c->v_scales, c->v_scales_stride, D / 32, 1, &to->v.scales}};
+    for (const auto& e : t) {
+        const gdn_status st = strided_rows(e.p, e.stride, c->rows, HK, e.width, 1, e.align, e.to);
+        if (st != GDN_OK) return st;
+        if (e.stride[0] > kMaxRowBytes) return GDN_ERR_OVERFLOW;
+    }
+    return GDN_OK;
+}
+
+gdn_status fp4_rows(const gdn_fp4_rows_desc* d, const void* k, const void* v, const int32_t* offsets, const int32_t* past,
+                    const int64_t* kv_begin, const gdn_fp4_cache* cache, bool read, int32_t* dev_status,
+                    hipStream_t stream) {
+    if (d == nullptr || offsets == nullptr) return GDN_ERR_NULL;
+    gdn_status st = check_sizes(d->B, d->N, d->HK, d->HK, d->D, d->dtype);
+    if (st != GDN_OK) return st;
+    if (d->flags != 0) return GDN_ERR_UNSUPPORTED;
+    gdn::Fp4RowsLaunch a{};
+    if ((st = check_cache(cache, d->HK, d->D, &a.cache)) != GDN_OK) return st;
+    if (d->N > INT_MAX - 4096) return GDN_ERR_OVERFLOW;
+    if (kv_begin == nullptr && cache->rows < d->N) return GDN_ERR_SHAPE;  // rows are token indices
+    if ((st = head_rows(k, d->k_stride, d->N, d->HK, d->D, d->dtype, &a.k)) != GDN_OK) return st;
+    if ((st = head_rows(v, d->v_stride, d->N, d->HK, d->D, d->dtype, &a.v)) != GDN_OK) return st;
+    a.offsets = offsets;
+    a.past = past;
+    a.kv_begin = kv_begin;
+    a.dev_status = dev_status;
+    a.B = d->B;
+    a.N = d->N;
+    a.HK = d->HK;
+    a.D = d->D;
+    a.dtype = d->dtype;
+    a.read = read;
+    return from_hip(gdn::launch_fp4_rows(a, stream));
+}
+
+// The descriptor of an attention over a 4-bit cache, without the strides that are not read.
+gdn_status check_fp4_desc(const gdn_attn_desc* d, gdn::AttnLaunch* a) {
+    if (d == nullptr) return GDN_ERR_NULL;
+    gdn_attn_desc x = *d;
+    for (int i = 0; i < 2; ++i) x.k_stride[i] = x.v_stride[i] = 0;
+    if (x.prefix_len != 0) return GDN_ERR_SHAPE;
+    const gdn_status st = check_attn_desc(&x, a);
+    if (st != GDN_OK) return st;
+    return x.D % 32 != 0 ? GDN_ERR_SHAPE : GDN_OK;
 }
 
 }  // namespace
@@ -192,6 +225,51 @@ gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc* d, size_t* bytes) 
     gdn::AttnLaunch a{};
     const gdn_status st = check_attn_desc(d, &a);
     if (st == GDN_OK) *bytes = gdn::attention_workspace_bytes(a);
+    return st;
+}
+
+gdn_status gdn_cache_write_fp4_varlen(const gdn_fp4_rows_desc* d, const void* k, const void* v, const int32_t* offsets,
+                                      const int32_t* past, const int64_t* kv_begin, const gdn_fp4_cache* cache,
+                                      int32_t* dev_status, hipStream_t stream) {
+    return fp4_rows(d, k, v, offsets, past, kv_begin, cache, false, dev_status, stream);
+}
+
+gdn_status gdn_cache_read_fp4_varlen(const gdn_fp4_rows_desc* d, const gdn_fp4_cache* cache, const int32_t* offsets,
+                                     const int32_t* past, const int64_t* kv_begin, void* k_out, void* v_out,
+                                     int32_t* dev_status, hipStream_t stream) {
+    return fp4_rows(d, k_out, v_out, offsets, past, kv_begin, cache, true, dev_status, stream);
+}
+
+gdn_status gdn_attention_fp4_varlen(const gdn_attn_desc* d, const void* q, const gdn_fp4_cache* cache,
+                                    const int32_t* offsets, const int64_t* kv_begin, const int32_t* kv_len, void* out,
+                                    float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                    hipStream_t stream) {
+    gdn::AttnLaunch a{};
+    gdn::Fp4Cache c{};
+    gdn_status st = check_fp4_desc(d, &a);
+    if (st != GDN_OK) return st;
+    if (offsets == nullptr || kv_begin == nullptr || kv_len == nullptr) return GDN_ERR_NULL;
+    if ((st = check_cache(cache, d->HK, d->D, &c)) != GDN_OK) return st;
+    if (cache->rows != d->kv_rows) return GDN_ERR_SHAPE;
+    if ((st = head_rows(q, d->q_stride, d->N, d->H, d->D, d->dtype, &a.q)) != GDN_OK) return st;
+    if ((st = head_rows(out, d->out_stride, d->N, d->H, d->D, d->dtype, &a.out)) != GDN_OK) return st;
+    if (misaligned(workspace)) return GDN_ERR_ALIGN;
+    const size_t need = gdn::attention_fp4_workspace_bytes(a);
+    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+    a.offsets = offsets;
+    a.kv_begin = kv_begin;
+    a.kv_len = kv_len;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.dev_status = dev_status;
+    return from_hip(gdn::launch_attention_fp4(a, c, stream));
+}
+
+gdn_status gdn_attention_fp4_workspace_bytes(const gdn_attn_desc* d, size_t* bytes) {
+    if (bytes == nullptr) return GDN_ERR_NULL;
+    gdn::AttnLaunch a{};
+    const gdn_status st = check_fp4_desc(d, &a);
+    if (st == GDN_OK) *bytes = gdn::attention_fp4_workspace_bytes(a);
     return st;
 }
 

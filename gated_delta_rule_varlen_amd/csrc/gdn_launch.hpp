@@ -159,6 +159,51 @@ struct AttnLaunch {
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t stream);
 size_t attention_workspace_bytes(const AttnLaunch& a);
 
+// A cache in 4 bits: bytes of codes and scales, row r of head h at r*row + h*head (strides in bytes).
+struct Fp4Half {
+    HeadRows codes, scales;
+};
+struct Fp4Cache {
+    Fp4Half k, v;
+    long long rows;
+};
+struct Fp4RowsLaunch {
+    HeadRows k, v;  // the packed tokens, strides in elements
+    Fp4Cache cache;
+    const int32_t* offsets;
+    const int32_t* past;
+    const int64_t* kv_begin;
+    int32_t* dev_status;
+    int B, N, HK, D, dtype;
+    bool read;  // from the cache's rows to the packed tokens
+};
+hipError_t launch_fp4_rows(const Fp4RowsLaunch& a, hipStream_t stream);
+hipError_t launch_attention_fp4(const AttnLaunch& a, const Fp4Cache& cache, hipStream_t stream);
+size_t attention_fp4_workspace_bytes(const AttnLaunch& a);
+
+struct ResidualNormLaunch {
+    const void* x;
+    const void* residual;
+    const float* post_weight;
+    const float* channel_scale;
+    const float* weight;
+    void* out;
+    void* residual_out;
+    long long x_row, residual_row, out_row, residual_out_row;
+    int N, C, dtype, residual_dtype;
+    float eps, scale;
+};
+hipError_t launch_residual_norm(const ResidualNormLaunch& a, hipStream_t stream);
+
+struct GatedNormLaunch {
+    HeadRows x, gate, out;
+    const float* weight;
+    int N, H, V, dtype;
+    float eps;
+    bool sigmoid, gate_first, no_norm;
+};
+hipError_t launch_gated_norm(const GatedNormLaunch& a, hipStream_t stream);
+
 // Longest sequence the DECODE kernel carries column by column with staged token operands; AUTO
 // takes DECODE while the average sequence is no longer than this.
 constexpr int kDecodeShortTokens = 8;

@@ -1,0 +1,234 @@
+// gdn_norm.hip -- the norms before and behind a block: residual_norm over whole rows of the residual stream, gated_norm over
+// the heads of a mixer's output.  Both read every input once and write every output once, and hold a row in
+// registers between its sums and its results.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "gdn_device.hpp"
+#include "gdn_launch.hpp"
+
+namespace gdn {
+namespace {
+
+constexpr int kCUs = 256;
+
+// 16 bytes of a row of type T, as fp32.
+template <typename T>
+struct Piece {
+    using TS = typename T::storage;
+    static constexpr int VEC = 16 / sizeof(TS);
+    union {
+        u32x4 v;
+        TS e[VEC];
+    };
+    __device__ __forceinline__ float get(int i) const { return to_f32<T>(e[i]); }
+    __device__ __forceinline__ void set(int i, float x) { e[i] = from_f32<T>(x); }
+};
+
+// VEC consecutive elements of type R as whole pieces (VEC elements of fp32 are one or two of them).
+template <typename R, int VEC>
+struct Span {
+    static constexpr int PV = Piece<R>::VEC, NP = VEC / PV;
+    Piece<R> p[NP];
+    __device__ __forceinline__ void load(const typename R::storage* at) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) p[i].v = *reinterpret_cast<const u32x4*>(at + i * PV);
+    }
+    __device__ __forceinline__ void store(typename R::storage* at) const {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) *reinterpret_cast<u32x4*>(at + i * PV) = p[i].v;
+    }
+    __device__ __forceinline__ float get(int i) const { return p[i / PV].get(i % PV); }
+    __device__ __forceinline__ void set(int i, float x) { p[i / PV].set(i % PV, x); }
+};
+
+// Sum over the RT threads that share a row.  Two sums follow each other in different halves of `lds`, so a wave may write
+// the next one's part while another still reads this one's.
+template <int RT>
+__device__ __forceinline__ float row_sum(float x, float (*lds)[16], int& turn) {
+    x = group_sum<64>(x);
+    if constexpr (RT > 64) {
+        if ((threadIdx.x & 63) == 0) lds[turn][threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < RT / 64; ++w) x += lds[turn][w];
+        turn ^= 1;
+    }
+    return x;
+}
+
+// RT threads a row, P spans of 16 bytes of x a thread.
+template <typename T, typename R, int RT, int P>
+__global__ __launch_bounds__(RT < 256 ? 256 : RT) void residual_norm_kernel(ResidualNormLaunch a) {
+    using TS = typename T::storage;
+    using RS = typename R::storage;
+    constexpr int VEC = 16 / sizeof(TS), NT = RT < 256 ? 256 : RT, ROWS = NT / RT;
+    __shared__ float sums[2][16];
+    int turn = 0;
+    const int j = threadIdx.x % RT;
+    const float inv_c = 1.0f / (float)a.C;
+    for (long long row = (long long)blockIdx.x * ROWS + threadIdx.x / RT; row < a.N; row += (long long)gridDim.x * ROWS) {
+        const TS* x = static_cast<const TS*>(a.x) + row * a.x_row;
+        const RS* r = static_cast<const RS*>(a.residual) + row * a.residual_row;
+        Span<T, VEC> xs[P];
+        Span<R, VEC> rs[P];
+        float h[P][VEC];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * RT + j) * VEC;
+            xs[p].load(x + (e < a.C ? e : 0));
+            if (a.residual != nullptr) rs[p].load(r + (e < a.C ? e : 0));
+        }
+        float by = a.scale;
+        if (a.post_weight != nullptr) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                if ((p * RT + j) * VEC < a.C)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) sum = fmaf(xs[p].get(i), xs[p].get(i), sum);
+            by *= 1.0f / sqrtf(row_sum<RT>(sum, sums, turn) * inv_c + a.eps);
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * RT + j) * VEC;
+            if (e < a.C) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    float t = xs[p].get(i) * by;
+                    if (a.post_weight != nullptr) t *= a.post_weight[e + i];
+                    if (a.channel_scale != nullptr) t *= a.channel_scale[e + i];
+                    h[p][i] = a.residual != nullptr ? rs[p].get(i) + t : t;
+                    sum = fmaf(h[p][i], h[p][i], sum);
+                }
+            }
+        }
+        const float inv = 1.0f / sqrtf(row_sum<RT>(sum, sums, turn) * inv_c + a.eps);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * RT + j) * VEC;
+            if (e >= a.C) continue;
+            if (a.residual_out != nullptr) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) rs[p].set(i, h[p][i]);
+                rs[p].store(static_cast<RS*>(a.residual_out) + row * a.residual_out_row + e);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) xs[p].set(i, h[p][i] * inv * (a.weight != nullptr ? a.weight[e + i] : 1.0f));
+            xs[p].store(static_cast<TS*>(a.out) + row * a.out_row + e);
+        }
+    }
+}
+
+template <typename T, typename R, int RT, int P>
+hipError_t start_residual(const ResidualNormLaunch& a, hipStream_t stream) {
+    constexpr int NT = RT < 256 ? 256 : RT, ROWS = NT / RT;
+    const long long blocks = std::min<long long>(((long long)a.N + ROWS - 1) / ROWS, kCUs * 8);
+    residual_norm_kernel<T, R, RT, P><<<(unsigned)blocks, NT, 0, stream>>>(a);
+    return hipGetLastError();
+}
+template <typename T, typename R>
+hipError_t residual_for(const ResidualNormLaunch& a, hipStream_t stream) {
+    const int pieces = a.C / (16 / (int)sizeof(typename T::storage));
+    if (pieces <= 64) return start_residual<T, R, 64, 1>(a, stream);
+    if (pieces <= 256) return start_residual<T, R, 256, 1>(a, stream);
+    if (pieces <= 512) return start_residual<T, R, 256, 2>(a, stream);
+    if (pieces <= 1024) return start_residual<T, R, 256, 4>(a, stream);
+    if (pieces <= 4096) return start_residual<T, R, 1024, 4>(a, stream);
+    return start_residual<T, R, 1024, 8>(a, stream);
+}
+
+// A head's row: L lanes of a wave, P pieces of 16 bytes each.
+template <typename T, int L, int P>
+__global__ __launch_bounds__(256) void gated_norm_kernel(GatedNormLaunch a) {
+    using TS = typename T::storage;
+    constexpr int VEC = 16 / sizeof(TS), ROWS = 256 / L;
+    const int j = threadIdx.x % L;
+    const float inv_v = 1.0f / (float)a.V;
+    const unsigned rows = (unsigned)a.N * a.H, step = gridDim.x * ROWS;
+    // every lane goes round as often as its wave's first, so that all take part in the sums
+    for (unsigned first = blockIdx.x * ROWS; first < rows; first += step) {
+        const unsigned row = min(first + threadIdx.x / L, rows - 1), t = row / (unsigned)a.H, head = row - t * a.H;
+        const bool in = first + threadIdx.x / L < rows;
+        const TS* x = static_cast<const TS*>(a.x.p) + t * a.x.row + head * a.x.head;
+        const TS* z = static_cast<const TS*>(a.gate.p) + t * a.gate.row + head * a.gate.head;
+        Piece<T> xs[P], zs[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * L + j) * VEC, at = e < a.V ? e : 0;
+            xs[p].v = *reinterpret_cast<const u32x4*>(x + at);
+            zs[p].v = *reinterpret_cast<const u32x4*>(z + at);
+        }
+        float y[P][VEC], act[P][VEC], sum = 0.0f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const bool real = (p * L + j) * VEC < a.V;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float g = zs[p].get(i), s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+                act[p][i] = a.sigmoid ? s : g * s;
+                y[p][i] = xs[p].get(i);
+                if (a.gate_first) y[p][i] *= act[p][i];
+                sum = real ? fmaf(y[p][i], y[p][i], sum) : sum;
+            }
+        }
+        const float inv = a.no_norm ? 1.0f : 1.0f / sqrtf(group_sum<L>(sum) * inv_v + a.eps);
+        TS* out = static_cast<TS*>(a.out.p) + t * a.out.row + head * a.out.head;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * L + j) * VEC;
+            if (e >= a.V || !in) continue;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                float v = y[p][i] * inv;
+                if (a.weight != nullptr) v *= a.weight[e + i];
+                xs[p].set(i, a.gate_first ? v : v * act[p][i]);
+            }
+            *reinterpret_cast<u32x4*>(out + e) = xs[p].v;
+        }
+    }
+}
+
+template <typename T, int L, int P>
+hipError_t start_gated(const GatedNormLaunch& a, hipStream_t stream) {
+    constexpr int ROWS = 256 / L;
+    const long long blocks = std::min<long long>(((long long)a.N * a.H + ROWS - 1) / ROWS, kCUs * 32);
+    gated_norm_kernel<T, L, P><<<(unsigned)blocks, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t gated_for(const GatedNormLaunch& a, hipStream_t stream) {
+    const int pieces = a.V / (16 / (int)sizeof(typename T::storage));
+    if (pieces <= 4) return start_gated<T, 4, 1>(a, stream);
+    if (pieces <= 8) return start_gated<T, 8, 1>(a, stream);
+    if (pieces <= 16) return start_gated<T, 16, 1>(a, stream);
+    if (pieces <= 32) return start_gated<T, 32, 1>(a, stream);
+    if (pieces <= 64) return start_gated<T, 64, 1>(a, stream);
+    if (pieces <= 128) return start_gated<T, 64, 2>(a, stream);
+    if (pieces <= 256) return start_gated<T, 64, 4>(a, stream);
+    return start_gated<T, 64, 8>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_residual_norm(const ResidualNormLaunch& a, hipStream_t stream) {
+    const bool wide = a.residual_dtype != a.dtype;
+    switch (a.dtype) {
+        case GDN_F32: return residual_for<F32, F32>(a, stream);
+        case GDN_BF16: return wide ? residual_for<BF16, F32>(a, stream) : residual_for<BF16, BF16>(a, stream);
+        default: return wide ? residual_for<F16, F32>(a, stream) : residual_for<F16, F16>(a, stream);
+    }
+}
+
+hipError_t launch_gated_norm(const GatedNormLaunch& a, hipStream_t stream) {
+    switch (a.dtype) {
+        case GDN_F32: return gated_for<F32>(a, stream);
+        case GDN_BF16: return gated_for<BF16>(a, stream);
+        default: return gated_for<F16>(a, stream);
+    }
+}
+
+}  // namespace gdn

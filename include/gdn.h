@@ -20,7 +20,14 @@
  *                         new keys and values into the cache
  *   gdn_attention_varlen  causal grouped-head attention of each sequence over its rows of the cache
  *   gdn_attention_prefix_varlen   the same for a batch whose sequences all start with one prefix
- * plus gdn_scan_workspace_bytes, gdn_attention_workspace_bytes, gdn_status_string and gdn_abi_version.
+ * the same attention over a cache held in 4 bits:
+ *   gdn_cache_write_fp4_varlen, gdn_cache_read_fp4_varlen   new keys and values into it, and its rows as values
+ *   gdn_attention_fp4_varlen  gdn_attention_varlen over it
+ * and what stands before and behind a block of either kind:
+ *   gdn_residual_norm     norm of a block's output, its scaled sum with the residual stream, norm before the next block
+ *   gdn_gated_norm        per-head norm of a recurrence's or an attention's output times its activated gate
+ * plus gdn_scan_workspace_bytes, gdn_attention_workspace_bytes, gdn_attention_fp4_workspace_bytes, gdn_status_string and
+ * gdn_abi_version.
  *
  * Sources (docs.rs source pages): "onnxruntime-ep-mlx 0.31.1 src/ops/paged_ssm.rs" -- kernel strings
  * CONV, DELTA_PREPARE and DELTA, the capture strings, host functions conv(), delta() and the claim
@@ -463,6 +470,117 @@ gdn_status gdn_attention_prefix_varlen(const gdn_attn_desc *desc, const void *q,
 /* Workspace bytes the attention calls need for `desc`; 0 when none is needed.  Returns the same
  * descriptor errors as the calls. */
 gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc *desc, size_t *bytes);
+
+/* ------------------------------------------------------------------------------------------------
+ * A cache of keys and values in 4 bits.  A head's D elements are blocks of 32 that share a power of two 2^e (a byte
+ * e + 127); an element is a code of 4 bits: sign, two bits of exponent, one of fraction, which stand for 0, 1/2, 1,
+ * 3/2, 2, 3, 4 and 6 and their negatives, times 2^e.  Element 2j of a head is the low half of byte j of its codes.
+ * 4.25 bits an element; every value is exact in bf16 and fp32, and in fp16 for the scales below.
+ *
+ * gdn_cache_write_fp4_varlen -- token t of sequence b (i = t - offsets[b]) into row kv_begin[b] + past[b] + i (t where
+ * kv_begin is NULL).  For each block x of its keys and values:
+ *     e = the least with max|x| <= 6 * 2^e, within -126 .. 125 (fp16: -23 .. 13), where all values are numbers of the
+ *         type; what passes 6 * 2^125 (fp16: 49152) becomes that
+ *     code = the nearest to x / 2^e, ties to the even code, with the sign of x
+ * A block with an infinity or NaN gets the scale byte 255 (and codes 0), and reads as NaN throughout.
+ *
+ * gdn_cache_read_fp4_varlen -- the way back: k_out[t], v_out[t] = what row kv_begin[b] + past[b] + i stands for (a scale of
+ * 2^-127, which the write does not make, may read as zeros; in fp16 values round to fp16).
+ *
+ * gdn_attention_fp4_varlen -- gdn_attention_varlen with k and v the values of a cache: arguments, formula, masks and
+ * errors as there (out = q included), except that kv_begin and kv_len are required, desc->prefix_len is 0, its strides of k,
+ * v and the prefix are not read, desc->kv_rows = cache->rows, and D is a multiple of 32 (GDN_ERR_SHAPE).  With fp16 queries
+ * the cache's values are operands in fp16: those of scales past 2^13 may be infinite.
+ *
+ * Tensors (element (row, head, j) at row*stride[0] + head*stride[1] + j, strides in bytes):
+ *   k_codes, v_codes [rows, HK, D/2] uint8    16-byte aligned, strides multiples of 16 (GDN_ERR_ALIGN), rows at most 4 MiB
+ *   k_scales, v_scales [rows, HK, D/32] uint8   any alignment                       apart (GDN_ERR_OVERFLOW, both)
+ *   k, v, k_out, v_out [N, HK, D] dtype       required unless N == 0, strides in elements, multiples of 16 bytes
+ *   past [B] int32 NULL = zeros; kv_begin [B] int64
+ * Constraints of the write and the read: B >= 1, N >= 0, HK >= 1, D a multiple of 32 up to 256 (GDN_ERR_SHAPE), strides not
+ * negative, N and N*HK at most 2^31 - 4097 (GDN_ERR_OVERFLOW), no two tokens name one row of a write, inputs and
+ * outputs do not overlap.  Malformed offsets and rows outside [0, rows) of a sequence with tokens write nothing
+ * (GDN_ERR_OFFSETS in *dev_status).
+ * ---------------------------------------------------------------------------------------------- */
+typedef struct gdn_fp4_cache {
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t rows;
+    int64_t k_codes_stride[2], k_scales_stride[2], v_codes_stride[2], v_scales_stride[2]; /* bytes */
+} gdn_fp4_cache;
+
+typedef struct gdn_fp4_rows_desc {
+    int32_t B, N, HK, D;
+    int32_t dtype;    /* gdn_dtype of k and v */
+    uint32_t flags;   /* 0 */
+    int64_t k_stride[2], v_stride[2]; /* of the packed tokens */
+} gdn_fp4_rows_desc;
+
+gdn_status gdn_cache_write_fp4_varlen(const gdn_fp4_rows_desc *desc, const void *k, const void *v, const int32_t *offsets,
+                                      const int32_t *past, const int64_t *kv_begin, const gdn_fp4_cache *cache,
+                                      int32_t *dev_status, hipStream_t stream);
+
+gdn_status gdn_cache_read_fp4_varlen(const gdn_fp4_rows_desc *desc, const gdn_fp4_cache *cache, const int32_t *offsets,
+                                     const int32_t *past, const int64_t *kv_begin, void *k_out, void *v_out,
+                                     int32_t *dev_status, hipStream_t stream);
+
+gdn_status gdn_attention_fp4_varlen(const gdn_attn_desc *desc, const void *q, const gdn_fp4_cache *cache,
+                                    const int32_t *offsets, const int64_t *kv_begin, const int32_t *kv_len, void *out,
+                                    float *lse, void *workspace, size_t ws_bytes, int32_t *dev_status,
+                                    hipStream_t stream);
+
+/* Workspace bytes gdn_attention_fp4_varlen needs for `desc` (kv_rows = the cache's); 0 when none is needed. */
+gdn_status gdn_attention_fp4_workspace_bytes(const gdn_attn_desc *desc, size_t *bytes);
+
+/* ------------------------------------------------------------------------------------------------
+ * gdn_residual_norm -- between two blocks, for every token's row (C elements) in one pass:
+ *     t = x,  or x * post_weight / sqrt(mean(x^2) + eps) where post_weight is given
+ *     h = residual + scale * channel_scale * t
+ *     residual_out = h,   out = h * weight / sqrt(mean(h^2) + eps)
+ * fp32 throughout; out and residual_out are each rounded once, from the same h (out is the norm of h, not of what
+ * residual_out rounded it to).
+ *   x, out [N, C] dtype                            required unless N == 0; out may be x (same stride)
+ *   residual, residual_out [N, C] residual_dtype   NULL = zeros / not produced; may be the same (same stride)
+ *   weight, post_weight, channel_scale [C] fp32    NULL = ones (post_weight: no norm of x)
+ * Constraints: N >= 0, 1 <= C <= 32768 (GDN_ERR_SHAPE), residual_dtype = dtype or GDN_F32, strides at least C, finite scale,
+ * bases, strides and rows multiples of 16 bytes in either type (GDN_ERR_ALIGN).  No other overlap.
+ *
+ * gdn_gated_norm -- behind a recurrence or an attention, for every head (V elements) of every token:
+ *     out = n(x) * act(gate),  or n(x * act(gate)) with GDN_GATE_FIRST
+ *     n(y) = y * weight / sqrt(mean(y^2) + eps),  or y with GDN_GATE_NO_NORM
+ *     act(z) = z / (1 + exp(-z)),  or 1 / (1 + exp(-z)) with GDN_GATE_SIGMOID
+ * fp32, rounded once.
+ *   x, gate, out [N, H, V] dtype (strides as gdn_rope_desc's)   required unless N == 0; out may be x or gate (same strides)
+ *   weight [V] fp32                                             NULL = ones; NULL with GDN_GATE_NO_NORM (GDN_ERR_UNSUPPORTED)
+ * Constraints: N >= 0, H >= 1, 1 <= V <= 2048 (GDN_ERR_SHAPE), N*H at most 2^31 - 4097 (GDN_ERR_OVERFLOW), strides not
+ * negative, bases, strides and V multiples of 16 bytes (GDN_ERR_ALIGN).  No other overlap.
+ * ---------------------------------------------------------------------------------------------- */
+typedef struct gdn_residual_norm_desc {
+    int32_t N, C;
+    int32_t dtype;          /* gdn_dtype of x and out */
+    int32_t residual_dtype; /* of residual and residual_out: dtype or GDN_F32 */
+    float eps;              /* >= 0 */
+    float scale;
+    int64_t x_stride, residual_stride, out_stride, residual_out_stride; /* elements between rows */
+} gdn_residual_norm_desc;
+
+gdn_status gdn_residual_norm(const gdn_residual_norm_desc *desc, const void *x, const void *residual,
+                             const float *post_weight, const float *channel_scale, const float *weight, void *out,
+                             void *residual_out, hipStream_t stream);
+
+#define GDN_GATE_SIGMOID 1u
+#define GDN_GATE_FIRST 2u
+#define GDN_GATE_NO_NORM 4u
+
+typedef struct gdn_gated_norm_desc {
+    int32_t N, H, V;
+    int32_t dtype;   /* gdn_dtype of x, gate and out */
+    uint32_t flags;  /* GDN_GATE_SIGMOID | GDN_GATE_FIRST | GDN_GATE_NO_NORM */
+    float eps;       /* >= 0 */
+    int64_t x_stride[2], gate_stride[2], out_stride[2];
+} gdn_gated_norm_desc;
+
+gdn_status gdn_gated_norm(const gdn_gated_norm_desc *desc, const void *x, const void *gate, const float *weight, void *out,
+                          hipStream_t stream);
 
 /* Static description of a status code; never NULL. */
 const char *gdn_status_string(gdn_status status);
