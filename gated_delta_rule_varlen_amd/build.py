@@ -22,7 +22,8 @@ SOURCES = ["gdn_api.cpp", "gdn_conv.hip", "gdn_prepare.hip", "gdn_scan.hip", "gd
            "gdn_chunk_k64.hip", "gdn_chunk_k128.hip", "gdn_chunk_k256.hip",
            "gdn_decode.hip", "gdn_noalloc.hip", "gdn_attn_api.cpp", "gdn_rope.hip", "gdn_attn.hip",
            "gdn_attn_bf16.hip", "gdn_attn_f16.hip", "gdn_attn_f32.hip",
-           "gdn_fp4.hip", "gdn_attn_fp4.hip", "gdn_norm_api.cpp", "gdn_norm.hip"]
+           "gdn_fp4.hip", "gdn_attn_fp4.hip", "gdn_attn_fp4_bf16.hip", "gdn_attn_fp4_f16.hip", "gdn_attn_fp4_f32.hip",
+           "gdn_norm_api.cpp", "gdn_norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [

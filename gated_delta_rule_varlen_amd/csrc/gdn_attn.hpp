@@ -1370,8 +1370,8 @@ template <typename T>
 hipError_t start_both(const Args& a, int dp, int wr, long long blocks, int lds, hipStream_t stream);
 
 // `asked`: the devices on which the kernel may have more than 64 KB of LDS already.
-template <typename F>
-hipError_t start_kernel(F* f, std::atomic<uint64_t>& asked, const Args& a, long long blocks, int threads, int lds,
+template <typename F, typename A>
+hipError_t start_kernel(F* f, std::atomic<uint64_t>& asked, const A& a, long long blocks, int threads, int lds,
                         hipStream_t stream) {
     if (blocks * threads > kMaxThreads || lds > kMaxLds) return hipErrorInvalidConfiguration;
     if (lds > 64 * 1024) {

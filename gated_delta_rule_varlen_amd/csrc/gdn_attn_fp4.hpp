@@ -1,0 +1,550 @@
+// gdn_attn_fp4.hpp -- the kernels of the attention over a 4-bit cache (instances per type in gdn_attn_fp4_<type>.hip, host
+// side in gdn_attn_fp4.hip).  Rows, products and softmax are those of gdn_attn.hpp.
+//
+// Short form (decode and drafts, up to 64 rows a sequence and key head): bound by the cache's bytes.  Codes go from
+// memory to the registers they are used in, with nothing in between: a lane loads the codes of its part of a key, a
+// block of 32 elements or half of one, and they become matrix operands two elements an instruction, the block's power of two
+// included.  A contraction may run in any order, so the lane's elements are taken eight a step and the queries
+// are held in the same order.  Values are needed key by key for one element of the head: a lane loads the same few
+// elements of eight keys, widens them, and swaps halves of registers between two keys.
+//
+// A block's four waves take 32 keys each of every 128, with nothing shared until a run's end, where their sums are joined
+// through LDS.  All runs lie end to end and are cut into equal parts, one a block, as in the short form there.
+#pragma once
+
+#include "gdn_attn.hpp"
+#include "gdn_fp4.hpp"
+
+namespace gdn {
+namespace attn {
+
+struct Fp4Args {
+    Args a;
+    Fp4Cache cache;
+};
+
+// One run of a head's cache rows.
+struct Fp4Keys {
+    const char *kc, *ks, *vc, *vs;
+};
+__device__ __forceinline__ Fp4Keys fp4_keys(const Fp4Cache& c, long long begin, int hk) {
+    const auto at = [&](const HeadRows& x) { return static_cast<const char*>(x.p) + begin * x.row + hk * x.head; };
+    return Fp4Keys{at(c.k.codes), at(c.k.scales), at(c.v.codes), at(c.v.scales)};
+}
+
+// Row q over the keys j0 .. j1 - 1 plainly, by a wave: the largest score to base 2, the sum of exponentials and, four
+// elements a lane (4 * lane ..), their products with the values.
+struct RowSums {
+    float m, sum;
+    f32x4 o;
+};
+template <typename T>
+__device__ __forceinline__ RowSums plain_row(const typename T::storage* q, const Fp4Keys& s, const Fp4Cache& c, int D, float s2,
+                                             int j0, int j1) {
+    const int lane = threadIdx.x & 63;
+    RowSums r{kNoMax, 0.0f, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll 1
+    for (; j0 < j1; j0 += 64) {
+        float y = -INFINITY;
+        if (j0 + lane < j1) {
+            const char* codes = s.kc + (j0 + lane) * c.k.codes.row;
+            const uint8_t* scales = reinterpret_cast<const uint8_t*>(s.ks + (j0 + lane) * c.k.scales.row);
+            y = 0.0f;
+#pragma unroll 1
+            for (int x = 0; x < D / 8; ++x) {
+                float k[8];
+                fp4::values(reinterpret_cast<const uint32_t*>(codes)[x], scales[x / 4], k);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y = fmaf(to_f32<T>(q[8 * x + e]), k[e], y);
+            }
+            y *= s2;
+        }
+        float top = y;
+        for (int z = 1; z < 64; z <<= 1) top = fmaxf(top, __shfl_xor(top, z));
+        const float to = fmaxf(r.m, top), w = __builtin_amdgcn_exp2f(r.m - to), p = __builtin_amdgcn_exp2f(y - to);
+        r.sum = r.sum * w + group_sum<64>(p);
+        r.m = to;
+        r.o *= w;
+#pragma unroll 1
+        for (int j = 0; j < min(64, j1 - j0); ++j) {
+            const float pj = __shfl(p, j);
+            if (4 * lane >= D) continue;
+            float v[8];
+            fp4::values(*reinterpret_cast<const uint16_t*>(s.vc + (j0 + j) * c.v.codes.row + 2 * lane),
+                        *reinterpret_cast<const uint8_t*>(s.vs + (j0 + j) * c.v.scales.row + lane / 8), v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r.o[e] = fmaf(pj, v[e], r.o[e]);
+        }
+    }
+    return r;
+}
+
+// T: the type of queries and outputs.  fp16 has operands in fp16, the others in bf16, where an fp32 query or probability is
+// the sum of three parts: their products with the cache's values, which are exact in bf16, are exact as well.
+template <typename T_, int DP_, int RT_, int WAVES_>
+struct Cfg4 {
+    using T = T_;
+    using TS = typename T::storage;
+    using OP = std::conditional_t<T::code == GDN_F16, F16, BF16>;
+    static constexpr int DP = DP_, RT = RT_, WAVES = WAVES_;  // WAVES: of a SIMD, which is blocks of a CU
+    static constexpr int PARTS = T::code == GDN_F32 ? 3 : 1;
+    static constexpr int W = 4, NT = 64 * W, BN = 32, UNIT = BN * W, BM = 16 * RT;
+    static constexpr int CL = DP / 4 < 32 ? DP / 4 : 32;  // neighbouring elements a lane holds of a key
+    static constexpr int KH = DP / (4 * CL);              // such pieces of a key
+    static constexpr int STEPS = DP / 32, SPP = CL / 8;   // operand steps, and of a piece
+    static constexpr int VD = DP / 16;                    // neighbouring elements a lane holds of a value
+    static constexpr int ROW = DP + 4;                    // fp32 sums of a row in LDS
+    static constexpr float BIAS = T::code == GDN_F16 ? 4.0f : 0.0f, LAG = 8.0f;
+    static constexpr int lds(int rows) { return W * (rows < 16 ? rows : 16) * ROW * 4; }
+};
+
+template <typename OP>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes, float scale, int pair) {
+    // the pair is part of the instruction
+    switch (pair) {
+#define GDN_PAIR(p)                                                                                                    \
+    case p:                                                                                                            \
+        if constexpr (OP::code == GDN_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, p)); \
+        else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, p));
+        GDN_PAIR(0)
+        GDN_PAIR(1)
+        GDN_PAIR(2)
+        default: GDN_PAIR(3)
+#undef GDN_PAIR
+    }
+}
+
+// The parts of two fp32 numbers as operands.
+template <typename OP, int PARTS>
+__device__ __forceinline__ void split2(float x, float y, uint32_t* to, int step) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        const uint32_t w = pack<OP>(x, y);
+        to[i * step] = w;
+        if (i + 1 < PARTS) {
+            x -= __uint_as_float(w << 16);
+            y -= __uint_as_float(w & 0xffff0000u);
+        }
+    }
+}
+
+template <typename C>
+struct Short4 {
+    using T = typename C::T;
+    using TS = typename C::TS;
+    using OP = typename C::OP;
+    static constexpr int RT = C::RT, PARTS = C::PARTS, KH = C::KH, VD = C::VD;
+
+    // What a lane holds of 32 keys.
+    struct Tile {
+        uint32_t k[2][KH][C::CL / 8], ks[2][KH];
+        uint32_t v[8][VD > 8 ? 2 : 1], vs[8];
+    };
+
+    const Fp4Args& f;
+    const Args& a;
+    char* lds;
+    int lane, wave, col, grp;
+    int kv, ksv[KH], kc_off[KH], vc_off, vs_off;  // byte offsets of the lane's pieces in a tile
+    int kstride, kst, vstride, vst;               // bytes between rows
+    uint32_t q[RT][PARTS][C::STEPS][4];
+    Acc<16> o[RT][VD];
+    float ref[RT], l[RT], c;
+    int vis[RT], vis_lo, vis_hi;
+    bool spoiled;
+
+    __device__ __forceinline__ Short4(const Fp4Args& f_, char* lds_) : f(f_), a(f_.a), lds(lds_) {
+        lane = threadIdx.x & 63;
+        wave = uniform((int)threadIdx.x >> 6);
+        col = lane & 15;
+        grp = lane >> 4;
+        c = a.s2;
+        kstride = (int)f.cache.k.codes.row;
+        kst = (int)f.cache.k.scales.row;
+        vstride = (int)f.cache.v.codes.row;
+        vst = (int)f.cache.v.scales.row;
+        const int D = a.c.D;
+#pragma unroll
+        for (int h = 0; h < KH; ++h) {
+            const int e = h * 128 + C::CL * grp;  // first element of the piece
+            kc_off[h] = e < D ? col * kstride + e / 2 : kOutside;
+            ksv[h] = e < D ? col * kst + e / 32 : kOutside;
+        }
+        const int d = VD * col;
+        vc_off = d < D ? 4 * grp * vstride + d / 2 : kOutside;
+        vs_off = d < D ? 4 * grp * vst + d / 32 : kOutside;
+    }
+
+    using Rsrc = __amdgpu_buffer_rsrc_t;
+    // Rows j0 .. of the `left` rows of a tensor of which `width` bytes are a head's; reads past them are zeros.
+    __device__ __forceinline__ Rsrc rows_of(const char* p, int j0, int left, int stride, int width) const {
+        const int rows = min(left, C::BN);
+        return __builtin_amdgcn_make_buffer_rsrc((void*)(p + (long long)j0 * stride), 0, rows > 0 ? (rows - 1) * stride + width : 0, kRsrc);
+    }
+    __device__ __forceinline__ void load(Tile& t, const Fp4Keys& s, int j0, int left) const {
+        const int D = a.c.D;
+        const Rsrc kc = rows_of(s.kc, j0, left, kstride, D / 2), ks = rows_of(s.ks, j0, left, kst, D / 32);
+        const Rsrc vc = rows_of(s.vc, j0, left, vstride, D / 2), vs = rows_of(s.vs, j0, left, vst, D / 32);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < KH; ++h) {
+                if constexpr (C::CL == 32) {
+                    const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kc, kc_off[h], u * 16 * kstride, 0));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t.k[u][h][i] = x[i];
+                } else {
+                    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(kc, kc_off[h], u * 16 * kstride, 0));
+                    t.k[u][h][0] = x[0], t.k[u][h][1] = x[1];
+                }
+                t.ks[u][h] = __builtin_amdgcn_raw_buffer_load_b8(ks, ksv[h], u * 16 * kst, 0);
+            }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int row = x < 4 ? x : 12 + x;  // behind 4 * grp
+            if constexpr (VD == 4) {
+                t.v[x][0] = __builtin_amdgcn_raw_buffer_load_b16(vc, vc_off, row * vstride, 0);
+            } else if constexpr (VD == 8) {
+                t.v[x][0] = __builtin_amdgcn_raw_buffer_load_b32(vc, vc_off, row * vstride, 0);
+            } else {
+                const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vc, vc_off, row * vstride, 0));
+                t.v[x][0] = y[0], t.v[x][1] = y[1];
+            }
+            t.vs[x] = __builtin_amdgcn_raw_buffer_load_b8(vs, vs_off, row * vst, 0);
+        }
+    }
+
+    // The queries of the sequence's rows, eight elements a step in the order of the keys' pieces.
+    __device__ __forceinline__ void take_rows(int rows, long long first, int hk) {
+        const int G = a.G;
+        const uint32_t flip = a.negate ? 0x80008000u : 0u;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int r = 16 * rt + col, i = r / G, g = r - i * G;
+            const bool in = r < rows;
+            const TS* p = static_cast<const TS*>(a.c.q.p) + (first + (in ? i : 0)) * a.c.q.row + (long long)(hk * G + (in ? g : 0)) * a.c.q.head;
+#pragma unroll
+            for (int s = 0; s < C::STEPS; ++s) {
+                const int e = s / C::SPP * 128 + C::CL * grp + s % C::SPP * 8;
+                const bool real = in && e < a.c.D;
+                const TS* at = p + (real ? e : 0);
+                if constexpr (PARTS == 1) {
+                    const u32x4 x = *reinterpret_cast<const u32x4*>(at);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) q[rt][0][s][j] = real ? x[j] ^ flip : 0u;
+                } else {
+                    const f32x4 x = reinterpret_cast<const f32x4*>(at)[0], y = reinterpret_cast<const f32x4*>(at)[1];
+                    const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[PARTS];
+                        split2<OP, PARTS>(v[2 * j], v[2 * j + 1], w, 1);
+#pragma unroll
+                        for (int z = 0; z < PARTS; ++z) q[rt][z][s][j] = real ? w[z] ^ flip : 0u;
+                    }
+                }
+            }
+            ref[rt] = kNoMax;
+            l[rt] = 0.0f;
+#pragma unroll
+            for (int y = 0; y < VD; ++y) o[rt][y] = Acc<16>{};
+        }
+        spoiled = false;
+    }
+    // The keys each row sees: seen0 + its token, at least 0 and at most n.
+    __device__ __forceinline__ void see(int rows, int seen0, int n) {
+        const int G = a.G;
+        auto keys = [&](int r) { return min(max(seen0 + r / G, 0), n); };
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) vis[rt] = 16 * rt + col < rows ? keys(16 * rt + col) : n;
+        vis_lo = uniform(keys(0));
+        vis_hi = uniform(keys(rows - 1));
+    }
+
+    static __device__ __forceinline__ u32x4 vec(const uint32_t* x) { return u32x4{x[0], x[1], x[2], x[3]}; }
+
+    // Keys j0 .. j0 + 31 of a run of n against all rows.
+    __device__ __forceinline__ void use(const Tile& t, int j0, int n) {
+        if (j0 >= vis_hi) return;
+        Acc<16> s[RT][2];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = Acc<16>{};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int x = 0; x < C::STEPS; ++x) {
+                const float scale = fp4::scale_of(t.ks[u][x / C::SPP]);
+                uint32_t k[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) k[j] = widen2<OP>(t.k[u][x / C::SPP][x % C::SPP], scale, j);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int z = PARTS - 1; z >= 0; --z) multiply<OP, 16>(vec(k), vec(q[rt][z][x]), s[rt][u]);
+            }
+        uint32_t p[RT][PARTS][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            if (j0 + C::BN > vis_lo) {
+                const int room = vis[rt] - j0 - 4 * grp;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[rt][i / 4][i % 4] = 16 * (i / 4) + i % 4 >= room ? -INFINITY : s[rt][i / 4][i % 4];
+            }
+            float top = s[rt][0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top = fmaxf(top, s[rt][i / 4][i % 4]);
+            top = over_row<16, true>(top) * c;
+            if (__builtin_amdgcn_ballot_w64(top > ref[rt] + (C::BIAS + C::LAG)) != 0) {
+                const float to = fmaxf(ref[rt], top - C::BIAS), w = __builtin_amdgcn_exp2f(ref[rt] - to);
+                ref[rt] = to;
+                l[rt] *= w;
+#pragma unroll
+                for (int y = 0; y < VD; ++y) o[rt][y] *= w;
+            }
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                e[i] = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], c, -ref[rt]));
+                l[rt] += e[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split2<OP, PARTS>(e[2 * i], e[2 * i + 1], &p[rt][0][i], 4);
+        }
+        // 0 * NaN is NaN: where rows differ in what they see, a value without a number would reach rows that must not
+        // see it.  Such a tile is found here, and the piece's rows are done again plainly.
+        if (vis_lo < min(j0 + C::BN, n)) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) most = max(most, t.vs[x]);
+            spoiled |= __builtin_amdgcn_ballot_w64(most == fp4::kNotANumber) != 0;
+        }
+        float scale[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) scale[x] = fp4::scale_of(t.vs[x]);
+#pragma unroll
+        for (int y = 0; y < VD; y += 2) {
+            uint32_t w[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) w[x] = widen2<OP>(t.v[x][y / 8], scale[x], y % 8 / 2);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], half ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int z = PARTS - 1; z >= 0; --z) multiply<OP, 16>(vec(v), vec(p[rt][z]), o[rt][y + half]);
+            }
+        }
+    }
+
+    // Units t0 .. t1 - 1 of the run.  A tile is on its way while another is used; past the end the loads have an empty range.
+    __device__ __forceinline__ void run(const Fp4Keys& s, int t0, int t1, int n) {
+        Tile x, y;
+        auto ask = [&](Tile& to, int t) {
+            const int j0 = t * C::UNIT + wave * C::BN;
+            load(to, s, t < t1 ? j0 : 0, t < t1 ? n - j0 : 0);
+        };
+        ask(x, t0);
+        for (int t = t0; t < t1; t += 2) {
+            ask(y, t + 1);
+            use(x, t * C::UNIT + wave * C::BN, n);
+            ask(x, t + 2);
+            if (t + 1 < t1) use(y, (t + 1) * C::UNIT + wave * C::BN, n);
+        }
+    }
+};
+
+// Where a piece's rows go: `slot` of the workspace, or out.
+template <typename C>
+__device__ __forceinline__ void put_row(const Args& a, long long first, int hk, int r, long long slot, float m, float sum, int e,
+                                        f32x4 o) {
+    using TS = typename C::TS;
+    const int i = r / a.G, h = hk * a.G + r - i * a.G;
+    if (slot >= 0) {
+        const long long at = slot * C::BM + r;
+        *reinterpret_cast<f32x4*>(a.slot_o + at * a.c.D + e) = o;
+        if (e == 0) a.slot_ml[at] = make_float2(m, sum);
+        return;
+    }
+    o *= sum == 0.0f ? 0.0f : 1.0f / sum;
+    TS* p = static_cast<TS*>(a.c.out.p) + (first + i) * a.c.out.row + h * a.c.out.head + e;
+    if constexpr (sizeof(TS) == 2) *reinterpret_cast<u32x2*>(p) = u32x2{pack<typename C::T>(o[0], o[1]), pack<typename C::T>(o[2], o[3])};
+    else *reinterpret_cast<f32x4*>(p) = o;
+    if (e == 0 && a.c.lse != nullptr)
+        a.c.lse[(first + i) * a.c.H + h] = sum == 0.0f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(sum));
+}
+
+// Joins the waves' sums of a piece and stores its rows.  Reached by all threads of the block.
+template <typename C>
+__device__ __forceinline__ void finish_piece(Short4<C>& b, const Fp4Keys& keys, const Run& run, int rows, long long slot) {
+    const Args& a = b.a;
+    __shared__ float2 ml[C::W][16];
+    __shared__ int spoiled[C::W];
+    float* const sums = reinterpret_cast<float*>(b.lds);
+    const int most = min(rows, 16);  // rows of a tile in LDS
+    bool again = false;
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
+        const int here = min(rows - 16 * rt, 16);
+        if (rt > 0) {
+            if (here <= 0) break;
+            __syncthreads();  // the last tile's sums are read
+        }
+        const float l = over_row<16, false>(b.l[rt]);
+        if (b.col < here) {
+            if (b.grp == 0) ml[b.wave][b.col] = make_float2(b.ref[rt], l);
+            float* at = sums + (b.wave * most + b.col) * C::ROW;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int y = 0; y < C::VD; y += 4)
+                    *reinterpret_cast<f32x4*>(at + C::VD * (4 * b.grp + i) + y) =
+                        f32x4{b.o[rt][y][i], b.o[rt][y + 1][i], b.o[rt][y + 2][i], b.o[rt][y + 3][i]};
+        }
+        if (rt == 0 && b.lane == 0) spoiled[b.wave] = b.spoiled;
+        __syncthreads();
+        if (rt == 0)
+#pragma unroll
+            for (int w = 0; w < C::W; ++w) again |= spoiled[w] != 0;
+        if (again) break;
+        for (int x = threadIdx.x; x < here * (C::DP / 4); x += C::NT) {
+            const int r = x / (C::DP / 4), e = x % (C::DP / 4) * 4;
+            if (e >= a.c.D) continue;
+            float m = ml[0][r].x, sum = 0.0f;
+#pragma unroll
+            for (int w = 1; w < C::W; ++w) m = fmaxf(m, ml[w][r].x);
+            f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < C::W; ++w) {
+                const float by = __builtin_amdgcn_exp2f(ml[w][r].x - m);
+                sum = fmaf(ml[w][r].y, by, sum);
+                o += *reinterpret_cast<const f32x4*>(sums + (w * most + r) * C::ROW + e) * by;
+            }
+            put_row<C>(a, run.first, run.hk, 16 * rt + r, slot, m, sum, e, o);
+        }
+    }
+    if (again) {
+        using TS = typename C::TS;
+        const float s2 = a.negate ? -a.s2 : a.s2;
+#pragma unroll 1
+        for (int r = b.wave; r < rows; r += C::W) {
+            const int i = r / a.G, g = r - i * a.G, seen = min(max(run.n - run.T + 1 + i, 0), run.n);
+            const TS* q = static_cast<const TS*>(a.c.q.p) + (run.first + i) * a.c.q.row + (long long)(run.hk * a.G + g) * a.c.q.head;
+            const RowSums x = plain_row<typename C::T>(q, keys, b.f.cache, a.c.D, s2, run.t0 * C::UNIT, min(run.t1 * C::UNIT, seen));
+            if (4 * b.lane < a.c.D) put_row<C>(a, run.first, run.hk, r, slot, x.m, x.sum, 4 * b.lane, x.o);
+        }
+    }
+}
+
+template <typename C>
+__global__ __launch_bounds__(C::NT, C::WAVES) void short4_kernel(Fp4Args f) {
+    extern __shared__ __align__(1024) char lds[];
+    const Args& a = f.a;
+    const int HK = a.c.HK, w = blockIdx.x;
+    using All = Tiles<C::UNIT>;
+    const All all(a.c);
+    const long long total = uniform(all.total) * HK;
+    report(a, all.malformed, w);
+    const int W = (int)min(total, (long long)a.workers);
+    if (all.malformed || w >= W) {
+        if (a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    const Cut cut(total, W);
+    long long u = uniform(cut.start(w));
+    const long long u1 = uniform(cut.start(w + 1));
+    Run run;
+    long long base;
+    all.find(u >> 31 ? u / HK : (unsigned)u / (unsigned)HK, &run.b, &base);
+    run.b = uniform(run.b);
+    base = uniform(base) * HK;
+    auto open = [&] {
+        run.first = uniform(entry(a.c.offsets, run.b));
+        run.T = uniform(entry(a.c.offsets, run.b + 1)) - run.first;
+        run.n = uniform(entry(a.c.kv_len, run.b));
+        run.begin = uniform((long long)entry(a.c.kv_begin, run.b));
+        run.tiles = All::of(run.T, run.n);
+    };
+    open();
+    const int within = (int)(u - base);
+    run.hk = uniform(within / run.tiles);
+    run.t0 = within - run.hk * run.tiles;
+    Short4<C> b(f, lds);
+    while (true) {
+        run.t1 = (int)min((long long)run.tiles, run.t0 + (u1 - u));
+        const int rows = run.T * a.G;
+        const Fp4Keys keys = fp4_keys(f.cache, run.begin, run.hk);
+        b.take_rows(rows, run.first, run.hk);
+        b.see(rows, run.n - run.T + 1, run.n);
+        b.run(keys, run.t0, run.t1, run.n);
+        const bool whole = run.t1 - run.t0 == run.tiles;
+        // a worker's slot 0: a run cut at the front; slot 1: a run that starts here and goes on in the next worker
+        finish_piece<C>(b, keys, run, rows, whole ? -1 : w * 2ll + (run.t0 == 0 ? 1 : 0));
+        if (run.t0 == 0) {
+            const int pieces = whole ? 1 : cut.part(u + run.tiles - 1) - w + 1;
+            if (a.row_info != nullptr)
+                for (int i = threadIdx.x; i < run.T; i += C::NT)
+                    a.row_info[(long long)(run.first + i) * HK + run.hk] = make_int2(whole ? -1 : w, pieces * 128 + i);
+            if (!whole && a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(run.first, run.T, run.hk, pieces);
+        }
+        u += run.t1 - run.t0;
+        if (u >= u1) {
+            if ((whole || run.t0 != 0) && a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(0, 0, 0, 0);
+            return;
+        }
+        run.t0 = 0;
+        if (++run.hk == HK) {
+            run.hk = 0;
+            do {
+                ++run.b;
+                open();
+            } while (run.tiles == 0);
+        }
+        __syncthreads();  // the piece's sums are read
+    }
+}
+
+// Waves of a SIMD that the registers of a configuration leave room for.
+template <typename T, int DP, int RT>
+struct Short4For {
+    static constexpr int STATE = RT * (DP / 4 + DP / 8 * (T::code == GDN_F32 ? 3 : 1)) + 2 * (DP / 8 + 20);
+    using C = Cfg4<T, DP, RT, (STATE <= 120 ? 3 : STATE <= 200 ? 2 : 1)>;
+};
+
+struct Shape4 {
+    int bm, unit, waves, row;
+};
+
+template <typename T, int DP, typename F>
+auto with_row_tiles(int rt, F f) {
+    switch (rt) {
+        case 1: return f(Short4For<T, DP, 1>{});
+        case 2: return f(Short4For<T, DP, 2>{});
+        case 3: return f(Short4For<T, DP, 3>{});
+        default: return f(Short4For<T, DP, 4>{});
+    }
+}
+template <typename T, typename F>
+auto with_short4(int dp, int rt, F f) {
+    return dp == 64 ? with_row_tiles<T, 64>(rt, f) : dp == 128 ? with_row_tiles<T, 128>(rt, f) : with_row_tiles<T, 256>(rt, f);
+}
+
+template <typename T>
+hipError_t start_short4(const Fp4Args& f, int dp, int rt, int lds, hipStream_t stream);
+
+template <typename C>
+hipError_t start_one_short4(const Fp4Args& f, int lds, hipStream_t stream) {
+    static std::atomic<uint64_t> asked{0};
+    return start_kernel(&short4_kernel<C>, asked, f, f.a.workers, C::NT, lds, stream);
+}
+
+#define GDN_ATTN_FP4_INSTANCES(T)                                                                                      \
+    template <>                                                                                                        \
+    hipError_t start_short4<T>(const Fp4Args& f, int dp, int rt, int lds, hipStream_t stream) {                        \
+        return with_short4<T>(dp, rt, [&](auto p) { return start_one_short4<typename decltype(p)::C>(f, lds, stream); }); \
+    }
+
+}  // namespace attn
+}  // namespace gdn

@@ -1,0 +1,8 @@
+// gdn_attn_fp4_f32.hip -- the kernels of the attention over a 4-bit cache for fp32 I/O.
+#include "gdn_attn_fp4.hpp"
+
+namespace gdn {
+namespace attn {
+GDN_ATTN_FP4_INSTANCES(F32)
+}  // namespace attn
+}  // namespace gdn

@@ -277,7 +277,7 @@ def test_streams_and_graphs(torch, lengths):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             call()
-        runs.append((graph, x, y, z, out, lse, c))
+        runs.append((graph, x, y, z, out, lse, (c, ws)))  # the graph needs its workspace
     for _ in range(3):
         for graph, x, y, z, out, lse, _ in runs:
             y.fill_(7.0)
@@ -286,7 +286,7 @@ def test_streams_and_graphs(torch, lengths):
             graph.replay()
             torch.cuda.synchronize()
             assert (bits(y) == bits(out)).all() and (bits(z) == bits(lse)).all()
-    for graph, x, y, z, _, _, c in runs:  # fewer keys in the same buffers
+    for graph, x, y, z, _, _, (c, _) in runs:  # fewer keys in the same buffers
         c.n = [max(n // 2, 1) for n in c.n]
         x["kv_len"].copy_(torch.tensor(c.n, dtype=torch.int32))
         want = c.check("fewer keys")
