@@ -506,15 +506,239 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short4_kernel(Fp4Args f) {
     }
 }
 
+// The long form (prompts): gdn_attn.hpp's tiles, pipeline and products, with the keys and values of a tile widened on their way
+// to LDS: a thread loads the codes of a run of elements of one key and of one value, a tile ahead of their use, and writes
+// them as operands where the asynchronous loads of a plain cache would have put them.
+template <typename C>
+struct Long4 : Block<C> {
+    using B = Block<C>;
+    using T = typename C::T;
+    using Scores = typename B::Scores;
+    using Rsrc = __amdgpu_buffer_rsrc_t;
+    static constexpr int U = C::BN * C::DP / C::NT, UPR = C::DP / U;  // elements a thread, and such runs of a row
+    static_assert((U == 16 || U == 32) && U * UPR == C::DP, "half a block of elements or a whole one");
+    struct Half {
+        uint32_t codes[U / 8], scale;
+    };
+    const Fp4Cache& cache;
+    int row, run_at;        // the thread's row of a tile and its run of elements there
+    int kc_off, ks_off, vc_off, vs_off;
+    Half k, v;
+
+    __device__ __forceinline__ Long4(const Fp4Args& f, char* lds) : B(f.a, lds), cache(f.cache) {
+        row = (int)threadIdx.x / UPR;
+        run_at = (int)threadIdx.x % UPR;
+        const int e = run_at * U;
+        const bool in = e < f.a.c.D;
+        kc_off = in ? row * (int)cache.k.codes.row + e / 2 : kOutside;
+        ks_off = in ? row * (int)cache.k.scales.row + e / 32 : kOutside;
+        vc_off = in ? row * (int)cache.v.codes.row + e / 2 : kOutside;
+        vs_off = in ? row * (int)cache.v.scales.row + e / 32 : kOutside;
+    }
+    __device__ __forceinline__ Rsrc rows_of(const char* p, int j0, int left, long long stride, int width) const {
+        const int rows = min(left, C::BN);
+        return __builtin_amdgcn_make_buffer_rsrc((void*)(p + j0 * stride), 0, rows > 0 ? (rows - 1) * (int)stride + width : 0, kRsrc);
+    }
+    // Asks for a tile's keys or values; nothing for one that is not real.
+    template <bool V>
+    __device__ __forceinline__ void fetch(const Fp4Keys& s, int tile, bool real) {
+        const Fp4Half& h = V ? cache.v : cache.k;
+        const int j0 = real ? tile * C::BN : 0, left = real ? B::run_n - j0 : 0, D = B::a.c.D;
+        const Rsrc rc = rows_of(V ? s.vc : s.kc, j0, left, h.codes.row, D / 2), rs = rows_of(V ? s.vs : s.ks, j0, left, h.scales.row, D / 32);
+        Half& to = V ? v : k;
+        if constexpr (U == 32) {
+            const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, V ? vc_off : kc_off, 0, 0));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to.codes[i] = x[i];
+        } else {
+            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, V ? vc_off : kc_off, 0, 0));
+            to.codes[0] = x[0], to.codes[1] = x[1];
+        }
+        to.scale = __builtin_amdgcn_raw_buffer_load_b8(rs, V ? vs_off : ks_off, 0, 0);
+    }
+    // Writes them to a stage of the ring.
+    template <bool V>
+    __device__ __forceinline__ void put(int stage) {
+        char* at = B::lds + stage * C::STAGE + (V ? C::KTILE + C::template row_at<C::VSTEP>(row) : C::template row_at<C::KSTEP>(row));
+        const int sw = V ? C::place_v(row) : C::place_k(row);
+        const Half& x = V ? v : k;
+        const float scale = fp4::scale_of(x.scale);
+#pragma unroll
+        for (int i = 0; i < U / 8; ++i) {
+            if constexpr (C::HALF) {
+                u32x4 w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = widen2<T>(x.codes[i], scale, j);
+                *reinterpret_cast<u32x4*>(at + (((run_at * (U / 8) + i) ^ sw) * 16)) = w;
+            } else {
+                float y[8];
+                fp4::values(x.codes[i], x.scale, y);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<f32x4*>(at + (((run_at * (U / 4) + 2 * i + j) ^ sw) * 16)) = f32x4{y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]};
+            }
+        }
+    }
+
+    // Tiles [t0, t1) of the run, as Block::run.
+    template <typename F>
+    __device__ __forceinline__ bool run(const Fp4Keys& s, int t0, int t1, int full, F stop) {
+        B::fresh_addresses();
+        int stage = 0, t = t0;
+        fetch<false>(s, t0, true);
+        fetch<true>(s, t0, true);
+        if (stop()) return false;
+        put<false>(0);
+        put<true>(0);
+        fetch<false>(s, t0 + 1, t0 + 1 < t1);
+        fetch<true>(s, t0 + 1, t0 + 1 < t1);
+        if constexpr (!C::PIPE) {
+            Scores cur;
+            auto one = [&](auto hidden, int at) {
+                wait_and_meet<63>();
+                put<false>(at ^ 1);
+                put<true>(at ^ 1);
+                fetch<false>(s, t + 2, t + 2 < t1);
+                fetch<true>(s, t + 2, t + 2 < t1);
+                if (hidden.value) B::look(B::lds + at * C::STAGE + C::KTILE, t * C::BN);
+                B::template plain_step<hidden.value>(at, t, cur);
+                ++t;
+            };
+            while (t + 1 < min(full, t1)) {
+                one(std::false_type{}, 0);
+                one(std::false_type{}, 1);
+            }
+            for (; t < t1; stage ^= 1) one(std::true_type{}, stage);
+        } else {
+            Scores now, next;
+            float top;
+            put<false>(1);
+            fetch<false>(s, t0 + 2, t0 + 2 < t1);
+            wait_and_meet<63>();
+            B::template scores<true>(0, now);
+            if (t0 >= full) B::hide(now, t0 * C::BN);
+            top = B::largest(now);
+            auto ahead = [&](int at) {
+                wait_and_meet<63>();
+                put<true>(at ^ 1);
+                put<false>(at);
+                fetch<true>(s, t + 2, t + 2 < t1);
+                fetch<false>(s, t + 3, t + 3 < t1);
+            };
+            while (t + 2 < min(full, t1 - 1)) {
+                ahead(0);
+                B::template step<false, false>(0, t, now, next, top);
+                ++t;
+                ahead(1);
+                B::template step<false, false>(1, t, next, now, top);
+                ++t;
+            }
+            for (; t < t1 - 1; ++t) {
+                ahead(stage);
+                if (t >= full) B::look(B::lds + stage * C::STAGE + C::KTILE, t * C::BN);
+                B::template step<true, false>(stage, t, now, next, top);
+#pragma unroll
+                for (int x = 0; x < B::KT; ++x)
+#pragma unroll
+                    for (int u = 0; u < C::SUB; ++u) now[x][u] = next[x][u];
+                stage ^= 1;
+            }
+            wait_and_meet<63>();
+            if (t >= full) B::look(B::lds + stage * C::STAGE + C::KTILE, t * C::BN);
+            B::template step<false, true>(stage, t, now, next, top);
+        }
+        wait_and_meet<63>();
+        return true;
+    }
+
+    // The wave's rows again, plainly, in place of store(), over the keys k0 .. k1 - 1.
+    __device__ __forceinline__ void redo4(const typename B::To& to, const Fp4Keys& s, int k0, int k1, int seen0) {
+        const Args& a = B::a;
+        const float s2 = a.negate ? -a.s2 : a.s2;
+#pragma unroll 1
+        for (int x0 = 0; x0 < B::M; ++x0) {
+            const int r = to.row0 + B::wave * B::M + x0;
+            if (r >= to.rows) break;
+            const int i = r / a.G, g = r - i * a.G;
+            const auto* q = static_cast<const typename C::TS*>(a.c.q.p) + (to.first + i) * a.c.q.row + (long long)(to.hk * a.G + g) * a.c.q.head;
+            const RowSums x = plain_row<T>(q, s, cache, a.c.D, s2, k0, min(k1, seen0 + i));
+            const auto y = B::row_at(to, r, x.m, x.sum, B::lane == 0);
+            for (int z = 0; z < 4 && 4 * B::lane < a.c.D; ++z) {
+                if (y.sums != nullptr) y.sums[4 * B::lane + z] = x.o[z];
+                else y.out[4 * B::lane + z] = from_f32<T>(x.o[z] * y.inv);
+            }
+        }
+    }
+};
+
+// One block per key head, key part and tile of BM rows, as gdn_attn.hpp's long form.
+template <typename C>
+__global__ __launch_bounds__(C::NT, C::WAVES) void long4_kernel(Fp4Args f) {
+    extern __shared__ __align__(1024) char lds[];
+    const Args& a = f.a;
+    const unsigned block = blockIdx.x;
+    unsigned x = block;
+    const int hk = x % a.c.HK;
+    x /= a.c.HK;
+    const unsigned slots = a.c.N * a.G / C::BM + a.c.B;
+    int part = 0;
+    if (a.splits > 1) {
+        const int four = x / (4 * slots), of = min(4, a.splits - 4 * four);
+        x -= four * 4 * slots;
+        part = 4 * four + x % of;
+        x /= of;
+    }
+    int b = 0;
+    unsigned back = x;  // tiles of the sequence behind this one
+    if (a.c.B <= 64) {
+        back = by_keys<C::BM>(a.c, a.G, x, &b);
+    } else {
+        b = sequence_at<C::BM>(a.c, a.G, x);
+        back = x - slot_of<C::BM>(a.c, a.G, uniform(entry(a.c.offsets, b)), b);
+    }
+    const Sequence seq = sequence(a.c, b);
+    const int first = seq.first, T = seq.T, n = seq.n;
+    auto stop = [&] {
+        const bool malformed = check<C::NT>(a.c);
+        report(a, malformed, block);
+        return malformed;
+    };
+    const int rows = T * a.G, tiles = (rows + C::BM - 1) / C::BM;
+    const int parts = min(a.splits, max(1, (int)((unsigned)n / kPartKeys)));
+    if (back >= (unsigned)tiles || part >= parts) {
+        if (block == 0) stop();  // the block that reports
+        return;
+    }
+    const int row0 = (tiles - 1 - (int)back) * C::BM;
+    const int seen0 = n - T + 1;
+    const int last_token = min(row0 + C::BM, rows) - 1;
+    const int reach = uniform(max(0, min(n, seen0 + last_token / a.G)));  // keys the last row sees
+    const int all = (reach + C::BN - 1) / C::BN;
+    const int t0 = uniform((int)((long long)all * part / parts)), t1 = uniform((int)((long long)all * (part + 1) / parts));
+
+    Long4<C> blk(f, lds);
+    blk.load_rows(row0, rows, first, hk);
+    blk.see(row0, rows, true, seen0, n);
+    const Fp4Keys keys = fp4_keys(f.cache, seq.begin, hk);
+    if (t0 < t1) {
+        const int full = uniform(max(0, min(n, seen0 + row0 / a.G)) / C::BN);
+        if (!blk.run(keys, t0, t1, full, stop)) return;
+    } else if (stop()) {
+        return;  // no keys at all
+    }
+    if (a.live != nullptr && part == 0 && hk == 0)
+        for (int i = row0 / a.G + (int)threadIdx.x; i <= last_token / a.G; i += C::NT) a.live[first + i] = parts;
+    blk.sum_rows();
+    const typename Block<C>::To to{row0, rows, first, hk, a.to_sets ? part : -1, -1};
+    blk.store(to);
+    if (blk.spoiled) blk.redo4(to, keys, t0 * C::BN, max(0, min(t1 * C::BN, n)), seen0);
+}
+
 // Waves of a SIMD that the registers of a configuration leave room for.
 template <typename T, int DP, int RT>
 struct Short4For {
     static constexpr int STATE = RT * (DP / 4 + DP / 8 * (T::code == GDN_F32 ? 3 : 1)) + 2 * (DP / 8 + 20);
     using C = Cfg4<T, DP, RT, (STATE <= 120 ? 3 : STATE <= 200 ? 2 : 1)>;
-};
-
-struct Shape4 {
-    int bm, unit, waves, row;
 };
 
 template <typename T, int DP, typename F>
@@ -534,6 +758,14 @@ auto with_short4(int dp, int rt, F f) {
 template <typename T>
 hipError_t start_short4(const Fp4Args& f, int dp, int rt, int lds, hipStream_t stream);
 
+template <typename T>
+hipError_t start_long4(const Fp4Args& f, int dp, long long blocks, int lds, hipStream_t stream);
+
+template <typename C>
+hipError_t start_one_long4(const Fp4Args& f, long long blocks, int lds, hipStream_t stream) {
+    static std::atomic<uint64_t> asked{0};
+    return start_kernel(&long4_kernel<C>, asked, f, blocks, C::NT, lds, stream);
+}
 template <typename C>
 hipError_t start_one_short4(const Fp4Args& f, int lds, hipStream_t stream) {
     static std::atomic<uint64_t> asked{0};
@@ -544,6 +776,10 @@ hipError_t start_one_short4(const Fp4Args& f, int lds, hipStream_t stream) {
     template <>                                                                                                        \
     hipError_t start_short4<T>(const Fp4Args& f, int dp, int rt, int lds, hipStream_t stream) {                        \
         return with_short4<T>(dp, rt, [&](auto p) { return start_one_short4<typename decltype(p)::C>(f, lds, stream); }); \
+    }                                                                                                                  \
+    template <>                                                                                                        \
+    hipError_t start_long4<T>(const Fp4Args& f, int dp, long long blocks, int lds, hipStream_t stream) {               \
+        return with_long<T>(dp, [&](auto p) { return start_one_long4<typename decltype(p)::C>(f, blocks, lds, stream); }); \
     }
 
 }  // namespace attn
