@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "gdn_device.hpp"
 #include "gdn_launch.hpp"
@@ -59,52 +60,99 @@ __device__ __forceinline__ float row_sum(float x, float (*lds)[16], int& turn) {
     return x;
 }
 
-// RT threads a row, P spans of 16 bytes of x a thread.
+// VEC consecutive entries of a vector in fp32.
+template <int VEC>
+__device__ __forceinline__ void load_vector(const float* p, float* to) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(p + i);
+        to[i] = x[0], to[i + 1] = x[1], to[i + 2] = x[2], to[i + 3] = x[3];
+    }
+}
+
+// RT threads a row, P spans of 16 bytes of x a thread.  A block goes over rows with the next one on its way, and keeps the
+// vectors in registers where they are few (P <= 2): read again for every row they are as many bytes from L2 as the row.
 template <typename T, typename R, int RT, int P>
 __global__ __launch_bounds__(RT < 256 ? 256 : RT) void residual_norm_kernel(ResidualNormLaunch a) {
     using TS = typename T::storage;
     using RS = typename R::storage;
     constexpr int VEC = 16 / sizeof(TS), NT = RT < 256 ? 256 : RT, ROWS = NT / RT;
+    constexpr bool KEEP = P <= 2;
     __shared__ float sums[2][16];
     int turn = 0;
     const int j = threadIdx.x % RT;
     const float inv_c = 1.0f / (float)a.C;
-    for (long long row = (long long)blockIdx.x * ROWS + threadIdx.x / RT; row < a.N; row += (long long)gridDim.x * ROWS) {
-        const TS* x = static_cast<const TS*>(a.x) + row * a.x_row;
-        const RS* r = static_cast<const RS*>(a.residual) + row * a.residual_row;
-        Span<T, VEC> xs[P];
-        Span<R, VEC> rs[P];
-        float h[P][VEC];
+    struct Row {
+        Span<T, VEC> x[P];
+        Span<R, VEC> r[P];
+    };
+    auto fetch = [&](long long row) {
+        Row y;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int e = (p * RT + j) * VEC;
-            xs[p].load(x + (e < a.C ? e : 0));
-            if (a.residual != nullptr) rs[p].load(r + (e < a.C ? e : 0));
+            const int e = (p * RT + j) * VEC, at = e < a.C ? e : 0;
+            y.x[p].load(static_cast<const TS*>(a.x) + row * a.x_row + at);
+            if (a.residual != nullptr) y.r[p].load(static_cast<const RS*>(a.residual) + row * a.residual_row + at);
         }
-        float by = a.scale;
+        return y;
+    };
+    float by_kept[KEEP ? P : 1][VEC], w_kept[KEEP ? P : 1][VEC];
+    // scale * channel_scale * post_weight, and the weight, of a span
+    auto factors = [&](int p, float* by) {
+        const int e = (p * RT + j) * VEC, at = e < a.C ? e : 0;
+        float x[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) by[i] = a.scale;
+        for (const float* v : {a.channel_scale, a.post_weight}) {
+            if (v == nullptr) continue;
+            load_vector<VEC>(v + at, x);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) by[i] *= x[i];
+        }
+    };
+    auto weights = [&](int p, float* w) {
+        const int e = (p * RT + j) * VEC;
+        if (a.weight != nullptr) {
+            load_vector<VEC>(a.weight + (e < a.C ? e : 0), w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = 1.0f;
+        }
+    };
+    const long long step = (long long)gridDim.x * ROWS;
+    long long row = (long long)blockIdx.x * ROWS + threadIdx.x / RT;
+    if (row >= a.N) return;
+    Row next = fetch(row);
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) factors(p, by_kept[p]), weights(p, w_kept[p]);
+    }
+    for (; row < a.N; row += step) {
+        Row cur = next;
+        if (row + step < a.N) next = fetch(row + step);
+        float inv_x = 1.0f;
         if (a.post_weight != nullptr) {
             float sum = 0.0f;
 #pragma unroll
             for (int p = 0; p < P; ++p)
                 if ((p * RT + j) * VEC < a.C)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) sum = fmaf(xs[p].get(i), xs[p].get(i), sum);
-            by *= 1.0f / sqrtf(row_sum<RT>(sum, sums, turn) * inv_c + a.eps);
+                    for (int i = 0; i < VEC; ++i) sum = fmaf(cur.x[p].get(i), cur.x[p].get(i), sum);
+            inv_x = 1.0f / sqrtf(row_sum<RT>(sum, sums, turn) * inv_c + a.eps);
         }
-        float sum = 0.0f;
+        float h[P][VEC], sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int e = (p * RT + j) * VEC;
-            if (e < a.C) {
+            float now[VEC];
+            if constexpr (!KEEP) factors(p, now);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    float t = xs[p].get(i) * by;
-                    if (a.post_weight != nullptr) t *= a.post_weight[e + i];
-                    if (a.channel_scale != nullptr) t *= a.channel_scale[e + i];
-                    h[p][i] = a.residual != nullptr ? rs[p].get(i) + t : t;
-                    sum = fmaf(h[p][i], h[p][i], sum);
-                }
+            for (int i = 0; i < VEC; ++i) {
+                const float t = cur.x[p].get(i) * inv_x, by = KEEP ? by_kept[KEEP ? p : 0][i] : now[i];
+                h[p][i] = fmaf(t, by, a.residual != nullptr ? cur.r[p].get(i) : 0.0f);
             }
+            if ((p * RT + j) * VEC < a.C)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sum = fmaf(h[p][i], h[p][i], sum);
         }
         const float inv = 1.0f / sqrtf(row_sum<RT>(sum, sums, turn) * inv_c + a.eps);
 #pragma unroll
@@ -113,21 +161,28 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void residual_norm_kernel(Resi
             if (e >= a.C) continue;
             if (a.residual_out != nullptr) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) rs[p].set(i, h[p][i]);
-                rs[p].store(static_cast<RS*>(a.residual_out) + row * a.residual_out_row + e);
+                for (int i = 0; i < VEC; ++i) cur.r[p].set(i, h[p][i]);
+                cur.r[p].store(static_cast<RS*>(a.residual_out) + row * a.residual_out_row + e);
             }
+            float now[VEC];
+            if constexpr (!KEEP) weights(p, now);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) xs[p].set(i, h[p][i] * inv * (a.weight != nullptr ? a.weight[e + i] : 1.0f));
-            xs[p].store(static_cast<TS*>(a.out) + row * a.out_row + e);
+            for (int i = 0; i < VEC; ++i) cur.x[p].set(i, h[p][i] * inv * (KEEP ? w_kept[KEEP ? p : 0][i] : now[i]));
+            cur.x[p].store(static_cast<TS*>(a.out) + row * a.out_row + e);
         }
     }
+}
+
+// Blocks for `groups` of rows, each as many of them as any other or one less, `most` at most.
+unsigned even_blocks(long long groups, long long most) {
+    const long long rounds = (groups + most - 1) / most;
+    return (unsigned)((groups + rounds - 1) / rounds);
 }
 
 template <typename T, typename R, int RT, int P>
 hipError_t start_residual(const ResidualNormLaunch& a, hipStream_t stream) {
     constexpr int NT = RT < 256 ? 256 : RT, ROWS = NT / RT;
-    const long long blocks = std::min<long long>(((long long)a.N + ROWS - 1) / ROWS, kCUs * 8);
-    residual_norm_kernel<T, R, RT, P><<<(unsigned)blocks, NT, 0, stream>>>(a);
+    residual_norm_kernel<T, R, RT, P><<<even_blocks(((long long)a.N + ROWS - 1) / ROWS, kCUs * 1024 / NT), NT, 0, stream>>>(a);
     return hipGetLastError();
 }
 template <typename T, typename R>
@@ -136,58 +191,85 @@ hipError_t residual_for(const ResidualNormLaunch& a, hipStream_t stream) {
     if (pieces <= 64) return start_residual<T, R, 64, 1>(a, stream);
     if (pieces <= 256) return start_residual<T, R, 256, 1>(a, stream);
     if (pieces <= 512) return start_residual<T, R, 256, 2>(a, stream);
-    if (pieces <= 1024) return start_residual<T, R, 256, 4>(a, stream);
+    if (pieces <= 1024) return start_residual<T, R, 512, 2>(a, stream);
+    if (pieces <= 2048) return start_residual<T, R, 1024, 2>(a, stream);
     if (pieces <= 4096) return start_residual<T, R, 1024, 4>(a, stream);
-    return start_residual<T, R, 1024, 8>(a, stream);
+    if constexpr (sizeof(typename T::storage) == 4) return start_residual<T, R, 1024, 8>(a, stream);
+    return hipErrorInvalidValue;  // 32768 elements are 4096 pieces
 }
 
-// A head's row: L lanes of a wave, P pieces of 16 bytes each.
+// A head's row: L lanes of a wave, P pieces of 16 bytes each.  A block goes over rows with the next ones on their way.
 template <typename T, int L, int P>
-__global__ __launch_bounds__(256) void gated_norm_kernel(GatedNormLaunch a) {
+__global__ __launch_bounds__(256) void gated_norm_kernel(GatedNormLaunch a, uint32_t h_inverse) {
     using TS = typename T::storage;
     constexpr int VEC = 16 / sizeof(TS), ROWS = 256 / L;
     const int j = threadIdx.x % L;
     const float inv_v = 1.0f / (float)a.V;
     const unsigned rows = (unsigned)a.N * a.H, step = gridDim.x * ROWS;
-    // every lane goes round as often as its wave's first, so that all take part in the sums
-    for (unsigned first = blockIdx.x * ROWS; first < rows; first += step) {
-        const unsigned row = min(first + threadIdx.x / L, rows - 1), t = row / (unsigned)a.H, head = row - t * a.H;
-        const bool in = first + threadIdx.x / L < rows;
+    struct Row {
+        Piece<T> x[P], z[P];
+        TS* out;
+    };
+    // lanes past the last row read that one, so that no load stands in a branch
+    auto fetch = [&](unsigned first) {
+        const unsigned row = min(first + threadIdx.x / L, rows - 1);
+        unsigned t = a.H == 1 ? row : __umulhi(row, h_inverse);  // one too many at most, as h_inverse is 2^32 / H rounded up
+        t -= t * a.H > row;
+        const unsigned head = row - t * a.H;
         const TS* x = static_cast<const TS*>(a.x.p) + t * a.x.row + head * a.x.head;
         const TS* z = static_cast<const TS*>(a.gate.p) + t * a.gate.row + head * a.gate.head;
-        Piece<T> xs[P], zs[P];
+        Row y;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int e = (p * L + j) * VEC, at = e < a.V ? e : 0;
-            xs[p].v = *reinterpret_cast<const u32x4*>(x + at);
-            zs[p].v = *reinterpret_cast<const u32x4*>(z + at);
+            y.x[p].v = *reinterpret_cast<const u32x4*>(x + at);
+            y.z[p].v = *reinterpret_cast<const u32x4*>(z + at);
         }
+        y.out = static_cast<TS*>(a.out.p) + t * a.out.row + head * a.out.head;
+        return y;
+    };
+    unsigned first = blockIdx.x * ROWS;
+    Row next = fetch(first);
+    float w[P][VEC];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int e = (p * L + j) * VEC;
+        if (a.weight != nullptr) {
+            load_vector<VEC>(a.weight + (e < a.V ? e : 0), w[p]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[p][i] = 1.0f;
+        }
+    }
+    // every lane goes round as often as its wave's first, so that all take part in the sums
+    for (; first < rows; first += step) {
+        Row cur = next;
+        const bool in = first + threadIdx.x / L < rows;
+        if (first + step < rows) next = fetch(first + step);
         float y[P][VEC], act[P][VEC], sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const bool real = (p * L + j) * VEC < a.V;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float g = zs[p].get(i), s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+                const float g = cur.z[p].get(i), s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
                 act[p][i] = a.sigmoid ? s : g * s;
-                y[p][i] = xs[p].get(i);
+                y[p][i] = cur.x[p].get(i);
                 if (a.gate_first) y[p][i] *= act[p][i];
                 sum = real ? fmaf(y[p][i], y[p][i], sum) : sum;
             }
         }
         const float inv = a.no_norm ? 1.0f : 1.0f / sqrtf(group_sum<L>(sum) * inv_v + a.eps);
-        TS* out = static_cast<TS*>(a.out.p) + t * a.out.row + head * a.out.head;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int e = (p * L + j) * VEC;
             if (e >= a.V || !in) continue;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                float v = y[p][i] * inv;
-                if (a.weight != nullptr) v *= a.weight[e + i];
-                xs[p].set(i, a.gate_first ? v : v * act[p][i]);
+                const float v = y[p][i] * inv * w[p][i];
+                cur.x[p].set(i, a.gate_first ? v : v * act[p][i]);
             }
-            *reinterpret_cast<u32x4*>(out + e) = xs[p].v;
+            *reinterpret_cast<u32x4*>(cur.out + e) = cur.x[p].v;
         }
     }
 }
@@ -195,8 +277,8 @@ __global__ __launch_bounds__(256) void gated_norm_kernel(GatedNormLaunch a) {
 template <typename T, int L, int P>
 hipError_t start_gated(const GatedNormLaunch& a, hipStream_t stream) {
     constexpr int ROWS = 256 / L;
-    const long long blocks = std::min<long long>(((long long)a.N * a.H + ROWS - 1) / ROWS, kCUs * 32);
-    gated_norm_kernel<T, L, P><<<(unsigned)blocks, 256, 0, stream>>>(a);
+    const uint32_t h_inverse = (uint32_t)(((1ull << 32) + a.H - 1) / a.H);
+    gated_norm_kernel<T, L, P><<<even_blocks(((long long)a.N * a.H + ROWS - 1) / ROWS, kCUs * 8), 256, 0, stream>>>(a, h_inverse);
     return hipGetLastError();
 }
 template <typename T>
