@@ -11,18 +11,26 @@ namespace {
 
 using namespace attn;
 
-constexpr int kShortRows = 64;
+// Whether a head's scales can be read several bytes at a time: as many heads' widths as there are kernels for have all
+// their blocks, and then only where every row starts at a multiple of that.
+bool wide_scales(const Fp4Cache& c, int D) {
+    const int n = std::min(D / 32, 4);
+    auto fits = [&](const HeadRows& x) { return reinterpret_cast<uintptr_t>(x.p) % n == 0 && x.row % n == 0 && x.head % n == 0; };
+    return (D == 64 || D == 128 || D == 256) && fits(c.k.scales) && fits(c.v.scales);
+}
 
 struct Plan {
     Fp4Args f;
     bool is_short, join;
-    int dp, rt, bm, lds;
+    int dp, rt, bm;
+    bool wide;
+    int lds;
     long long blocks;
     size_t bytes;
 };
 
 template <typename T>
-Plan plan(const AttnLaunch& c) {
+Plan plan(const AttnLaunch& c, bool wide) {
     Plan p{};
     Args& a = p.f.a;
     a.c = c;
@@ -33,21 +41,20 @@ Plan plan(const AttnLaunch& c) {
     a.set_rows = (long long)c.N * c.H;
     p.dp = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
     const long long rows = std::max(1ll, (long long)c.max_q * a.G);
-    p.is_short = rows <= kShortRows;
+    p.is_short = rows <= short_rows<T>(p.dp);
+    p.wide = wide;
     if (p.is_short) {
         p.rt = (int)(rows + 15) / 16;
         struct Tile {
-            int bm, unit, waves, lds;
+            int bm, unit, per_cu;
         };
-        const Tile s = with_short4<T>(p.dp, p.rt, [&](auto x) {
-            using C = typename decltype(x)::C;
-            return Tile{C::BM, C::UNIT, C::WAVES, C::lds((int)rows)};
+        const Tile s = with_short4<T>(p.dp, p.rt, wide, [&](auto c) {
+            using C = decltype(c);
+            return Tile{C::BM, C::UNIT, std::max(1, std::min(C::WAVES, kCULds / (C::LDS + 1280)))};
         });
         p.bm = s.bm;
-        p.lds = s.lds;
-        const int per_cu = std::max(1, std::min(s.waves, kCULds / (p.lds + 2048)));
         const long long units = c.HK * (c.kv_rows / s.unit + c.B);  // fewer blocks than that have work, bar overlapping runs
-        a.workers = (int)std::max(1ll, std::min((long long)kCUs * per_cu, units));
+        a.workers = (int)std::max(1ll, std::min((long long)kCUs * s.per_cu, units));
         p.join = c.N > 0 && a.workers > 1;
     } else {
         // row tiles and key parts as for a plain cache
@@ -84,20 +91,24 @@ Plan plan(const AttnLaunch& c) {
 
 template <typename T>
 hipError_t launch(const AttnLaunch& c, const Fp4Cache& cache, hipStream_t stream) {
-    Plan p = plan<T>(c);
+    Plan p = plan<T>(c, wide_scales(cache, c.D));
     p.f.cache = cache;
-    const hipError_t e = p.is_short ? start_short4<T>(p.f, p.dp, p.rt, p.lds, stream) : start_long4<T>(p.f, p.dp, p.blocks, p.lds, stream);
+    const hipError_t e = p.is_short ? start_short4<T>(p.f, p.dp, p.rt, p.wide, stream) : start_long4<T>(p.f, p.dp, p.blocks, p.lds, stream);
     return e != hipSuccess || !p.join ? e : start_join<T>(p.f.a, p.bm, -1, stream);
 }
 
 }  // namespace
 
+// Of the kernel for either way to read scales, as the query does not know the cache.
 size_t attention_fp4_workspace_bytes(const AttnLaunch& c) {
-    switch (c.dtype) {
-        case GDN_F32: return plan<F32>(c).bytes;
-        case GDN_BF16: return plan<BF16>(c).bytes;
-        default: return plan<F16>(c).bytes;
-    }
+    auto bytes = [&](bool wide) {
+        switch (c.dtype) {
+            case GDN_F32: return plan<F32>(c, wide).bytes;
+            case GDN_BF16: return plan<BF16>(c, wide).bytes;
+            default: return plan<F16>(c, wide).bytes;
+        }
+    };
+    return std::max(bytes(false), bytes(true));
 }
 
 hipError_t launch_attention_fp4(const AttnLaunch& c, const Fp4Cache& cache, hipStream_t stream) {
