@@ -11,6 +11,8 @@ namespace {
 
 using namespace attn;
 
+constexpr long long kWholeKeys = 4096;  // of a cache whose runs are not cut
+
 // Whether a head's scales can be read several bytes at a time: as many heads' widths as there are kernels for have all
 // their blocks, and then only where every row starts at a multiple of that.
 bool wide_scales(const Fp4Cache& c, int D) {
@@ -21,10 +23,8 @@ bool wide_scales(const Fp4Cache& c, int D) {
 
 struct Plan {
     Fp4Args f;
-    bool is_short, join;
-    int dp, rt, bm;
-    bool wide;
-    int lds;
+    bool is_short, whole, wide, join;  // whole: a block a run
+    int dp, tiles, bm, lds;
     long long blocks;
     size_t bytes;
 };
@@ -43,14 +43,17 @@ Plan plan(const AttnLaunch& c, bool wide) {
     const long long rows = std::max(1ll, (long long)c.max_q * a.G);
     p.is_short = rows <= short_rows<T>(p.dp);
     p.wide = wide;
+    p.f.g_inverse = 65536u / (uint32_t)a.G + 1;
+    p.tiles = (int)std::min(rows + 15, 64ll) / 16;
+    p.whole = p.tiles == 1 && c.kv_rows <= kWholeKeys && (long long)c.B * c.HK <= kCUs;
+    if (p.whole) return p;
     if (p.is_short) {
-        p.rt = (int)(rows + 15) / 16;
         struct Tile {
             int bm, unit, per_cu;
         };
-        const Tile s = with_short4<T>(p.dp, p.rt, wide, [&](auto c) {
+        const Tile s = with_short4<T>(p.dp, p.tiles, wide, [&](auto c) {
             using C = decltype(c);
-            return Tile{C::BM, C::UNIT, std::max(1, std::min(C::WAVES, kCULds / (C::LDS + 1280)))};
+            return Tile{C::BM, C::UNIT, std::max(1, std::min(C::WAVES * 4 / C::W, kCULds / (C::LDS + 1280)))};
         });
         p.bm = s.bm;
         const long long units = c.HK * (c.kv_rows / s.unit + c.B);  // fewer blocks than that have work, bar overlapping runs
@@ -93,7 +96,8 @@ template <typename T>
 hipError_t launch(const AttnLaunch& c, const Fp4Cache& cache, hipStream_t stream) {
     Plan p = plan<T>(c, wide_scales(cache, c.D));
     p.f.cache = cache;
-    const hipError_t e = p.is_short ? start_short4<T>(p.f, p.dp, p.rt, p.wide, stream) : start_long4<T>(p.f, p.dp, p.blocks, p.lds, stream);
+    if (p.whole) return start_whole4<T>(p.f, p.dp, p.wide, stream);
+    const hipError_t e = p.is_short ? start_short4<T>(p.f, p.dp, p.tiles, p.wide, stream) : start_long4<T>(p.f, p.dp, p.blocks, p.lds, stream);
     return e != hipSuccess || !p.join ? e : start_join<T>(p.f.a, p.bm, -1, stream);
 }
 

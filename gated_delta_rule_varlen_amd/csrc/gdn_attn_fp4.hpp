@@ -22,6 +22,7 @@ namespace attn {
 struct Fp4Args {
     Args a;
     Fp4Cache cache;
+    uint32_t g_inverse;  // floor(2^16 / G) + 1: r * g_inverse >> 16 is r / G for the short form's rows, as r * G < 2^16
 };
 
 // The kernel's argument, read again: what a loop does not need is not worth scalar registers across it (with all of it
@@ -91,15 +92,17 @@ __device__ __forceinline__ RowSums plain_row(const typename T::storage* q, const
 // T: the type of queries and outputs.  fp16 has operands in fp16, the others in bf16, where an fp32 query or probability is
 // the sum of three parts: their products with the cache's values, which are exact in bf16, are exact as well.
 // WIDE: a head's scales are read as many as fit 32 bits at a time, otherwise byte by byte.
-template <typename T_, int DP_, int RT_, int WAVES_, bool WIDE_>
+// KW x RG waves: of every 32 KW keys a wave takes 32, and of the rows the RT tiles of its group; the groups of a
+// wave's keys share their ring, and one asks for the keys, the other for the values.
+template <typename T_, int DP_, int RT_, int KW_, int RG_, int WAVES_, bool WIDE_>
 struct Cfg4 {
     using T = T_;
     using TS = typename T::storage;
     using OP = std::conditional_t<T::code == GDN_F16, F16, BF16>;
-    static constexpr int DP = DP_, RT = RT_, WAVES = WAVES_;  // WAVES: of a SIMD, which is blocks of a CU
+    static constexpr int DP = DP_, RT = RT_, KW = KW_, RG = RG_, WAVES = WAVES_;  // WAVES: of a SIMD
     static constexpr bool WIDE = WIDE_;
     static constexpr int PARTS = T::code == GDN_F32 ? 3 : 1;
-    static constexpr int W = 4, NT = 64 * W, BN = 32, UNIT = BN * W, BM = 16 * RT, NS = 2;
+    static constexpr int W = KW * RG, NT = 64 * W, BN = 32, UNIT = BN * KW, BM = 16 * RT * RG, NS = 2;
     static constexpr int CL = DP / 4 < 32 ? DP / 4 : 32;  // neighbouring elements a lane holds of a key
     static constexpr int KH = DP / (4 * CL);              // such pieces of a key
     static constexpr int STEPS = DP / 32, SPP = CL / 8;   // operand steps, and of a piece
@@ -108,12 +111,15 @@ struct Cfg4 {
     static constexpr int SB = WIDE ? (NB < 4 ? NB : 4) : 1, SLOTS = NB / SB;  // scales of a 32-bit place in LDS, places of a row
     static constexpr int CODES = BN * RB, CN = CODES / 1024, RPL = 1024 / RB; // bytes, loads, rows a load
     static constexpr int SN = (BN * SLOTS + 63) / 64, SCALES = 256 * SN;      // loads of scales, and their bytes in LDS
-    static constexpr int STAGE = 2 * (CODES + SCALES), LOADS = 2 * (CN + SN);
-    static constexpr bool QLDS = RT * PARTS > 1;          // queries in LDS: read once for two products
-    static constexpr int RING = NS * STAGE, QBYTES = QLDS ? RT * PARTS * STEPS * 1024 : 0;
+    static constexpr int STAGE = 2 * (CODES + SCALES), LOADS = 2 * (CN + SN) / RG;
+    static constexpr bool QLDS = RT * RG > 1;             // queries in LDS: read once for two products
+    static constexpr int RINGS = NS * KW * STAGE, QBYTES = QLDS ? RG * RT * PARTS * STEPS * 1024 : 0;
     static constexpr int ROW = DP + 4;                    // fp32 sums of a row in LDS
-    static constexpr int LDS = W * RING + QBYTES;
-    static_assert(W * 16 * ROW * 4 <= W * RING && LDS <= 159 * 1024, "the waves' sums take the ring's place");
+    static constexpr int STATS = KW * 16 * 8 + W * 4;     // the waves' maxima and sums of a tile's rows, and who met NaN
+    static constexpr int LDS = RINGS + QBYTES + STATS;
+    static_assert(RG <= 2 && 16 * ROW * 4 <= NS * STAGE, "the waves' sums take the rings' place");
+    // Rows whose sums fit the rings' second stage, while the next piece's first tile is on its way to the first.
+    static constexpr int EARLY = RT * RG == 1 ? STAGE / (ROW * 4) : 0;
     static constexpr float BIAS = T::code == GDN_F16 ? 4.0f : 0.0f, LAG = 8.0f;
     // Codes in LDS: 16-byte pieces (a block each) of key r at place piece ^ place_k(r), so that the 16 rows that are read
     // at a time lie in different banks; values in the order of row_of, so that four groups' rows are neighbours.
@@ -159,9 +165,9 @@ __device__ __forceinline__ float scale_at(uint32_t x, uint32_t at) {
 
 // 64 x BYTES to LDS, 32 bits a lane (zeros above) for fewer than 16 bytes, as load_to_lds of gdn_attn.hpp.
 template <int BYTES>
-__device__ __forceinline__ void stream_to_lds(const Range& s, uint32_t at, int voff, int soff) {
+__device__ __forceinline__ void stream_to_lds(u32x4 s, uint32_t at, int voff, int soff) {
     static_assert(BYTES == 1 || BYTES == 2 || BYTES == 4 || BYTES == 16, "bytes");
-#define GDN_LOAD(op) asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t" op " %1, %2, %3 offen nt lds" ::"s"(at), "v"(voff), "s"(s.r), "s"(soff) : "m0", "memory")
+#define GDN_LOAD(op) asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t" op " %1, %2, %3 offen nt lds" ::"s"(at), "v"(voff), "s"(s), "s"(soff) : "m0", "memory")
     if constexpr (BYTES == 16) GDN_LOAD("buffer_load_dwordx4");
     else if constexpr (BYTES == 4) GDN_LOAD("buffer_load_dword");
     else if constexpr (BYTES == 2) GDN_LOAD("buffer_load_ushort");
@@ -178,31 +184,31 @@ struct Short4 {
     static constexpr int KO = C::RPL < 16 ? 2 : 1;  // loads after which the places of a key's pieces repeat
 
     char* lds;
-    char* ring;         // this wave's
-    uint32_t ring_at;   // its LDS address
-    int lane, wave, col, grp;
+    uint32_t lds_at;    // its LDS address
+    int lane, wave, keys_of, rows_of, col, grp;  // keys_of, rows_of: the wave's part of the keys and of the rows
     int kc_off[KO], vc_off, ks_off[SN], vs_off[SN];  // byte offsets of what the lane loads of a tile
     int krow, vrow;                              // bytes between rows of codes
-    uint32_t q[C::QLDS ? 1 : C::STEPS][4];
+    uint32_t q[C::QLDS ? 1 : PARTS][C::QLDS ? 1 : C::STEPS][4];
     Acc<16> o[RT][VD];
     float ref[RT], l[RT], c;
-    int vis[RT], vis_lo, vis_hi;
+    int vis[RT], vis_lo;
     bool spoiled;
 
     // One tensor of the run, from the wave's next tile on.
     struct Stream {
-        uint64_t at;
-        int step, full, tail;  // bytes to the wave's next tile; of 32 rows; of the rows of the last, shorter tile
-        __device__ __forceinline__ void open(const char* p, int j0, int rows, long long stride, int width) {
-            at = (uint64_t)uniform((long long)(reinterpret_cast<uint64_t>(p) + j0 * stride));
-            step = C::UNIT * (int)stride;
-            full = (C::BN - 1) * (int)stride + width;
-            tail = uniform(rows > 0 ? (rows - 1) * (int)stride + width : 0);
+        u32x4 r;
+        int step, tail;  // bytes to the wave's next tile, and of the rows of the last, shorter one
+        __device__ __forceinline__ void open(const HeadRows& x, long long row, int hk, int rows, int width) {
+            const uint64_t at = (uint64_t)uniform((long long)(reinterpret_cast<uint64_t>(x.p) + row * x.row + hk * x.head));
+            const int stride = (int)x.row;
+            r = u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)uniform((C::BN - 1) * stride + width), (uint32_t)kRsrc};
+            step = uniform(C::UNIT * stride);
+            tail = uniform(rows > 0 ? (rows - 1) * stride + width : 0);
         }
-        __device__ __forceinline__ Range tile(int left) {
-            Range r(reinterpret_cast<const void*>(at), uniform(left >= C::BN ? full : left > 0 ? tail : 0));
-            at += (uint64_t)(int64_t)step;
-            return r;
+        __device__ __forceinline__ void advance() {
+            const uint64_t at = ((uint64_t)r[1] << 32 | r[0]) + (uint32_t)step;
+            r[0] = (uint32_t)at;
+            r[1] = (uint32_t)(at >> 32);
         }
     };
     Stream kc, ks, vc, vs;
@@ -212,13 +218,14 @@ struct Short4 {
         const Fp4Args& f = args_again();
         lane = threadIdx.x & 63;
         wave = uniform((int)threadIdx.x >> 6);
+        keys_of = C::RG == 1 ? wave : wave % C::KW;
+        rows_of = C::RG == 1 ? 0 : wave / C::KW;
         col = lane & 15;
         grp = lane >> 4;
         c = f.a.s2;
         krow = (int)f.cache.k.codes.row;
         vrow = (int)f.cache.v.codes.row;
-        ring = lds + wave * C::RING;
-        ring_at = uniform((int)(uintptr_t)(__attribute__((address_space(3))) char*)ring);
+        lds_at = uniform((int)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
         const int D = f.a.c.D, in_load = lane / C::NB, piece = lane % C::NB;
 #pragma unroll
         for (int j = 0; j < KO; ++j) {
@@ -234,50 +241,65 @@ struct Short4 {
             vs_off[j] = in ? C::row_of(row) * (int)f.cache.v.scales.row + slot * C::SB : kOutside;
         }
     }
+    static __device__ __forceinline__ int ring(int stage, int keys) { return (stage * C::KW + keys) * C::STAGE; }
 
-    // The wave's tile of every unit from t0 on, of a run of n rows; nothing from unit t1 on.
-    __device__ __forceinline__ void open(const Fp4Args& f, const Fp4Keys& s, int t0, int t1, int n) {
-        const int j0 = t0 * C::UNIT + wave * C::BN, end = min(n, t1 * C::UNIT), D = f.a.c.D;
-        left = uniform(end - j0);
+    // The wave's tile of every unit from t0 on, of a run of n rows that begins at `begin`; nothing from unit t1 on.
+    __device__ __forceinline__ void open(const Fp4Args& f, long long begin, int hk, int t0, int t1, int n) {
+        const int j0 = t0 * C::UNIT + keys_of * C::BN, D = f.a.c.D;
+        left = uniform(min(n, t1 * C::UNIT) - j0);
         const int tail = left & (C::BN - 1);  // of the one tile that may be shorter, if it is this wave's
-        kc.open(s.kc, j0, tail, f.cache.k.codes.row, D / 2);
-        ks.open(s.ks, j0, tail, f.cache.k.scales.row, D / 32);
-        vc.open(s.vc, j0, tail, f.cache.v.codes.row, D / 2);
-        vs.open(s.vs, j0, tail, f.cache.v.scales.row, D / 32);
+        kc.open(f.cache.k.codes, begin + j0, hk, tail, D / 2);
+        ks.open(f.cache.k.scales, begin + j0, hk, tail, D / 32);
+        vc.open(f.cache.v.codes, begin + j0, hk, tail, D / 2);
+        vs.open(f.cache.v.scales, begin + j0, hk, tail, D / 32);
     }
     // Asks for the next tile.  Who read this stage before is done: the wait is for its reads.
     __device__ __forceinline__ void ask(int stage) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        const uint32_t to = ring_at + stage * C::STAGE;
-        const Range rk = kc.tile(left), rks = ks.tile(left), rv = vc.tile(left), rvs = vs.tile(left);
-#pragma unroll
-        for (int j = 0; j < CN; ++j) stream_to_lds<16>(rk, to + j * 1024, kc_off[j % KO], j * C::RPL * krow);
-#pragma unroll
-        for (int j = 0; j < SN; ++j) stream_to_lds<C::SB>(rks, to + 2 * C::CODES + j * 256, ks_off[j], 0);
-#pragma unroll
-        for (int j = 0; j < CN; ++j) {
-            // rows of 16 lie one behind the other in eights: places 8 .. 15 are two rows further
-            const int rows = C::RPL >= 16 ? j * C::RPL : j / 2 * 16 + j % 2 * 2;
-            stream_to_lds<16>(rv, to + C::CODES + j * 1024, vc_off, rows * vrow);
+        if (left < C::BN) {
+            kc.r[2] = left > 0 ? kc.tail : 0;
+            ks.r[2] = left > 0 ? ks.tail : 0;
+            vc.r[2] = left > 0 ? vc.tail : 0;
+            vs.r[2] = left > 0 ? vs.tail : 0;
         }
+        const uint32_t to = lds_at + ring(stage, keys_of);
+        if (C::RG == 1 || rows_of == 0) {
 #pragma unroll
-        for (int j = 0; j < SN; ++j) stream_to_lds<C::SB>(rvs, to + 2 * C::CODES + C::SCALES + j * 256, vs_off[j], 0);
+            for (int j = 0; j < CN; ++j) stream_to_lds<16>(kc.r, to + j * 1024, kc_off[j % KO], j * C::RPL * krow);
+#pragma unroll
+            for (int j = 0; j < SN; ++j) stream_to_lds<C::SB>(ks.r, to + 2 * C::CODES + j * 256, ks_off[j], 0);
+            kc.advance();
+            ks.advance();
+        }
+        if (C::RG == 1 || rows_of == 1) {
+#pragma unroll
+            for (int j = 0; j < CN; ++j) {
+                // rows of 16 lie one behind the other in eights: places 8 .. 15 are two rows further
+                const int rows = C::RPL >= 16 ? j * C::RPL : j / 2 * 16 + j % 2 * 2;
+                stream_to_lds<16>(vc.r, to + C::CODES + j * 1024, vc_off, rows * vrow);
+            }
+#pragma unroll
+            for (int j = 0; j < SN; ++j) stream_to_lds<C::SB>(vs.r, to + 2 * C::CODES + C::SCALES + j * 256, vs_off[j], 0);
+            vc.advance();
+            vs.advance();
+        }
         left -= C::UNIT;
     }
 
     // The queries of the sequence's rows, eight elements a step in the order of the keys' pieces; in LDS each wave
     // leaves a part of them.
-    __device__ __forceinline__ void take_rows(const Args& a, int rows, long long first, int hk) {
+    __device__ __forceinline__ void take_rows(const Fp4Args& f, int rows, long long first, int hk) {
+        const Args& a = f.a;
         const int G = a.G;
         const uint32_t flip = a.negate ? 0x80008000u : 0u;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const int r = 16 * rt + col, i = r / G, g = r - i * G;
+            const int r = 16 * (rows_of * RT + rt) + col, i = (int)(r * f.g_inverse >> 16), g = r - i * G;
             const bool in = r < rows;
             const TS* p = static_cast<const TS*>(a.c.q.p) + (first + (in ? i : 0)) * a.c.q.row + (long long)(hk * G + (in ? g : 0)) * a.c.q.head;
 #pragma unroll
             for (int s = 0; s < C::STEPS; ++s) {
-                if (C::QLDS && (rt * C::STEPS + s) % C::W != wave) continue;
+                if (C::QLDS && (rt * C::STEPS + s) % C::KW != keys_of) continue;
                 const int e = s / C::SPP * 128 + C::CL * grp + s % C::SPP * 8;
                 const bool real = in && e < a.c.D;
                 const TS* at = p + (real ? e : 0);
@@ -300,7 +322,7 @@ struct Short4 {
                         *query_at(rt, z, s) = vec(w[z]);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) q[s][j] = w[0][j];
+                        for (int j = 0; j < 4; ++j) q[z][s][j] = w[z][j];
                     }
                 }
             }
@@ -312,23 +334,24 @@ struct Short4 {
         spoiled = false;
     }
     __device__ __forceinline__ u32x4* query_at(int rt, int part, int step) const {
-        return reinterpret_cast<u32x4*>(lds + C::W * C::RING + ((rt * PARTS + part) * C::STEPS + step) * 1024 + lane * 16);
+        return reinterpret_cast<u32x4*>(lds + C::RINGS + (((rows_of * RT + rt) * PARTS + part) * C::STEPS + step) * 1024 + lane * 16);
     }
-    // The keys each row sees: seen0 + its token, at least 0 and at most n.
-    __device__ __forceinline__ void see(int G, int rows, int seen0, int n) {
-        auto keys = [&](int r) { return min(max(seen0 + r / G, 0), n); };
+    // The keys each row sees: seen0 + its token, at least 0; the last token sees all n.
+    __device__ __forceinline__ void see(const Fp4Args& f, int rows, int seen0, int n) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) vis[rt] = 16 * rt + col < rows ? keys(16 * rt + col) : n;
-        vis_lo = uniform(keys(0));
-        vis_hi = uniform(keys(rows - 1));
+        for (int rt = 0; rt < RT; ++rt) {
+            const int r = 16 * (rows_of * RT + rt) + col;
+            vis[rt] = r < rows ? max(seen0 + (int)(r * f.g_inverse >> 16), 0) : n;
+        }
+        vis_lo = uniform(max(seen0, 0));
     }
 
     static __device__ __forceinline__ u32x4 vec(const uint32_t* x) { return u32x4{x[0], x[1], x[2], x[3]}; }
 
     // The tile at `stage`, keys j0 .. j0 + 31 of a run of n, against all rows.
     __device__ __forceinline__ void use(int stage, int j0, int n) {
-        if (j0 >= vis_hi) return;
-        const char* kt = ring + stage * C::STAGE;
+        if (j0 >= n) return;
+        const char* kt = lds + ring(stage, keys_of);
         const char* vt = kt + C::CODES;
         const uint32_t* kst = reinterpret_cast<const uint32_t*>(kt + 2 * C::CODES);
         const uint32_t* vst = reinterpret_cast<const uint32_t*>(kt + 2 * C::CODES + C::SCALES);
@@ -366,7 +389,7 @@ struct Short4 {
                     for (int z = PARTS - 1; z >= 0; --z) {
                         u32x4 y;
                         if constexpr (C::QLDS) y = *query_at(rt, z, h * C::SPP + x);
-                        else y = vec(q[h * C::SPP + x]);
+                        else y = vec(q[z][h * C::SPP + x]);
 #pragma unroll
                         for (int u = 0; u < 2; ++u) multiply<OP, 16>(vec(w[u]), y, s[rt][u]);
                     }
@@ -447,25 +470,32 @@ struct Short4 {
         }
     }
 
-    // Units t0 .. t1 - 1 of the run, a tile on its way while another is used; the loads past the end have an empty range.
+    // Units t0 .. t1 - 1 of the run, the first of them asked for already: a tile on its way while another is used.  The loads
+    // past the end have an empty range.
     __device__ __forceinline__ void run(int t0, int t1, int n) {
         int stage = 0;
         for (int t = t0; t < t1; ++t) {
-            ask(stage ^ 1);
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");
-            use(stage, t * C::UNIT + wave * C::BN, n);
+            if constexpr (C::RG == 1) {
+                ask(stage ^ 1);
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");
+            } else {
+                wait_and_meet<0>();  // both groups' loads of this tile are there, and the other stage is free
+                ask(stage ^ 1);
+            }
+            use(stage, t * C::UNIT + keys_of * C::BN, n);
             stage ^= 1;
         }
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        wait_and_meet<0>();  // all waves are done with the rings
     }
 };
 
 // Where a piece's rows go: `slot` of the workspace, or out.
 template <typename C>
-__device__ __forceinline__ void put_row(const Args& a, long long first, int hk, int r, long long slot, float m, float sum, int e,
+__device__ __forceinline__ void put_row(const Fp4Args& f, long long first, int hk, int r, long long slot, float m, float sum, int e,
                                         f32x4 o) {
     using TS = typename C::TS;
-    const int i = r / a.G, h = hk * a.G + r - i * a.G;
+    const Args& a = f.a;
+    const int i = (int)(r * f.g_inverse >> 16), h = hk * a.G + r - i * a.G;
     if (slot >= 0) {
         const long long at = slot * C::BM + r;
         *reinterpret_cast<f32x4*>(a.slot_o + at * a.c.D + e) = o;
@@ -486,32 +516,35 @@ __device__ __forceinline__ void finish_piece(Short4<C>& b, const Run& run, long 
     const Fp4Args& f = args_again();
     const Args& a = f.a;
     const int rows = run.T * a.G;
-    __shared__ float2 ml[C::W][16];
-    __shared__ int spoiled[C::W];
-    float* const sums = reinterpret_cast<float*>(b.lds);
+    auto ml = reinterpret_cast<float2(*)[16]>(b.lds + C::RINGS + C::QBYTES);
+    int* const spoiled = reinterpret_cast<int*>(b.lds + C::RINGS + C::QBYTES + C::KW * 16 * 8);
+    float* const sums = reinterpret_cast<float*>(b.lds + (rows <= C::EARLY ? Short4<C>::ring(1, 0) : 0));
     const int most = min(rows, 16);  // rows of a tile in LDS
     bool again = false;
 #pragma unroll
-    for (int rt = 0; rt < C::RT; ++rt) {
-        const int here = min(rows - 16 * rt, 16);
-        if (rt > 0) {
+    for (int tile = 0; tile < C::RT * C::RG; ++tile) {
+        const int here = min(rows - 16 * tile, 16);
+        const int rt = tile % C::RT;
+        if (tile > 0) {
             if (here <= 0) break;
-            __syncthreads();  // the last tile's sums are read
+            wait_and_meet<63>();  // the last tile's sums are read
         }
-        const float l = over_row<16, false>(b.l[rt]);
-        if (b.col < here) {
-            if (b.grp == 0) ml[b.wave][b.col] = make_float2(b.ref[rt], l);
-            float* at = sums + (b.wave * most + b.col) * C::ROW;
+        if (b.rows_of == tile / C::RT) {
+            const float l = over_row<16, false>(b.l[rt]);
+            if (b.col < here) {
+                if (b.grp == 0) ml[b.keys_of][b.col] = make_float2(b.ref[rt], l);
+                float* at = sums + (b.keys_of * most + b.col) * C::ROW;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int y = 0; y < C::VD; y += 4)
-                    *reinterpret_cast<f32x4*>(at + C::VD * (4 * b.grp + i) + y) =
-                        f32x4{b.o[rt][y][i], b.o[rt][y + 1][i], b.o[rt][y + 2][i], b.o[rt][y + 3][i]};
+                    for (int y = 0; y < C::VD; y += 4)
+                        *reinterpret_cast<f32x4*>(at + C::VD * (4 * b.grp + i) + y) =
+                            f32x4{b.o[rt][y][i], b.o[rt][y + 1][i], b.o[rt][y + 2][i], b.o[rt][y + 3][i]};
+            }
         }
-        if (rt == 0 && b.lane == 0) spoiled[b.wave] = b.spoiled;
-        __syncthreads();
-        if (rt == 0)
+        if (tile == 0 && b.lane == 0) spoiled[b.wave] = b.spoiled;
+        wait_and_meet<63>();
+        if (tile == 0)
 #pragma unroll
             for (int w = 0; w < C::W; ++w) again |= spoiled[w] != 0;
         if (again) break;
@@ -520,15 +553,15 @@ __device__ __forceinline__ void finish_piece(Short4<C>& b, const Run& run, long 
             if (e >= a.c.D) continue;
             float m = ml[0][r].x, sum = 0.0f;
 #pragma unroll
-            for (int w = 1; w < C::W; ++w) m = fmaxf(m, ml[w][r].x);
+            for (int w = 1; w < C::KW; ++w) m = fmaxf(m, ml[w][r].x);
             f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < C::W; ++w) {
+            for (int w = 0; w < C::KW; ++w) {
                 const float by = __builtin_amdgcn_exp2f(ml[w][r].x - m);
                 sum = fmaf(ml[w][r].y, by, sum);
                 o += *reinterpret_cast<const f32x4*>(sums + (w * most + r) * C::ROW + e) * by;
             }
-            put_row<C>(a, run.first, run.hk, 16 * rt + r, slot, m, sum, e, o);
+            put_row<C>(f, run.first, run.hk, 16 * tile + r, slot, m, sum, e, o);
         }
     }
     if (again) {
@@ -540,7 +573,7 @@ __device__ __forceinline__ void finish_piece(Short4<C>& b, const Run& run, long 
             const int i = r / a.G, g = r - i * a.G, seen = min(max(run.n - run.T + 1 + i, 0), run.n);
             const TS* q = static_cast<const TS*>(a.c.q.p) + (run.first + i) * a.c.q.row + (long long)(run.hk * a.G + g) * a.c.q.head;
             const RowSums x = plain_row<typename C::T>(q, keys, f.cache, a.c.D, s2, run.t0 * C::UNIT, min(run.t1 * C::UNIT, seen));
-            if (4 * b.lane < a.c.D) put_row<C>(a, run.first, run.hk, r, slot, x.m, x.sum, 4 * b.lane, x.o);
+            if (4 * b.lane < a.c.D) put_row<C>(f, run.first, run.hk, r, slot, x.m, x.sum, 4 * b.lane, x.o);
         }
     }
 }
@@ -571,57 +604,101 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short4_kernel(Fp4Args) {
         run.b = uniform(run.b);
         run.t0 = (int)(u - uniform(base) * a.c.HK);
     }
-    auto open = [&] {
+    auto look_up = [&](Run& r) {
         const AttnLaunch& c = args_again().a.c;
-        run.first = uniform(entry(c.offsets, run.b));
-        run.T = uniform(entry(c.offsets, run.b + 1)) - run.first;
-        run.n = uniform(entry(c.kv_len, run.b));
-        run.begin = uniform((long long)entry(c.kv_begin, run.b));
-        run.tiles = All::of(run.T, run.n);
+        r.first = uniform(entry(c.offsets, r.b));
+        r.T = uniform(entry(c.offsets, r.b + 1)) - r.first;
+        r.n = uniform(entry(c.kv_len, r.b));
+        r.begin = uniform((long long)entry(c.kv_begin, r.b));
+        r.tiles = All::of(r.T, r.n);
     };
-    open();
+    look_up(run);
     run.hk = uniform(run.t0 / run.tiles);
     run.t0 -= run.hk * run.tiles;
     Short4<C> b(lds);
+    auto start = [&](Run& r, long long at) {  // asks for the first tile of the piece that begins at unit `at`
+        r.t1 = (int)min((long long)r.tiles, r.t0 + (u1 - at));
+        b.open(args_again(), r.begin, r.hk, r.t0, r.t1, r.n);
+        b.ask(0);
+    };
+    start(run, u);
     while (true) {
-        run.t1 = (int)min((long long)run.tiles, run.t0 + (u1 - u));
-        const bool whole = run.t1 - run.t0 == run.tiles;
         {
             const Fp4Args& f = args_again();
             const int rows = run.T * f.a.G;
-            b.open(f, fp4_keys(f.cache, run.begin, run.hk), run.t0, run.t1, run.n);
-            b.ask(0);
-            b.take_rows(f.a, rows, run.first, run.hk);
-            b.see(f.a.G, rows, run.n - run.T + 1, run.n);
+            b.take_rows(f, rows, run.first, run.hk);
+            b.see(f, rows, run.n - run.T + 1, run.n);
         }
         if constexpr (C::QLDS) wait_and_meet<63>();
         b.run(run.t0, run.t1, run.n);
-        wait_and_meet<63>();  // the sums take the place of all waves' rings
-        // a worker's slot 0: a run cut at the front; slot 1: a run that starts here and goes on in the next worker
-        finish_piece<C>(b, run, whole ? -1 : w * 2ll + (run.t0 == 0 ? 1 : 0));
+
         const Args& a = args_again().a;
-        if (run.t0 == 0) {
+        const long long next_u = u + run.t1 - run.t0;
+        Run next = run;
+        bool early = false;
+        if (next_u < u1) {
+            next.t0 = 0;
+            if (++next.hk == a.c.HK) {
+                next.hk = 0;
+                do {
+                    ++next.b;
+                    look_up(next);
+                } while (next.tiles == 0);
+            }
+            early = run.T * a.G <= C::EARLY;
+            if (early) start(next, next_u);
+        }
+        // a worker's slot 0: a run cut at the front; slot 1: a run that starts here and goes on in the next worker
+        const bool whole = run.t1 - run.t0 == run.tiles;
+        finish_piece<C>(b, run, whole ? -1 : w * 2ll + (run.t0 == 0 ? 1 : 0));
+        if (run.t0 == 0 && (a.row_info != nullptr || !whole)) {
             const int pieces = whole ? 1 : Cut(total, W).part(u + run.tiles - 1) - w + 1;
             if (a.row_info != nullptr)
                 for (int i = threadIdx.x; i < run.T; i += C::NT)
                     a.row_info[(long long)(run.first + i) * a.c.HK + run.hk] = make_int2(whole ? -1 : w, pieces * 128 + i);
             if (!whole && a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(run.first, run.T, run.hk, pieces);
         }
-        u += run.t1 - run.t0;
-        if (u >= u1) {
+        if (next_u >= u1) {
             if ((whole || run.t0 != 0) && a.cut != nullptr && threadIdx.x == 0) a.cut[w] = make_int4(0, 0, 0, 0);
             return;
         }
-        run.t0 = 0;
-        if (++run.hk == a.c.HK) {
-            run.hk = 0;
-            do {
-                ++run.b;
-                open();
-            } while (run.tiles == 0);
-        }
-        __syncthreads();  // the piece's sums are read
+        u = next_u;
+        run = next;
+        wait_and_meet<63>();  // the piece's sums are read
+        if (!early) start(run, u);
     }
+}
+
+// A block a run, for short ones: nothing is cut, and no second launch joins anything.
+template <typename C>
+__global__ __launch_bounds__(C::NT, C::WAVES) void runs4_kernel(Fp4Args) {
+    extern __shared__ __align__(1024) char lds[];
+    const Fp4Args& f = args_again();
+    const AttnLaunch& c = f.a.c;
+    Run run;
+    run.b = blockIdx.x / c.HK;
+    run.hk = blockIdx.x - run.b * c.HK;
+    const Sequence s = sequence(c, run.b);  // in bounds, whatever the arrays hold
+    run.first = s.first, run.T = s.T, run.n = s.n, run.begin = s.begin;
+    run.t0 = 0;
+    run.t1 = run.tiles = Tiles<C::UNIT>::of(run.T, run.n);
+    Short4<C> b(lds);
+    if (run.T > 0) {
+        b.open(f, run.begin, run.hk, 0, run.t1, run.n);
+        b.ask(0);
+    }
+    const bool malformed = check<C::NT>(c);
+    report(f.a, malformed, blockIdx.x);
+    if (malformed || run.T == 0) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        return;
+    }
+    const int rows = run.T * f.a.G;
+    b.take_rows(f, rows, run.first, run.hk);
+    b.see(f, rows, run.n - run.T + 1, run.n);
+    if constexpr (C::QLDS) wait_and_meet<63>();
+    b.run(0, run.t1, run.n);
+    finish_piece<C>(b, run, -1);
 }
 
 // The long form (prompts): gdn_attn.hpp's tiles, pipeline and products, with the keys and values of a tile widened on their way
@@ -852,39 +929,59 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void long4_kernel(Fp4Args f) {
     if (blk.spoiled) blk.redo4(to, keys, t0 * C::BN, max(0, min(t1 * C::BN, n)), seen0);
 }
 
-// Waves of a SIMD that the registers of a configuration leave room for.
-template <typename T, int DP, int RT>
+// Row tiles and waves of the short form, for `tiles` tiles of 16 rows.  Up to four tiles a wave (WAVES: of a SIMD, as the
+// registers leave room for); at width 256 two, and two groups of waves for more.  (40 rows over 64 caches of 1000 to 8000
+// keys, D 256: 90 us with three tiles a wave and one wave a SIMD.)
+template <typename T, int DP, int TILES>
 struct Short4For {
-    static constexpr int STATE = RT * (DP / 4 + 18) + (RT == 1 && T::code != GDN_F32 ? DP / 8 : 0) + DP / 8 + 40;
+    static constexpr bool F32IO = T::code == GDN_F32;
+    static constexpr int RG = DP == 256 && TILES > 2 && !F32IO ? 2 : 1, RT = RG == 2 ? 2 : TILES;
+    static constexpr int STATE = RT * (DP / 4 + 18) + (TILES == 1 ? DP / 8 * (F32IO ? 3 : 1) : 0) + DP / 8 + 40;
     static constexpr int WAVES = STATE <= 128 ? 4 : STATE <= 170 ? 3 : STATE <= 256 ? 2 : 1;
     template <bool WIDE>
-    using C = Cfg4<T, DP, RT, WAVES, WIDE>;
+    using C = Cfg4<T, DP, RT, 4, RG, WAVES, WIDE>;
+    // a block a run: as many waves as there are registers and LDS for
+    template <bool WIDE, int KW>
+    using Wide = Cfg4<T, DP, RT, KW, 1, KW / 4, WIDE>;
+    template <bool WIDE>
+    using Whole = std::conditional_t<DP < 256 && Wide<WIDE, 16>::LDS <= kMaxLds, Wide<WIDE, 16>,
+                                     std::conditional_t<Wide<WIDE, 8>::LDS <= kMaxLds, Wide<WIDE, 8>, Wide<WIDE, 4>>>;
 };
-
-template <typename T, int DP, typename F>
-auto with_row_tiles(int rt, F f) {
-    switch (rt) {
-        case 1: return f(Short4For<T, DP, 1>{});
-        case 2: return f(Short4For<T, DP, 2>{});
-        case 3: return f(Short4For<T, DP, 3>{});
-        default: return f(Short4For<T, DP, T::code == GDN_F32 && DP == 256 ? 3 : 4>{});
-    }
-}
-template <typename T, typename F>
-auto with_short4(int dp, int rt, bool wide, F f) {
-    auto g = [&](auto x) {
-        return wide ? f(typename decltype(x)::template C<true>{}) : f(typename decltype(x)::template C<false>{});
-    };
-    return dp == 64 ? with_row_tiles<T, 64>(rt, g) : dp == 128 ? with_row_tiles<T, 128>(rt, g) : with_row_tiles<T, 256>(rt, g);
-}
-// Rows of the short form at most: three row tiles of fp32 queries wider than 128 fill LDS, otherwise four.
+// Rows of the short form at most: the three parts of more than 48 fp32 queries wider than 128 do not fit LDS.
 template <typename T>
 constexpr int short_rows(int dp) {
     return T::code == GDN_F32 && dp == 256 ? 48 : 64;
 }
 
+template <typename T, int DP, typename F>
+auto with_row_tiles(int tiles, F f) {
+    switch (tiles) {
+        case 1: return f(Short4For<T, DP, 1>{});
+        case 2: return f(Short4For<T, DP, 2>{});
+        case 3: return f(Short4For<T, DP, 3>{});
+        default: return f(Short4For<T, DP, short_rows<T>(DP) / 16>{});
+    }
+}
+template <typename T, typename F>
+auto with_short4(int dp, int tiles, bool wide, F f) {
+    auto g = [&](auto x) {
+        return wide ? f(typename decltype(x)::template C<true>{}) : f(typename decltype(x)::template C<false>{});
+    };
+    return dp == 64 ? with_row_tiles<T, 64>(tiles, g) : dp == 128 ? with_row_tiles<T, 128>(tiles, g) : with_row_tiles<T, 256>(tiles, g);
+}
+// One tile of rows.
+template <typename T, typename F>
+auto with_whole4(int dp, bool wide, F f) {
+    auto g = [&](auto x) {
+        return wide ? f(typename decltype(x)::template Whole<true>{}) : f(typename decltype(x)::template Whole<false>{});
+    };
+    return dp == 64 ? g(Short4For<T, 64, 1>{}) : dp == 128 ? g(Short4For<T, 128, 1>{}) : g(Short4For<T, 256, 1>{});
+}
+
 template <typename T>
-hipError_t start_short4(const Fp4Args& f, int dp, int rt, bool wide, hipStream_t stream);
+hipError_t start_short4(const Fp4Args& f, int dp, int tiles, bool wide, hipStream_t stream);
+template <typename T>
+hipError_t start_whole4(const Fp4Args& f, int dp, bool wide, hipStream_t stream);
 
 template <typename T>
 hipError_t start_long4(const Fp4Args& f, int dp, long long blocks, int lds, hipStream_t stream);
@@ -899,11 +996,20 @@ hipError_t start_one_short4(const Fp4Args& f, hipStream_t stream) {
     static std::atomic<uint64_t> asked{0};
     return start_kernel(&short4_kernel<C>, asked, f, f.a.workers, C::NT, C::LDS, stream);
 }
+template <typename C>
+hipError_t start_one_whole4(const Fp4Args& f, hipStream_t stream) {
+    static std::atomic<uint64_t> asked{0};
+    return start_kernel(&runs4_kernel<C>, asked, f, (long long)f.a.c.B * f.a.c.HK, C::NT, C::LDS, stream);
+}
 
 #define GDN_ATTN_FP4_INSTANCES(T)                                                                                      \
     template <>                                                                                                        \
-    hipError_t start_short4<T>(const Fp4Args& f, int dp, int rt, bool wide, hipStream_t stream) {                      \
-        return with_short4<T>(dp, rt, wide, [&](auto c) { return start_one_short4<decltype(c)>(f, stream); });         \
+    hipError_t start_short4<T>(const Fp4Args& f, int dp, int tiles, bool wide, hipStream_t stream) {                   \
+        return with_short4<T>(dp, tiles, wide, [&](auto c) { return start_one_short4<decltype(c)>(f, stream); });      \
+    }                                                                                                                  \
+    template <>                                                                                                        \
+    hipError_t start_whole4<T>(const Fp4Args& f, int dp, bool wide, hipStream_t stream) {                              \
+        return with_whole4<T>(dp, wide, [&](auto c) { return start_one_whole4<decltype(c)>(f, stream); });             \
     }                                                                                                                  \
     template <>                                                                                                        \
     hipError_t start_long4<T>(const Fp4Args& f, int dp, long long blocks, int lds, hipStream_t stream) {               \
