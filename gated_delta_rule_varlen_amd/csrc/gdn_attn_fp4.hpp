@@ -8,8 +8,8 @@
 // element of the head: a lane reads the same few elements of eight keys, widens them, and swaps halves of registers between
 // two keys.
 //
-// A block's four waves take 32 keys each of every 128, each with a ring of its own and nothing shared until a run's end,
-// where their sums are joined through LDS.  All runs lie end to end and are cut into equal parts, one a block, as in the
+// A block's four waves take 32 keys each of every 128, each with places of its own in LDS and nothing shared until a run's
+// end, where their sums are joined.  Scales are asked for two tiles at a time, as a tile's are half a load.  All runs lie end to end and are cut into equal parts, one a block, as in the
 // short form there.
 #pragma once
 
@@ -93,7 +93,7 @@ __device__ __forceinline__ RowSums plain_row(const typename T::storage* q, const
 // the sum of three parts: their products with the cache's values, which are exact in bf16, are exact as well.
 // WIDE: a head's scales are read as many as fit 32 bits at a time, otherwise byte by byte.
 // KW x RG waves: of every 32 KW keys a wave takes 32, and of the rows the RT tiles of its group; the groups of a
-// wave's keys share their ring, and one asks for the keys, the other for the values.
+// wave's keys share their places in LDS, and one asks for the keys, the other for the values.
 template <typename T_, int DP_, int RT_, int KW_, int RG_, int WAVES_, bool WIDE_>
 struct Cfg4 {
     using T = T_;
@@ -110,15 +110,16 @@ struct Cfg4 {
     static constexpr int NB = DP / 32, RB = DP / 2;       // blocks and bytes of codes of a row
     static constexpr int SB = WIDE ? (NB < 4 ? NB : 4) : 1, SLOTS = NB / SB;  // scales of a 32-bit place in LDS, places of a row
     static constexpr int CODES = BN * RB, CN = CODES / 1024, RPL = 1024 / RB; // bytes, loads, rows a load
-    static constexpr int SN = (BN * SLOTS + 63) / 64, SCALES = 256 * SN;      // loads of scales, and their bytes in LDS
-    static constexpr int STAGE = 2 * (CODES + SCALES), LOADS = 2 * (CN + SN) / RG;
+    static constexpr int SN = SLOTS, SCALES = 256 * SN;   // loads of the scales of two tiles, and their bytes in LDS
+    static constexpr int STAGE = 2 * (CODES + SCALES);    // of a wave's keys: a tile's codes, and the scales of two
+    static constexpr int CODE_LOADS = 2 * CN / RG, SCALE_LOADS = 2 * SN / RG;  // of a wave
     static constexpr bool QLDS = RT * RG > 1;             // queries in LDS: read once for two products
-    static constexpr int RINGS = NS * KW * STAGE, QBYTES = QLDS ? RG * RT * PARTS * STEPS * 1024 : 0;
+    static constexpr int PLACES = NS * KW * STAGE, QBYTES = QLDS ? RG * RT * PARTS * STEPS * 1024 : 0;
     static constexpr int ROW = DP + 4;                    // fp32 sums of a row in LDS
     static constexpr int STATS = KW * 16 * 8 + W * 4;     // the waves' maxima and sums of a tile's rows, and who met NaN
-    static constexpr int LDS = RINGS + QBYTES + STATS;
-    static_assert(RG <= 2 && 16 * ROW * 4 <= NS * STAGE, "the waves' sums take the rings' place");
-    // Rows whose sums fit the rings' second stage, while the next piece's first tile is on its way to the first.
+    static constexpr int LDS = PLACES + QBYTES + STATS;
+    static_assert(RG <= 2 && 16 * ROW * 4 <= NS * STAGE, "the waves' sums take the tiles' place");
+    // Rows whose sums fit the second half, while the next piece's first tile is on its way to the first.
     static constexpr int EARLY = RT * RG == 1 ? STAGE / (ROW * 4) : 0;
     static constexpr float BIAS = T::code == GDN_F16 ? 4.0f : 0.0f, LAG = 8.0f;
     // Codes in LDS: 16-byte pieces (a block each) of key r at place piece ^ place_k(r), so that the 16 rows that are read
@@ -197,12 +198,12 @@ struct Short4 {
     // One tensor of the run, from the wave's next tile on.
     struct Stream {
         u32x4 r;
-        int step, tail;  // bytes to the wave's next tile, and of the rows of the last, shorter one
-        __device__ __forceinline__ void open(const HeadRows& x, long long row, int hk, int rows, int width) {
+        int step, tail;  // bytes to the next tile (or two), and of the rows where the run ends
+        __device__ __forceinline__ void open(const HeadRows& x, long long row, int hk, int tiles, int full, int rows, int width) {
             const uint64_t at = (uint64_t)uniform((long long)(reinterpret_cast<uint64_t>(x.p) + row * x.row + hk * x.head));
             const int stride = (int)x.row;
-            r = u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)uniform((C::BN - 1) * stride + width), (uint32_t)kRsrc};
-            step = uniform(C::UNIT * stride);
+            r = u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)uniform((full - 1) * stride + width), (uint32_t)kRsrc};
+            step = uniform(tiles * C::UNIT * stride);
             tail = uniform(rows > 0 ? (rows - 1) * stride + width : 0);
         }
         __device__ __forceinline__ void advance() {
@@ -235,41 +236,61 @@ struct Short4 {
         vc_off = piece * 32 < D ? C::row_of(in_load) * vrow + piece * 16 : kOutside;
 #pragma unroll
         for (int j = 0; j < SN; ++j) {
-            const int x = j * 64 + lane, row = x / C::SLOTS, slot = x % C::SLOTS;
-            const bool in = row < C::BN && slot * C::SB * 32 < D;
-            ks_off[j] = in ? row * (int)f.cache.k.scales.row + slot * C::SB : kOutside;
-            vs_off[j] = in ? C::row_of(row) * (int)f.cache.v.scales.row + slot * C::SB : kOutside;
+            const int x = j * 64 + lane, row = x / C::SLOTS % C::BN, slot = x % C::SLOTS, later = x / (C::SLOTS * C::BN) * C::UNIT;
+            const bool in = slot * C::SB * 32 < D;
+            ks_off[j] = in ? (later + row) * (int)f.cache.k.scales.row + slot * C::SB : kOutside;
+            vs_off[j] = in ? (later + C::row_of(row)) * (int)f.cache.v.scales.row + slot * C::SB : kOutside;
         }
     }
-    static __device__ __forceinline__ int ring(int stage, int keys) { return (stage * C::KW + keys) * C::STAGE; }
+    // Places in LDS: two halves, each the codes of a tile for every wave's keys and behind them the scales of two tiles.
+    static __device__ __forceinline__ int codes_at(int half, int keys) { return half * C::KW * C::STAGE + keys * 2 * C::CODES; }
+    static __device__ __forceinline__ int scales_at(int half, int keys) {
+        return half * C::KW * C::STAGE + C::KW * 2 * C::CODES + keys * 2 * C::SCALES;
+    }
 
     // The wave's tile of every unit from t0 on, of a run of n rows that begins at `begin`; nothing from unit t1 on.
     __device__ __forceinline__ void open(const Fp4Args& f, long long begin, int hk, int t0, int t1, int n) {
         const int j0 = t0 * C::UNIT + keys_of * C::BN, D = f.a.c.D;
         left = uniform(min(n, t1 * C::UNIT) - j0);
         const int tail = left & (C::BN - 1);  // of the one tile that may be shorter, if it is this wave's
-        kc.open(f.cache.k.codes, begin + j0, hk, tail, D / 2);
-        ks.open(f.cache.k.scales, begin + j0, hk, tail, D / 32);
-        vc.open(f.cache.v.codes, begin + j0, hk, tail, D / 2);
-        vs.open(f.cache.v.scales, begin + j0, hk, tail, D / 32);
+        kc.open(f.cache.k.codes, begin + j0, hk, 1, C::BN, tail, D / 2);
+        vc.open(f.cache.v.codes, begin + j0, hk, 1, C::BN, tail, D / 2);
+        // of two tiles: until the run's end where that is nearer
+        const int end = left & (2 * C::UNIT - 1);
+        ks.open(f.cache.k.scales, begin + j0, hk, 2, C::UNIT + C::BN, end, D / 32);
+        vs.open(f.cache.v.scales, begin + j0, hk, 2, C::UNIT + C::BN, end, D / 32);
     }
-    // Asks for the next tile.  Who read this stage before is done: the wait is for its reads.
-    __device__ __forceinline__ void ask(int stage) {
+    // Asks for the scales of the next two tiles.  Who read these places before is done: the wait is for its reads.
+    __device__ __forceinline__ void ask_scales(int half) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (left < C::UNIT + C::BN) {
+            ks.r[2] = left > 0 ? ks.tail : 0;
+            vs.r[2] = left > 0 ? vs.tail : 0;
+        }
+        const uint32_t to = lds_at + scales_at(half, keys_of);
+        if (C::RG == 1 || rows_of == 0) {
+#pragma unroll
+            for (int j = 0; j < SN; ++j) stream_to_lds<C::SB>(ks.r, to + j * 256, ks_off[j], 0);
+            ks.advance();
+        }
+        if (C::RG == 1 || rows_of == 1) {
+#pragma unroll
+            for (int j = 0; j < SN; ++j) stream_to_lds<C::SB>(vs.r, to + C::SCALES + j * 256, vs_off[j], 0);
+            vs.advance();
+        }
+    }
+    // Asks for the codes of the next tile.
+    __device__ __forceinline__ void ask_codes(int half) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         if (left < C::BN) {
             kc.r[2] = left > 0 ? kc.tail : 0;
-            ks.r[2] = left > 0 ? ks.tail : 0;
             vc.r[2] = left > 0 ? vc.tail : 0;
-            vs.r[2] = left > 0 ? vs.tail : 0;
         }
-        const uint32_t to = lds_at + ring(stage, keys_of);
+        const uint32_t to = lds_at + codes_at(half, keys_of);
         if (C::RG == 1 || rows_of == 0) {
 #pragma unroll
             for (int j = 0; j < CN; ++j) stream_to_lds<16>(kc.r, to + j * 1024, kc_off[j % KO], j * C::RPL * krow);
-#pragma unroll
-            for (int j = 0; j < SN; ++j) stream_to_lds<C::SB>(ks.r, to + 2 * C::CODES + j * 256, ks_off[j], 0);
             kc.advance();
-            ks.advance();
         }
         if (C::RG == 1 || rows_of == 1) {
 #pragma unroll
@@ -278,12 +299,14 @@ struct Short4 {
                 const int rows = C::RPL >= 16 ? j * C::RPL : j / 2 * 16 + j % 2 * 2;
                 stream_to_lds<16>(vc.r, to + C::CODES + j * 1024, vc_off, rows * vrow);
             }
-#pragma unroll
-            for (int j = 0; j < SN; ++j) stream_to_lds<C::SB>(vs.r, to + 2 * C::CODES + C::SCALES + j * 256, vs_off[j], 0);
             vc.advance();
-            vs.advance();
         }
         left -= C::UNIT;
+    }
+    // The first tile of a piece.
+    __device__ __forceinline__ void ask_first() {
+        ask_scales(0);
+        ask_codes(0);
     }
 
     // The queries of the sequence's rows, eight elements a step in the order of the keys' pieces; in LDS each wave
@@ -334,7 +357,7 @@ struct Short4 {
         spoiled = false;
     }
     __device__ __forceinline__ u32x4* query_at(int rt, int part, int step) const {
-        return reinterpret_cast<u32x4*>(lds + C::RINGS + (((rows_of * RT + rt) * PARTS + part) * C::STEPS + step) * 1024 + lane * 16);
+        return reinterpret_cast<u32x4*>(lds + C::PLACES + (((rows_of * RT + rt) * PARTS + part) * C::STEPS + step) * 1024 + lane * 16);
     }
     // The keys each row sees: seen0 + its token, at least 0; the last token sees all n.
     __device__ __forceinline__ void see(const Fp4Args& f, int rows, int seen0, int n) {
@@ -348,13 +371,14 @@ struct Short4 {
 
     static __device__ __forceinline__ u32x4 vec(const uint32_t* x) { return u32x4{x[0], x[1], x[2], x[3]}; }
 
-    // The tile at `stage`, keys j0 .. j0 + 31 of a run of n, against all rows.
-    __device__ __forceinline__ void use(int stage, int j0, int n) {
+    // The tile of the half `codes`, with the first or second scales of the half `scales`: keys j0 .. j0 + 31 of a run of n,
+    // against all rows.
+    __device__ __forceinline__ void use(int codes, int scales, int second, int j0, int n) {
         if (j0 >= n) return;
-        const char* kt = lds + ring(stage, keys_of);
+        const char* kt = lds + codes_at(codes, keys_of);
         const char* vt = kt + C::CODES;
-        const uint32_t* kst = reinterpret_cast<const uint32_t*>(kt + 2 * C::CODES);
-        const uint32_t* vst = reinterpret_cast<const uint32_t*>(kt + 2 * C::CODES + C::SCALES);
+        const uint32_t* kst = reinterpret_cast<const uint32_t*>(lds + scales_at(scales, keys_of)) + second * C::BN * C::SLOTS;
+        const uint32_t* vst = kst + C::SCALES / 4;
         Acc<16> s[RT][2];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = Acc<16>{};
@@ -470,22 +494,22 @@ struct Short4 {
         }
     }
 
-    // Units t0 .. t1 - 1 of the run, the first of them asked for already: a tile on its way while another is used.  The loads
-    // past the end have an empty range.
+    // Units t0 .. t1 - 1 of the run, the first of them asked for already: a tile on its way while another is used, and
+    // scales for two.  The loads past the end have an empty range.
     __device__ __forceinline__ void run(int t0, int t1, int n) {
-        int stage = 0;
-        for (int t = t0; t < t1; ++t) {
+        for (int t = 0; t < t1 - t0; ++t) {
+            const int half = t & 1;
+            // (RG = 2: both groups' loads of this tile are there, and the other half is free)
+            if constexpr (C::RG > 1) wait_and_meet<0>();
+            if (half) ask_scales((t >> 1 & 1) ^ 1);
+            ask_codes(half ^ 1);
             if constexpr (C::RG == 1) {
-                ask(stage ^ 1);
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");
-            } else {
-                wait_and_meet<0>();  // both groups' loads of this tile are there, and the other stage is free
-                ask(stage ^ 1);
+                if (half) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::CODE_LOADS + C::SCALE_LOADS) : "memory");
+                else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::CODE_LOADS) : "memory");
             }
-            use(stage, t * C::UNIT + keys_of * C::BN, n);
-            stage ^= 1;
+            use(half, t >> 1 & 1, half, (t0 + t) * C::UNIT + keys_of * C::BN, n);
         }
-        wait_and_meet<0>();  // all waves are done with the rings
+        wait_and_meet<0>();  // all waves are done with their places
     }
 };
 
@@ -516,9 +540,9 @@ __device__ __forceinline__ void finish_piece(Short4<C>& b, const Run& run, long 
     const Fp4Args& f = args_again();
     const Args& a = f.a;
     const int rows = run.T * a.G;
-    auto ml = reinterpret_cast<float2(*)[16]>(b.lds + C::RINGS + C::QBYTES);
-    int* const spoiled = reinterpret_cast<int*>(b.lds + C::RINGS + C::QBYTES + C::KW * 16 * 8);
-    float* const sums = reinterpret_cast<float*>(b.lds + (rows <= C::EARLY ? Short4<C>::ring(1, 0) : 0));
+    auto ml = reinterpret_cast<float2(*)[16]>(b.lds + C::PLACES + C::QBYTES);
+    int* const spoiled = reinterpret_cast<int*>(b.lds + C::PLACES + C::QBYTES + C::KW * 16 * 8);
+    float* const sums = reinterpret_cast<float*>(b.lds + (rows <= C::EARLY ? Short4<C>::codes_at(1, 0) : 0));
     const int most = min(rows, 16);  // rows of a tile in LDS
     bool again = false;
 #pragma unroll
@@ -619,7 +643,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short4_kernel(Fp4Args) {
     auto start = [&](Run& r, long long at) {  // asks for the first tile of the piece that begins at unit `at`
         r.t1 = (int)min((long long)r.tiles, r.t0 + (u1 - at));
         b.open(args_again(), r.begin, r.hk, r.t0, r.t1, r.n);
-        b.ask(0);
+        b.ask_first();
     };
     start(run, u);
     while (true) {
@@ -683,9 +707,11 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void runs4_kernel(Fp4Args) {
     run.t0 = 0;
     run.t1 = run.tiles = Tiles<C::UNIT>::of(run.T, run.n);
     Short4<C> b(lds);
-    if (run.T > 0) {
+    const int rows = run.T * f.a.G;
+    if (run.T > 0) {  // on their way while the call is checked
         b.open(f, run.begin, run.hk, 0, run.t1, run.n);
-        b.ask(0);
+        b.ask_first();
+        b.take_rows(f, rows, run.first, run.hk);
     }
     const bool malformed = check<C::NT>(c);
     report(f.a, malformed, blockIdx.x);
@@ -693,8 +719,6 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void runs4_kernel(Fp4Args) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         return;
     }
-    const int rows = run.T * f.a.G;
-    b.take_rows(f, rows, run.first, run.hk);
     b.see(f, rows, run.n - run.T + 1, run.n);
     if constexpr (C::QLDS) wait_and_meet<63>();
     b.run(0, run.t1, run.n);
@@ -947,19 +971,21 @@ struct Short4For {
     using Whole = std::conditional_t<DP < 256 && Wide<WIDE, 16>::LDS <= kMaxLds, Wide<WIDE, 16>,
                                      std::conditional_t<Wide<WIDE, 8>::LDS <= kMaxLds, Wide<WIDE, 8>, Wide<WIDE, 4>>>;
 };
-// Rows of the short form at most: the three parts of more than 48 fp32 queries wider than 128 do not fit LDS.
+// Rows of the short form at most: the three parts of more than 32 fp32 queries wider than 128 do not fit LDS beside byte by
+// byte scales, nor the registers.
 template <typename T>
 constexpr int short_rows(int dp) {
-    return T::code == GDN_F32 && dp == 256 ? 48 : 64;
+    return T::code == GDN_F32 && dp == 256 ? 32 : 64;
 }
 
 template <typename T, int DP, typename F>
 auto with_row_tiles(int tiles, F f) {
-    switch (tiles) {
+    constexpr int MOST = short_rows<T>(DP) / 16;
+    switch (std::min(tiles, MOST)) {
         case 1: return f(Short4For<T, DP, 1>{});
         case 2: return f(Short4For<T, DP, 2>{});
-        case 3: return f(Short4For<T, DP, 3>{});
-        default: return f(Short4For<T, DP, short_rows<T>(DP) / 16>{});
+        case 3: return f(Short4For<T, DP, std::min(3, MOST)>{});
+        default: return f(Short4For<T, DP, MOST>{});
     }
 }
 template <typename T, typename F>
