@@ -370,7 +370,7 @@ struct Cut {
     }
 };
 
-template <typename T_, int M_, int DP_, int WR_, int KT_, int NS_, int WAVES_>
+template <typename T_, int M_, int DP_, int WR_, int KT_, int NS_, int WAVES_, int QL_ = 10>
 struct Cfg {
     using T = T_;
     using TS = typename T::storage;
@@ -402,7 +402,7 @@ struct Cfg {
     static constexpr int PRE = RPI >= 16 ? 1 : 16 / RPI;  // after which the places of a row's pieces repeat
     // Operand steps of the queries that lie in LDS, behind the ring: at width 256 eight waves' share of the CU's
     // registers holds six (with ten in LDS a 16384-token prompt takes 1785 us, with seven and spills 2195)
-    static constexpr int QL = PADDED ? 10 : 0;
+    static constexpr int QL = PADDED ? QL_ : 0;
     static constexpr int RING = NS * STAGE, LDS = RING + QL * NW * 1024;
     static constexpr bool PIPE = RB <= 256;       // the registers hold two tiles' scores (long form)
     static_assert(CPR >= 8 && TILE % (LW * 1024) == 0 && RPI >= 1 && LDS <= 159 * 1024 && JN % PRE == 0, "tile");
@@ -1317,11 +1317,11 @@ struct Short {
     using C = Cfg<T, 16, DP, WR, 1, NS, 1>;
 };
 // Long form, 32 x 32 tiles, four waves (eight at width 256 in half precision, where they share the queries' place).
-template <typename T, int DP>
+template <typename T, int DP, int QL = 10>
 struct Long {
     static constexpr int WIDTH = DP;
     static constexpr int RB = DP * (int)sizeof(typename T::storage);
-    using C = Cfg<T, 32, DP, RB == 512 && sizeof(typename T::storage) == 2 ? 8 : 4, RB <= 256 ? 2 : 1, 2, RB <= 512 ? 2 : 1>;
+    using C = Cfg<T, 32, DP, RB == 512 && sizeof(typename T::storage) == 2 ? 8 : 4, RB <= 256 ? 2 : 1, 2, RB <= 512 ? 2 : 1, QL>;
 };
 
 // What the host needs to know of a configuration: tile sizes, bytes of the ring and of a row in LDS, threads.
@@ -1353,9 +1353,9 @@ template <typename T, typename R, typename F>
 R with_short(int dp, int wr, R none, F f) {
     return dp == 64 ? with_waves<T, 64>(wr, none, f) : dp == 128 ? with_waves<T, 128>(wr, none, f) : with_waves<T, 256>(wr, none, f);
 }
-template <typename T, typename F>
+template <typename T, int QL = 10, typename F>
 auto with_long(int dp, F f) {
-    return dp == 64 ? f(Long<T, 64>{}) : dp == 128 ? f(Long<T, 128>{}) : f(Long<T, 256>{});
+    return dp == 64 ? f(Long<T, 64, QL>{}) : dp == 128 ? f(Long<T, 128, QL>{}) : f(Long<T, 256, QL>{});
 }
 
 // Both forms in one launch: for the widths and waves whose blocks of either form fit a CU twice.

@@ -725,6 +725,10 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void runs4_kernel(Fp4Args) {
     finish_piece<C>(b, run, -1);
 }
 
+// Operand steps of the long form's queries in LDS at width 256: one more than over a plain cache, as codes on their way take
+// registers.
+constexpr int kQueriesInLds = 11;
+
 // The long form (prompts): gdn_attn.hpp's tiles, pipeline and products, with the keys and values of a tile widened on their way
 // to LDS: a thread loads the codes of a run of elements of one key and of one value, a tile ahead of their use, and writes
 // them as operands where the asynchronous loads of a plain cache would have put them.
@@ -740,19 +744,16 @@ struct Long4 : Block<C> {
         uint32_t codes[U / 8], scale;
     };
     const Fp4Cache& cache;
-    int row, run_at;        // the thread's row of a tile and its run of elements there
-    int kc_off, ks_off, vc_off, vs_off;
     Half k, v;
 
-    __device__ __forceinline__ Long4(const Fp4Args& f, char* lds) : B(f.a, lds), cache(f.cache) {
-        row = (int)threadIdx.x / UPR;
-        run_at = (int)threadIdx.x % UPR;
-        const int e = run_at * U;
-        const bool in = e < f.a.c.D;
-        kc_off = in ? row * (int)cache.k.codes.row + e / 2 : kOutside;
-        ks_off = in ? row * (int)cache.k.scales.row + e / 32 : kOutside;
-        vc_off = in ? row * (int)cache.v.codes.row + e / 2 : kOutside;
-        vs_off = in ? row * (int)cache.v.scales.row + e / 32 : kOutside;
+    __device__ __forceinline__ Long4(const Fp4Args& f, char* lds) : B(f.a, lds), cache(f.cache) {}
+    // What says the thread's row of a tile and its run of elements there.  At width 256 these are worked out where they are
+    // needed, as there are no registers to keep them (16384 tokens 2231 us with fifty spilled, so 1940); at width 128 that
+    // takes longer than keeping them (24748 tokens 1513 us and 1427).
+    static __device__ __forceinline__ int thread() {
+        int x = threadIdx.x;
+        if constexpr (C::DP == 256) asm volatile("" : "+v"(x));
+        return x;
     }
     __device__ __forceinline__ Rsrc rows_of(const char* p, int j0, int left, long long stride, int width) const {
         const int rows = min(left, C::BN);
@@ -764,20 +765,23 @@ struct Long4 : Block<C> {
         const Fp4Half& h = V ? cache.v : cache.k;
         const int j0 = real ? tile * C::BN : 0, left = real ? B::run_n - j0 : 0, D = B::a.c.D;
         const Rsrc rc = rows_of(V ? s.vc : s.kc, j0, left, h.codes.row, D / 2), rs = rows_of(V ? s.vs : s.ks, j0, left, h.scales.row, D / 32);
+        const int x = thread(), row = x / UPR, e = x % UPR * U;
+        const int c_off = e < D ? row * (int)h.codes.row + e / 2 : kOutside, s_off = e < D ? row * (int)h.scales.row + e / 32 : kOutside;
         Half& to = V ? v : k;
         if constexpr (U == 32) {
-            const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, V ? vc_off : kc_off, 0, 0));
+            const u32x4 y = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, c_off, 0, 0));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) to.codes[i] = x[i];
+            for (int i = 0; i < 4; ++i) to.codes[i] = y[i];
         } else {
-            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, V ? vc_off : kc_off, 0, 0));
-            to.codes[0] = x[0], to.codes[1] = x[1];
+            const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, c_off, 0, 0));
+            to.codes[0] = y[0], to.codes[1] = y[1];
         }
-        to.scale = __builtin_amdgcn_raw_buffer_load_b8(rs, V ? vs_off : ks_off, 0, 0);
+        to.scale = __builtin_amdgcn_raw_buffer_load_b8(rs, s_off, 0, 0);
     }
     // Writes them to a stage of the ring.
     template <bool V>
     __device__ __forceinline__ void put(int stage) {
+        const int tid = thread(), row = tid / UPR, run_at = tid % UPR;
         char* at = B::lds + stage * C::STAGE + (V ? C::KTILE + C::template row_at<C::VSTEP>(row) : C::template row_at<C::KSTEP>(row));
         const int sw = V ? C::place_v(row) : C::place_k(row);
         const Half& x = V ? v : k;
@@ -837,25 +841,28 @@ struct Long4 : Block<C> {
             B::template scores<true>(0, now);
             if (t0 >= full) B::hide(now, t0 * C::BN);
             top = B::largest(now);
-            auto ahead = [&](int at) {
-                wait_and_meet<63>();
+            // Widening stands behind the step's products: 24748 tokens over up to 7100 keys 1419 us, before them 1463.
+            auto later = [&](int at) {
                 put<true>(at ^ 1);
                 put<false>(at);
                 fetch<true>(s, t + 2, t + 2 < t1);
                 fetch<false>(s, t + 3, t + 3 < t1);
             };
             while (t + 2 < min(full, t1 - 1)) {
-                ahead(0);
+                wait_and_meet<63>();
                 B::template step<false, false>(0, t, now, next, top);
+                later(0);
                 ++t;
-                ahead(1);
+                wait_and_meet<63>();
                 B::template step<false, false>(1, t, next, now, top);
+                later(1);
                 ++t;
             }
             for (; t < t1 - 1; ++t) {
-                ahead(stage);
+                wait_and_meet<63>();
                 if (t >= full) B::look(B::lds + stage * C::STAGE + C::KTILE, t * C::BN);
                 B::template step<true, false>(stage, t, now, next, top);
+                later(stage);
 #pragma unroll
                 for (int x = 0; x < B::KT; ++x)
 #pragma unroll
@@ -1039,7 +1046,7 @@ hipError_t start_one_whole4(const Fp4Args& f, hipStream_t stream) {
     }                                                                                                                  \
     template <>                                                                                                        \
     hipError_t start_long4<T>(const Fp4Args& f, int dp, long long blocks, int lds, hipStream_t stream) {               \
-        return with_long<T>(dp, [&](auto p) { return start_one_long4<typename decltype(p)::C>(f, blocks, lds, stream); }); \
+        return with_long<T, kQueriesInLds>(dp, [&](auto p) { return start_one_long4<typename decltype(p)::C>(f, blocks, lds, stream); }); \
     }
 
 }  // namespace attn
