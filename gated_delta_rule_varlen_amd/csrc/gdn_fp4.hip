@@ -54,6 +54,42 @@ struct Eight {
     }
 };
 
+// Eight elements' values from their codes.
+template <typename T>
+__device__ __forceinline__ void widen(uint32_t codes, uint32_t scale, Eight<T>& y) {
+    float f[8];
+    fp4::values(codes, scale, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y.e[e] = from_f32<T>(f[e]);
+}
+
+// Codes of eight elements of a block, and the scale byte that the four threads of the block find together.
+template <typename T>
+__device__ __forceinline__ void narrow(const Eight<T>& y, uint32_t& codes, uint32_t& scale) {
+    float f[8];
+    uint32_t top = 0;  // bits of the largest element: NaN above infinity above all numbers
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[e] = to_f32<T>(y.e[e]);
+        top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+    }
+    top = max(top, (uint32_t)__float_as_uint(dpp<DPP_QUAD_XOR1>(__uint_as_float(top))));
+    top = max(top, (uint32_t)__float_as_uint(dpp<DPP_QUAD_XOR2>(__uint_as_float(top))));
+    // top = 1.m * 2^(E - 127) is at most 6 * 2^e = 1.5 * 2^(e + 2)
+    const bool finite = top < 0x7f800000u;
+    int byte = (int)(top >> 23) - 2 + ((top & 0x7fffffu) > 0x400000u);
+    byte = max(byte, T::code == GDN_F16 ? 127 - 23 : 1);
+    byte = min(byte, T::code == GDN_F16 ? 127 + 13 : 127 + 125);  // with 4 * 2^126 a value would pass the type
+    const float s = fp4::scale_of(finite ? byte : 127);
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[0], f[1], s, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], s, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4], f[5], s, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[6], f[7], s, 3);
+    codes = finite ? w : 0u;
+    scale = finite ? (uint32_t)byte : fp4::kNotANumber;
+}
+
 template <typename T, bool READ>
 __global__ __launch_bounds__(NT) void fp4_rows_kernel(Fp4RowsLaunch a, int tpb) {
     using TS = typename T::storage;
@@ -62,49 +98,46 @@ __global__ __launch_bounds__(NT) void fp4_rows_kernel(Fp4RowsLaunch a, int tpb) 
     const bool bad = rows_malformed(a, t0, t1, rows);
     report_status(a.dev_status, bad);
     if (bad) return;
-    const unsigned per_head = (unsigned)a.D / 8, per_half = a.HK * per_head, per_token = 2 * per_half, all = (t1 - t0) * per_token;
-    // a block of 32 elements is four neighbouring lanes, which go round together
-    for (unsigned x = threadIdx.x; x < all; x += NT) {
-        const unsigned i = x / per_token, in_token = x - i * per_token, half = in_token >= per_half, in_half = in_token - half * per_half;
-        const unsigned head = in_half / per_head, piece = in_half - head * per_head;
+    // A thread keeps its place in the token's row and goes over tokens, UNROLL of them on their way at a time; where a row has
+    // fewer places than the block has threads, several tokens at once.
+    constexpr int UNROLL = 4;
+    const int per_head = a.D / 8, per_half = a.HK * per_head, per_token = 2 * per_half, count = t1 - t0;
+    const int groups = max(NT / per_token, 1);
+    for (int x = threadIdx.x; x < (per_token < NT ? groups * per_token : per_token); x += NT) {
+        const int in_token = per_token < NT ? x % per_token : x, first = per_token < NT ? x / per_token : 0;
+        const bool half = in_token >= per_half;
+        const int in_half = half ? in_token - per_half : in_token, head = in_half / per_head, piece = in_half - head * per_head;
         const HeadRows& tok = half ? a.v : a.k;
         const Fp4Half& to = half ? a.cache.v : a.cache.k;
-        TS* at = static_cast<TS*>(tok.p) + (t0 + i) * tok.row + head * tok.head + piece * 8;
-        const long long row = rows[i];
-        uint32_t* codes = reinterpret_cast<uint32_t*>(static_cast<char*>(to.codes.p) + row * to.codes.row + head * to.codes.head) + piece;
-        uint8_t* scale = static_cast<uint8_t*>(to.scales.p) + row * to.scales.row + head * to.scales.head + piece / 4;
-        Eight<T> y;
-        float f[8];
-        if constexpr (READ) {
-            const uint32_t s = *scale;
-            fp4::values(*codes, s, f);
+        TS* const at = static_cast<TS*>(tok.p) + (long long)t0 * tok.row + head * tok.head + piece * 8;
+        char* const codes = static_cast<char*>(to.codes.p) + head * to.codes.head + piece * 4;
+        uint8_t* const scales = static_cast<uint8_t*>(to.scales.p) + head * to.scales.head + piece / 4;
+        for (int i0 = first; i0 < count; i0 += UNROLL * groups) {
+            Eight<T> y[UNROLL];
+            uint32_t w[UNROLL], byte[UNROLL];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y.e[e] = from_f32<T>(s == fp4::kNotANumber ? __uint_as_float(0x7fc00000u) : f[e]);
-            y.store(at);
-        } else {
-            y.load(at);
-            uint32_t top = 0;  // bits of the largest element: NaN above infinity above all numbers
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[e] = to_f32<T>(y.e[e]);
-                top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+            for (int u = 0; u < UNROLL; ++u) {
+                const int i = min(i0 + u * groups, count - 1);  // past the last token that one again
+                if constexpr (READ) {
+                    w[u] = *reinterpret_cast<const uint32_t*>(codes + rows[i] * to.codes.row);
+                    byte[u] = scales[rows[i] * to.scales.row];
+                } else {
+                    y[u].load(at + i * tok.row);
+                }
             }
-            top = max(top, (uint32_t)__float_as_uint(dpp<DPP_QUAD_XOR1>(__uint_as_float(top))));
-            top = max(top, (uint32_t)__float_as_uint(dpp<DPP_QUAD_XOR2>(__uint_as_float(top))));
-            // top = 1.m * 2^(E - 127) is at most 6 * 2^e = 1.5 * 2^(e + 2)
-            const bool finite = top < 0x7f800000u;
-            int byte = (int)(top >> 23) - 2 + ((top & 0x7fffffu) > 0x400000u);
-            byte = max(byte, T::code == GDN_F16 ? 127 - 23 : 1);
-            byte = min(byte, T::code == GDN_F16 ? 127 + 13 : 127 + 125);  // with 4 * 2^126 a value would pass the type
-            if (!finite) byte = fp4::kNotANumber;
-            const float s = fp4::scale_of(finite ? byte : 127);
-            uint32_t w = 0;
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[0], f[1], s, 0);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], s, 1);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4], f[5], s, 2);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[6], f[7], s, 3);
-            *codes = finite ? w : 0u;
-            if (piece % 4 == 0) *scale = (uint8_t)byte;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int i = i0 + u * groups;
+                if (i >= count) break;  // four neighbours go round together
+                if constexpr (READ) {
+                    widen<T>(w[u], byte[u], y[u]);
+                    y[u].store(at + i * tok.row);
+                } else {
+                    narrow<T>(y[u], w[u], byte[u]);
+                    *reinterpret_cast<uint32_t*>(codes + rows[i] * to.codes.row) = w[u];
+                    if (piece % 4 == 0) scales[rows[i] * to.scales.row] = (uint8_t)byte[u];
+                }
+            }
         }
     }
 }
@@ -114,7 +147,7 @@ hipError_t launch_rows(const Fp4RowsLaunch& a, hipStream_t stream) {
     // enough blocks to fill the chip, and enough tokens a block that the whole-call check is shared
     const long long per_token = 2ll * a.HK * a.D / 8;
     int tpb = 1;
-    while (tpb < MAX_TPB && tpb * per_token < 4 * NT && ((long long)a.N + tpb - 1) / tpb > 4 * kCUs) tpb *= 2;
+    while (tpb < MAX_TPB && (tpb * per_token < NT || ((long long)a.N + tpb - 1) / tpb > 4 * kCUs)) tpb *= 2;
     const long long blocks = std::max(1ll, ((long long)a.N + tpb - 1) / tpb);
     if (blocks * NT > kMaxThreads) return hipErrorInvalidConfiguration;
     if (a.read) fp4_rows_kernel<T, true><<<(unsigned)blocks, NT, 0, stream>>>(a, tpb);
