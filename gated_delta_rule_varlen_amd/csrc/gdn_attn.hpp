@@ -1353,9 +1353,9 @@ template <typename T, typename R, typename F>
 R with_short(int dp, int wr, R none, F f) {
     return dp == 64 ? with_waves<T, 64>(wr, none, f) : dp == 128 ? with_waves<T, 128>(wr, none, f) : with_waves<T, 256>(wr, none, f);
 }
-template <typename T, int QL = 10, typename F>
+template <typename T, typename F>
 auto with_long(int dp, F f) {
-    return dp == 64 ? f(Long<T, 64, QL>{}) : dp == 128 ? f(Long<T, 128, QL>{}) : f(Long<T, 256, QL>{});
+    return dp == 64 ? f(Long<T, 64>{}) : dp == 128 ? f(Long<T, 128>{}) : f(Long<T, 256>{});
 }
 
 // Both forms in one launch: for the widths and waves whose blocks of either form fit a CU twice.

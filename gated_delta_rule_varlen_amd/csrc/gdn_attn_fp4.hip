@@ -61,7 +61,7 @@ Plan plan(const AttnLaunch& c, bool wide) {
         p.join = c.N > 0 && a.workers > 1;
     } else {
         // row tiles and key parts as for a plain cache
-        const Shape s = with_long<T, kQueriesInLds>(p.dp, [](auto x) { return shape_of<typename decltype(x)::C>(); });
+        const Shape s = with_long4<T>(p.dp, [](auto x) { return shape_of<typename decltype(x)::C>(); });
         p.bm = s.bm;
         p.lds = s.ring;
         const long long most = (rows + s.bm - 1) / s.bm, slots = (long long)c.N * a.G / s.bm + c.B;

@@ -897,9 +897,171 @@ struct Long4 : Block<C> {
     }
 };
 
-// One block per key head, key part and tile of BM rows, as gdn_attn.hpp's long form.
+// The long form for fp32 queries up to width 128, on matrix instructions of bf16: queries and probabilities are sums of
+// three parts each (short form, Cfg4), and three of those products take less than half of the fp32 one's time.
 template <typename C>
-__global__ __launch_bounds__(C::NT, C::WAVES) void long4_kernel(Fp4Args f) {
+struct Long4Split : Long4<C> {
+    using B = Block<C>;
+    using L = Long4<C>;
+    using Scores = typename B::Scores;
+    static constexpr int PARTS = 3;
+    u32x4 parts[PARTS][C::CS];
+
+    __device__ __forceinline__ Long4Split(const Fp4Args& f, char* lds) : L(f, lds) {}
+
+    __device__ __forceinline__ const float* query(const typename B::To& to, int r) const {
+        const Args& a = B::a;
+        const int i = r / a.G, g = r - i * a.G;
+        return static_cast<const float*>(a.c.q.p) + (to.first + i) * a.c.q.row + (long long)(to.hk * a.G + g) * a.c.q.head;
+    }
+    __device__ __forceinline__ void load_rows(int row0, int rows, long long first, int hk) {
+        const int r = row0 + B::wave * B::M + B::col;
+        const bool in = r < rows;
+        const float* p = query(typename B::To{row0, rows, first, hk, -1, -1}, in ? r : row0);
+        const uint32_t flip = B::a.negate ? 0x80008000u : 0u;
+#pragma unroll
+        for (int s = 0; s < C::CS; ++s) {
+            const int e = (C::NG * s + B::grp) * 8;
+            const bool real = in && e < B::a.c.D;
+            const f32x4 x = *reinterpret_cast<const f32x4*>(p + (real ? e : 0)), y = *reinterpret_cast<const f32x4*>(p + (real ? e + 4 : 0));
+            const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[PARTS];
+                split2<BF16, PARTS>(v[2 * j], v[2 * j + 1], w, 1);
+#pragma unroll
+                for (int z = 0; z < PARTS; ++z) parts[z][s][j] = real ? w[z] ^ flip : 0u;
+            }
+        }
+        B::clear();
+    }
+    __device__ __forceinline__ void scores(int stage, Scores& acc) {
+        const char* kt = B::lds + stage * C::STAGE + C::template row_at<C::KSTEP>(B::col);
+#pragma unroll
+        for (int k = 0; k < B::KT; ++k) {
+            acc[k][0] = Acc<B::M>{};
+#pragma unroll
+            for (int x = 0; x < C::CS; ++x) {
+                const u32x4 f = *reinterpret_cast<const u32x4*>(kt + C::template row_at<C::KSTEP>(k * 32) + (((C::NG * x + B::grp) ^ C::place_k(B::col)) * 16));
+#pragma unroll
+                for (int z = PARTS - 1; z >= 0; --z) multiply<BF16, B::M>(f, parts[z][x], acc[k][0]);
+            }
+        }
+    }
+    __device__ __forceinline__ void product(const char* vt, const Scores& s) {
+#pragma unroll
+        for (int k = 0; k < B::KT; ++k)
+#pragma unroll
+            for (int z = 0; z < B::SN / 8; ++z) {
+                uint32_t p[PARTS][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split2<BF16, PARTS>(s[k][0][8 * z + 2 * e], s[k][0][8 * z + 2 * e + 1], &p[0][e], 4);
+#pragma unroll
+                for (int d = 0; d < B::DT; ++d) {
+                    const u32x4 v = B::values(vt, k, z, d);
+#pragma unroll
+                    for (int x = PARTS - 1; x >= 0; --x) multiply<BF16, B::M>(v, u32x4{p[x][0], p[x][1], p[x][2], p[x][3]}, B::o[d]);
+                }
+            }
+    }
+    // Tiles [t0, t1) of the run, one after the other: three products take long enough for the other wave of the SIMD.
+    template <typename F>
+    __device__ __forceinline__ bool run(const Fp4Keys& s, int t0, int t1, int full, F stop) {
+        B::fresh_addresses();
+        L::template fetch<false>(s, t0, true);
+        L::template fetch<true>(s, t0, true);
+        if (stop()) return false;
+        L::template put<false>(0);
+        L::template put<true>(0);
+        L::template fetch<false>(s, t0 + 1, t0 + 1 < t1);
+        L::template fetch<true>(s, t0 + 1, t0 + 1 < t1);
+        Scores cur;
+        for (int t = t0, stage = 0; t < t1; ++t, stage ^= 1) {
+            wait_and_meet<63>();
+            const char* vt = B::lds + stage * C::STAGE + C::KTILE;
+            scores(stage, cur);
+            if (t >= full) {
+                B::hide(cur, t * C::BN);
+                B::look(vt, t * C::BN);
+            }
+            B::follow(B::largest(cur));
+            B::exponentials(cur);
+            product(vt, cur);
+            L::template put<false>(stage ^ 1);
+            L::template put<true>(stage ^ 1);
+            L::template fetch<false>(s, t + 2, t + 2 < t1);
+            L::template fetch<true>(s, t + 2, t + 2 < t1);
+        }
+        return true;
+    }
+    // Where row r goes: fp32 sums, or fp32 outputs.
+    __device__ __forceinline__ float* place(const typename B::To& to, int r, float m, float sum, bool stats, float& by) const {
+        const Args& a = B::a;
+        const int i = r / a.G, h = to.hk * a.G + r - i * a.G;
+        const long long token_row = (to.first + i) * a.c.H + h;
+        by = 1.0f;
+        if (to.set >= 0) {
+            const long long at = to.set * a.set_rows + token_row;
+            if (stats) a.set_ml[at] = make_float2(m, sum);
+            return a.set_o + at * a.c.D;
+        }
+        by = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (stats && a.c.lse != nullptr) a.c.lse[token_row] = sum == 0.0f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(sum));
+        return static_cast<float*>(a.c.out.p) + (to.first + i) * a.c.out.row + h * a.c.out.head;
+    }
+    __device__ __forceinline__ void store(const typename B::To& to) {
+        const int r = to.row0 + B::wave * B::M + B::col;
+        if (r >= to.rows || B::spoiled) return;
+        float by;
+        float* p = place(to, r, B::ref, B::l, B::grp == 0, by) + 4 * B::grp;
+#pragma unroll
+        for (int d = 0; d < B::DT; ++d)
+#pragma unroll
+            for (int i = 0; i < C::EA / 4; ++i) {
+                const int e = B::M * d + 4 * C::NG * i;
+                if (e + 4 * B::grp < B::a.c.D)
+                    *reinterpret_cast<f32x4*>(p + e) = f32x4{B::o[d][4 * i], B::o[d][4 * i + 1], B::o[d][4 * i + 2], B::o[d][4 * i + 3]} * by;
+            }
+    }
+    __device__ __forceinline__ void redo4(const typename B::To& to, const Fp4Keys& s, int k0, int k1, int seen0) {
+        const Args& a = B::a;
+#pragma unroll 1
+        for (int x0 = 0; x0 < B::M; ++x0) {
+            const int r = to.row0 + B::wave * B::M + x0;
+            if (r >= to.rows) break;
+            const RowSums x = plain_row<F32>(query(to, r), s, L::cache, a.c.D, a.negate ? -a.s2 : a.s2, k0, min(k1, seen0 + r / a.G));
+            float by;
+            float* p = place(to, r, x.m, x.sum, B::lane == 0, by);
+            if (4 * B::lane < a.c.D) *reinterpret_cast<f32x4*>(p + 4 * B::lane) = x.o * by;
+        }
+    }
+};
+
+// Which of them, and its tiles: L is the block, C its configuration.
+template <typename T, int DP>
+struct Long4For {
+    using C = typename Long<T, DP, kQueriesInLds>::C;
+    using L = Long4<C>;
+};
+template <>
+struct Long4For<F32, 64> {
+    using C = typename Long<BF16, 64>::C;
+    using L = Long4Split<C>;
+};
+template <>
+struct Long4For<F32, 128> {
+    using C = typename Long<BF16, 128>::C;
+    using L = Long4Split<C>;
+};
+template <typename T, typename F>
+auto with_long4(int dp, F f) {
+    return dp == 64 ? f(Long4For<T, 64>{}) : dp == 128 ? f(Long4For<T, 128>{}) : f(Long4For<T, 256>{});
+}
+
+// One block per key head, key part and tile of BM rows, as gdn_attn.hpp's long form.
+template <typename X>
+__global__ __launch_bounds__(X::C::NT, X::C::WAVES) void long4_kernel(Fp4Args f) {
+    using C = typename X::C;
     extern __shared__ __align__(1024) char lds[];
     const Args& a = f.a;
     const unsigned block = blockIdx.x;
@@ -942,7 +1104,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void long4_kernel(Fp4Args f) {
     const int all = (reach + C::BN - 1) / C::BN;
     const int t0 = uniform((int)((long long)all * part / parts)), t1 = uniform((int)((long long)all * (part + 1) / parts));
 
-    Long4<C> blk(f, lds);
+    typename X::L blk(f, lds);
     blk.load_rows(row0, rows, first, hk);
     blk.see(row0, rows, true, seen0, n);
     const Fp4Keys keys = fp4_keys(f.cache, seq.begin, hk);
@@ -1019,10 +1181,10 @@ hipError_t start_whole4(const Fp4Args& f, int dp, bool wide, hipStream_t stream)
 template <typename T>
 hipError_t start_long4(const Fp4Args& f, int dp, long long blocks, int lds, hipStream_t stream);
 
-template <typename C>
+template <typename X>
 hipError_t start_one_long4(const Fp4Args& f, long long blocks, int lds, hipStream_t stream) {
     static std::atomic<uint64_t> asked{0};
-    return start_kernel(&long4_kernel<C>, asked, f, blocks, C::NT, lds, stream);
+    return start_kernel(&long4_kernel<X>, asked, f, blocks, X::C::NT, lds, stream);
 }
 template <typename C>
 hipError_t start_one_short4(const Fp4Args& f, hipStream_t stream) {
@@ -1046,7 +1208,7 @@ hipError_t start_one_whole4(const Fp4Args& f, hipStream_t stream) {
     }                                                                                                                  \
     template <>                                                                                                        \
     hipError_t start_long4<T>(const Fp4Args& f, int dp, long long blocks, int lds, hipStream_t stream) {               \
-        return with_long<T, kQueriesInLds>(dp, [&](auto p) { return start_one_long4<typename decltype(p)::C>(f, blocks, lds, stream); }); \
+        return with_long4<T>(dp, [&](auto x) { return start_one_long4<decltype(x)>(f, blocks, lds, stream); });        \
     }
 
 }  // namespace attn
