@@ -803,9 +803,10 @@ struct Long4 : Block<C> {
         }
     }
 
-    // Tiles [t0, t1) of the run, as Block::run.
+    // Tiles [t0, t1) of the run, as Block::run.  A wave without rows (`idle`) widens its share of every tile and leaves the matrix
+    // cores to the others.
     template <typename F>
-    __device__ __forceinline__ bool run(const Fp4Keys& s, int t0, int t1, int full, F stop) {
+    __device__ __forceinline__ bool run(const Fp4Keys& s, int t0, int t1, int full, bool idle, F stop) {
         B::fresh_addresses();
         int stage = 0, t = t0;
         fetch<false>(s, t0, true);
@@ -817,12 +818,16 @@ struct Long4 : Block<C> {
         fetch<true>(s, t0 + 1, t0 + 1 < t1);
         if constexpr (!C::PIPE) {
             Scores cur;
-            auto one = [&](auto hidden, int at) {
+            auto next = [&](int at) {
                 wait_and_meet<63>();
                 put<false>(at ^ 1);
                 put<true>(at ^ 1);
                 fetch<false>(s, t + 2, t + 2 < t1);
                 fetch<true>(s, t + 2, t + 2 < t1);
+            };
+            for (; idle && t < t1; ++t, stage ^= 1) next(stage);
+            auto one = [&](auto hidden, int at) {
+                next(at);
                 if (hidden.value) B::look(B::lds + at * C::STAGE + C::KTILE, t * C::BN);
                 B::template plain_step<hidden.value>(at, t, cur);
                 ++t;
@@ -838,9 +843,6 @@ struct Long4 : Block<C> {
             put<false>(1);
             fetch<false>(s, t0 + 2, t0 + 2 < t1);
             wait_and_meet<63>();
-            B::template scores<true>(0, now);
-            if (t0 >= full) B::hide(now, t0 * C::BN);
-            top = B::largest(now);
             // Widening stands behind the step's products: 24748 tokens over up to 7100 keys 1419 us, before them 1463.
             auto later = [&](int at) {
                 put<true>(at ^ 1);
@@ -848,6 +850,18 @@ struct Long4 : Block<C> {
                 fetch<true>(s, t + 2, t + 2 < t1);
                 fetch<false>(s, t + 3, t + 3 < t1);
             };
+            if (idle) {
+                for (; t < t1 - 1; ++t, stage ^= 1) {
+                    wait_and_meet<63>();
+                    later(stage);
+                }
+                wait_and_meet<63>();
+                wait_and_meet<63>();
+                return true;
+            }
+            B::template scores<true>(0, now);
+            if (t0 >= full) B::hide(now, t0 * C::BN);
+            top = B::largest(now);
             while (t + 2 < min(full, t1 - 1)) {
                 wait_and_meet<63>();
                 B::template step<false, false>(0, t, now, next, top);
@@ -966,7 +980,7 @@ struct Long4Split : Long4<C> {
     }
     // Tiles [t0, t1) of the run, one after the other: three products take long enough for the other wave of the SIMD.
     template <typename F>
-    __device__ __forceinline__ bool run(const Fp4Keys& s, int t0, int t1, int full, F stop) {
+    __device__ __forceinline__ bool run(const Fp4Keys& s, int t0, int t1, int full, bool idle, F stop) {
         B::fresh_addresses();
         L::template fetch<false>(s, t0, true);
         L::template fetch<true>(s, t0, true);
@@ -979,14 +993,16 @@ struct Long4Split : Long4<C> {
         for (int t = t0, stage = 0; t < t1; ++t, stage ^= 1) {
             wait_and_meet<63>();
             const char* vt = B::lds + stage * C::STAGE + C::KTILE;
-            scores(stage, cur);
-            if (t >= full) {
-                B::hide(cur, t * C::BN);
-                B::look(vt, t * C::BN);
+            if (!idle) {
+                scores(stage, cur);
+                if (t >= full) {
+                    B::hide(cur, t * C::BN);
+                    B::look(vt, t * C::BN);
+                }
+                B::follow(B::largest(cur));
+                B::exponentials(cur);
+                product(vt, cur);
             }
-            B::follow(B::largest(cur));
-            B::exponentials(cur);
-            product(vt, cur);
             L::template put<false>(stage ^ 1);
             L::template put<true>(stage ^ 1);
             L::template fetch<false>(s, t + 2, t + 2 < t1);
@@ -1110,7 +1126,7 @@ __global__ __launch_bounds__(X::C::NT, X::C::WAVES) void long4_kernel(Fp4Args f)
     const Fp4Keys keys = fp4_keys(f.cache, seq.begin, hk);
     if (t0 < t1) {
         const int full = uniform(max(0, min(n, seen0 + row0 / a.G)) / C::BN);
-        if (!blk.run(keys, t0, t1, full, stop)) return;
+        if (!blk.run(keys, t0, t1, full, row0 + blk.wave * C::M >= rows, stop)) return;
     } else if (stop()) {
         return;  // no keys at all
     }
