@@ -372,16 +372,17 @@ struct Short4 {
     static __device__ __forceinline__ u32x4 vec(const uint32_t* x) { return u32x4{x[0], x[1], x[2], x[3]}; }
 
     // The tile of the half `codes`, with the first or second scales of the half `scales`: keys j0 .. j0 + 31 of a run of n,
-    // against all rows.
+    // against the first ACT tiles of the wave's rows.
+    template <int ACT>
     __device__ __forceinline__ void use(int codes, int scales, int second, int j0, int n) {
-        if (j0 >= n) return;
+        if (ACT == 0 || j0 >= n) return;
         const char* kt = lds + codes_at(codes, keys_of);
         const char* vt = kt + C::CODES;
         const uint32_t* kst = reinterpret_cast<const uint32_t*>(lds + scales_at(scales, keys_of)) + second * C::BN * C::SLOTS;
         const uint32_t* vst = kst + C::SCALES / 4;
-        Acc<16> s[RT][2];
+        Acc<16> s[ACT + 1][2];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = Acc<16>{};
+        for (int rt = 0; rt < ACT; ++rt) s[rt][0] = s[rt][1] = Acc<16>{};
 #pragma unroll
         for (int h = 0; h < KH; ++h) {
             uint32_t k[2][C::CL / 8];
@@ -408,7 +409,7 @@ struct Short4 {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) w[u][j] = widen2<OP>(k[u][x], scale[u], j);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                for (int rt = 0; rt < ACT; ++rt)
 #pragma unroll
                     for (int z = PARTS - 1; z >= 0; --z) {
                         u32x4 y;
@@ -422,16 +423,16 @@ struct Short4 {
         const bool masked = j0 + C::BN > vis_lo;
         if (masked) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
+            for (int rt = 0; rt < ACT; ++rt) {
                 const int room = vis[rt] - j0 - 4 * grp;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s[rt][i / 4][i % 4] = 16 * (i / 4) + i % 4 >= room ? -INFINITY : s[rt][i / 4][i % 4];
             }
             asm volatile("");  // keeps this a branch: most tiles hide nothing
         }
-        uint32_t p[RT][PARTS][4];
+        uint32_t p[ACT + 1][PARTS][4];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
+        for (int rt = 0; rt < ACT; ++rt) {
             float top = s[rt][0][0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) top = fmaxf(top, s[rt][i / 4][i % 4]);
@@ -487,7 +488,7 @@ struct Short4 {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) z[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], half ? 0x07060302u : 0x05040100u);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                for (int rt = 0; rt < ACT; ++rt)
 #pragma unroll
                     for (int part = PARTS - 1; part >= 0; --part) multiply<OP, 16>(vec(z), vec(p[rt][part]), o[rt][y + half]);
             }
@@ -496,7 +497,8 @@ struct Short4 {
 
     // Units t0 .. t1 - 1 of the run, the first of them asked for already: a tile on its way while another is used, and
     // scales for two.  The loads past the end have an empty range.
-    __device__ __forceinline__ void run(int t0, int t1, int n) {
+    template <int ACT>
+    __device__ __forceinline__ void run_tiles(int t0, int t1, int n) {
         for (int t = 0; t < t1 - t0; ++t) {
             const int half = t & 1;
             // (RG = 2: both groups' loads of this tile are there, and the other half is free)
@@ -507,8 +509,15 @@ struct Short4 {
                 if (half) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::CODE_LOADS + C::SCALE_LOADS) : "memory");
                 else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::CODE_LOADS) : "memory");
             }
-            use(half, t >> 1 & 1, half, (t0 + t) * C::UNIT + keys_of * C::BN, n);
+            use<ACT>(half, t >> 1 & 1, half, (t0 + t) * C::UNIT + keys_of * C::BN, n);
         }
+    }
+    // With two groups of waves the second one may have no rows, or one tile of them.
+    __device__ __forceinline__ void run(int t0, int t1, int n, int rows) {
+        const int mine = rows - 16 * rows_of * RT;
+        if (C::RG == 1 || mine > 16) run_tiles<RT>(t0, t1, n);
+        else if (mine > 0) run_tiles<1>(t0, t1, n);
+        else run_tiles<0>(t0, t1, n);
         wait_and_meet<0>();  // all waves are done with their places
     }
 };
@@ -654,7 +663,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void short4_kernel(Fp4Args) {
             b.see(f, rows, run.n - run.T + 1, run.n);
         }
         if constexpr (C::QLDS) wait_and_meet<63>();
-        b.run(run.t0, run.t1, run.n);
+        b.run(run.t0, run.t1, run.n, run.T * args_again().a.G);
 
         const Args& a = args_again().a;
         const long long next_u = u + run.t1 - run.t0;
@@ -721,7 +730,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void runs4_kernel(Fp4Args) {
     }
     b.see(f, rows, run.n - run.T + 1, run.n);
     if constexpr (C::QLDS) wait_and_meet<63>();
-    b.run(0, run.t1, run.n);
+    b.run(0, run.t1, run.n, rows);
     finish_piece<C>(b, run, -1);
 }
 
