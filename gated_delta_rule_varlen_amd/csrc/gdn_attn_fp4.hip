@@ -11,7 +11,11 @@ namespace {
 
 using namespace attn;
 
-constexpr long long kWholeKeys = 4096;  // of a cache whose runs are not cut
+// A block a run, without a joining launch, where a run takes a block few steps: the cache has at most kWholeSteps of them a
+// sequence, and kWholeMost in all, as one sequence may hold nearly all of it.  (H 32, HK 8, D 128, 512 keys a step: eight
+// sequences of 500 keys 9.1 us, cut and joined 11.3, of 2000 keys 13.5 and 13.9, of 4000 19.6 and 16.7; one of 2000 12.9
+// and 11.6, of 8000 27 and 13.5.  H 16, HK 2, D 256, 256 keys a step: one of 500 keys 10.3 and 12.2, of 2000 17.4 and 12.9.)
+constexpr int kWholeSteps = 3, kWholeMost = 16;
 
 // Whether a head's scales can be read several bytes at a time: as many heads' widths as there are kernels for have all
 // their blocks, and then only where every row starts at a multiple of that.
@@ -45,7 +49,8 @@ Plan plan(const AttnLaunch& c, bool wide) {
     p.wide = wide;
     p.f.g_inverse = 65536u / (uint32_t)a.G + 1;
     p.tiles = (int)std::min(rows + 15, 64ll) / 16;
-    p.whole = p.tiles == 1 && c.kv_rows <= kWholeKeys && (long long)c.B * c.HK <= kCUs;
+    const long long step = with_whole4<T>(p.dp, wide, [](auto x) { return decltype(x)::UNIT; });
+    p.whole = p.tiles == 1 && c.kv_rows <= step * std::min<long long>((long long)c.B * kWholeSteps, kWholeMost) && (long long)c.B * c.HK <= kCUs;
     if (p.whole) return p;
     if (p.is_short) {
         struct Tile {
