@@ -102,7 +102,7 @@ gdn_status check_cache(const gdn_fp4_cache* c, int HK, int D, gdn::Fp4Cache* to)
     for (const auto& e : t) {
         const gdn_status st = strided_rows(e.p, e.stride, c->rows, HK, e.width, 1, e.align, e.to);
         if (st != GDN_OK) return st;
-        if (e.stride[0] > kMaxRowBytes) return GDN_ERR_OVERFLOW;
+        if (e.stride[0] > kMaxFp4RowBytes) return GDN_ERR_OVERFLOW;
     }
     return GDN_OK;
 }
@@ -116,7 +116,7 @@ gdn_status fp4_rows(const gdn_fp4_rows_desc* d, const void* k, const void* v, co
     if (d->flags != 0) return GDN_ERR_UNSUPPORTED;
     gdn::Fp4RowsLaunch a{};
     if ((st = check_cache(cache, d->HK, d->D, &a.cache)) != GDN_OK) return st;
-    if (d->N > INT_MAX - 4096) return GDN_ERR_OVERFLOW;
+    if (d->N > (1 << 27) - 8) return GDN_ERR_OVERFLOW;  // tokens of one launch
     if (kv_begin == nullptr && cache->rows < d->N) return GDN_ERR_SHAPE;  // rows are token indices
     if ((st = head_rows(k, d->k_stride, d->N, d->HK, d->D, d->dtype, &a.k)) != GDN_OK) return st;
     if ((st = head_rows(v, d->v_stride, d->N, d->HK, d->D, d->dtype, &a.v)) != GDN_OK) return st;

@@ -44,5 +44,6 @@ inline gdn_status head_rows(const void* p, const int64_t stride[2], long long ro
 }
 
 constexpr long long kMaxRowBytes = 4ll << 20;  // between two rows of a cache: 32-bit offsets inside a key tile
+constexpr long long kMaxFp4RowBytes = 1ll << 20;  // of a 4-bit one, of which 544 rows lie in one range
 
 }  // namespace gdn

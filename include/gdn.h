@@ -484,8 +484,8 @@ gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc *desc, size_t *byte
  *     code = the nearest to x / 2^e, ties to the even code, with the sign of x
  * A block with an infinity or NaN gets the scale byte 255 (and codes 0), and reads as NaN throughout.
  *
- * gdn_cache_read_fp4_varlen -- the way back: k_out[t], v_out[t] = what row kv_begin[b] + past[b] + i stands for (a scale of
- * 2^-127, which the write does not make, may read as zeros; in fp16 values round to fp16).
+ * gdn_cache_read_fp4_varlen -- the way back: k_out[t], v_out[t] = what row kv_begin[b] + past[b] + i stands for, rounded
+ * to the type where it is no number of it.
  *
  * gdn_attention_fp4_varlen -- gdn_attention_varlen with k and v the values of a cache: arguments, formula, masks and
  * errors as there (out = q included), except that kv_begin and kv_len are required, desc->prefix_len is 0, its strides of k,
@@ -493,12 +493,12 @@ gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc *desc, size_t *byte
  * the cache's values are operands in fp16: those of scales past 2^13 may be infinite.
  *
  * Tensors (element (row, head, j) at row*stride[0] + head*stride[1] + j, strides in bytes):
- *   k_codes, v_codes [rows, HK, D/2] uint8    16-byte aligned, strides multiples of 16 (GDN_ERR_ALIGN), rows at most 4 MiB
+ *   k_codes, v_codes [rows, HK, D/2] uint8    16-byte aligned, strides multiples of 16 (GDN_ERR_ALIGN), rows at most 1 MiB
  *   k_scales, v_scales [rows, HK, D/32] uint8   any alignment                       apart (GDN_ERR_OVERFLOW, both)
  *   k, v, k_out, v_out [N, HK, D] dtype       required unless N == 0, strides in elements, multiples of 16 bytes
  *   past [B] int32 NULL = zeros; kv_begin [B] int64
  * Constraints of the write and the read: B >= 1, N >= 0, HK >= 1, D a multiple of 32 up to 256 (GDN_ERR_SHAPE), strides not
- * negative, N and N*HK at most 2^31 - 4097 (GDN_ERR_OVERFLOW), no two tokens name one row of a write, inputs and
+ * negative, N at most 2^27 - 8 and N*HK at most 2^31 - 4097 (GDN_ERR_OVERFLOW), no two tokens name one row of a write, inputs and
  * outputs do not overlap.  Malformed offsets and rows outside [0, rows) of a sequence with tokens write nothing
  * (GDN_ERR_OFFSETS in *dev_status).
  * ---------------------------------------------------------------------------------------------- */

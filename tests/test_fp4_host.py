@@ -103,6 +103,8 @@ CACHE_REFUSALS = [
     (dict(v_scales_stride=(4, -2)), "ERR_SHAPE"),
     (dict(v_codes_stride=(2**23, 32)), "ERR_OVERFLOW"),  # rows 8 MiB apart
     (dict(k_scales_stride=(2**23, 2)), "ERR_OVERFLOW"),
+    (dict(v_codes_stride=(2**20 + 16, 32)), "ERR_OVERFLOW"),
+    (dict(v_scales_stride=(2**20 + 1, 2)), "ERR_OVERFLOW"),
     (dict(k_codes_stride=(64, 2**61)), "ERR_OVERFLOW"),
 ]
 
@@ -125,6 +127,7 @@ def test_rows_refuse_a_cache(abi, read, fields, want):
         (dict(D=288), {}, "ERR_SHAPE"),
         (dict(N=2**31 - 100, HK=1), {}, "ERR_OVERFLOW"),
         (dict(N=2**30, HK=2), {}, "ERR_OVERFLOW"),
+        (dict(N=2**27 - 7, HK=1), {}, "ERR_OVERFLOW"),
         (dict(dtype=3), {}, "ERR_DTYPE"),
         (dict(flags=1), {}, "ERR_UNSUPPORTED"),
         (dict(k_stride=(-128, 64)), {}, "ERR_SHAPE"),
