@@ -489,20 +489,19 @@ def cache_read_fp4_varlen(cache, offsets: torch.Tensor, *, N: Optional[int] = No
     """What a cache's rows stand for (gdn_cache_read_fp4_varlen): k, v [N, HK, D] of `dtype`, token i of sequence b from
     row kv_begin[b] + past[b] + i as in cache_write_fp4_varlen.  N is the number of tokens, offsets' last entry; k_out and
     v_out, if given, decide N and dtype.  Returns (k, v)."""
-    codes = cache[0]
     given = k_out if k_out is not None else v_out
-    if not isinstance(codes, torch.Tensor) or not (given is None or isinstance(given, torch.Tensor)):
-        raise TypeError("cache, k_out and v_out must be tensors")
     if given is None:
         if N is None:
             raise ValueError("N is required without k_out and v_out")
-        shape, like = (N, codes.shape[1], 2 * codes.shape[2]), dict(dtype=dtype, device=codes.device)
-    else:
-        shape, like = tuple(given.shape), dict(dtype=given.dtype, device=given.device)
-    if k_out is None:
-        k_out = torch.empty(shape, **like)
-    if v_out is None:
-        v_out = torch.empty(shape, **like)
+        st, k_out, v_out = (_native or _marshal()).fp4_read(cache, offsets, N, past, kv_begin, dtype, dev_status,
+                                                            _raw_stream(cache[0] if cache else None))
+        if st:
+            _check(st, "gdn_cache_read_fp4_varlen")
+        return k_out, v_out
+    if not isinstance(given, torch.Tensor):
+        raise TypeError("k_out and v_out must be tensors")
+    k_out = torch.empty_like(given, memory_format=torch.contiguous_format) if k_out is None else k_out
+    v_out = torch.empty_like(given, memory_format=torch.contiguous_format) if v_out is None else v_out
     st = (_native or _marshal()).fp4_rows(True, k_out, v_out, offsets, cache, past, kv_begin, dev_status, _raw_stream(k_out))
     if st:
         _check(st, "gdn_cache_read_fp4_varlen")

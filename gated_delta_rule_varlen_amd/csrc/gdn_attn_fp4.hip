@@ -44,13 +44,26 @@ Plan plan(const AttnLaunch& c, bool wide) {
     a.splits = 1;
     a.set_rows = (long long)c.N * c.H;
     p.dp = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
+    // Where a key head's rows are too many for the short form's registers (fp32, wider than 128), its query heads are divided
+    // among so many blocks that they are not: keys are read more than once, which bounds nothing there.  (26 sequences of
+    // 7 tokens and 131 keys, H 32, HK 4, D 160: 149 us in the long form, so 24.)
+    p.f.share = 1;
+    if (short_rows<T>(p.dp) < 64 && (long long)c.max_q * a.G <= 64) {
+        int share = 1;
+        while (share <= a.G && (a.G % share != 0 || (long long)c.max_q * (a.G / share) > short_rows<T>(p.dp))) ++share;
+        if (share <= a.G) {
+            p.f.share = share;
+            a.G /= share;
+            a.c.HK *= share;
+        }
+    }
     const long long rows = std::max(1ll, (long long)c.max_q * a.G);
     p.is_short = rows <= short_rows<T>(p.dp);
     p.wide = wide;
     p.f.g_inverse = 65536u / (uint32_t)a.G + 1;
     p.tiles = (int)std::min(rows + 15, 64ll) / 16;
     const long long step = with_whole4<T>(p.dp, wide, [](auto x) { return decltype(x)::UNIT; });
-    p.whole = p.tiles == 1 && c.kv_rows <= step * std::min<long long>((long long)c.B * kWholeSteps, kWholeMost) && (long long)c.B * c.HK <= kCUs;
+    p.whole = p.tiles == 1 && c.kv_rows <= step * std::min<long long>((long long)c.B * kWholeSteps, kWholeMost) && (long long)c.B * a.c.HK <= kCUs;
     if (p.whole) return p;
     if (p.is_short) {
         struct Tile {
@@ -61,7 +74,7 @@ Plan plan(const AttnLaunch& c, bool wide) {
             return Tile{C::BM, C::UNIT, std::max(1, std::min(C::WAVES * 4 / C::W, kCULds / (C::LDS + 1280)))};
         });
         p.bm = s.bm;
-        const long long units = c.HK * (c.kv_rows / s.unit + c.B);  // fewer blocks than that have work, bar overlapping runs
+        const long long units = a.c.HK * (c.kv_rows / s.unit + c.B);  // fewer blocks than that have work, bar overlapping runs
         a.workers = (int)std::max(1ll, std::min((long long)kCUs * s.per_cu, units));
         p.join = c.N > 0 && a.workers > 1;
     } else {
@@ -70,9 +83,9 @@ Plan plan(const AttnLaunch& c, bool wide) {
         p.bm = s.bm;
         p.lds = s.ring;
         const long long most = (rows + s.bm - 1) / s.bm, slots = (long long)c.N * a.G / s.bm + c.B;
-        const long long tiles = std::min(most * c.B, slots) * c.HK;
+        const long long tiles = std::min(most * c.B, slots) * a.c.HK;
         a.splits = (int)std::max(1ll, std::min(std::min((2 * kCUs + tiles - 1) / std::max(1ll, tiles), c.kv_rows / kPartKeys), 64ll));
-        p.blocks = slots * c.HK * a.splits;
+        p.blocks = slots * a.c.HK * a.splits;
         p.join = a.to_sets = a.splits > 1;
         a.sets = p.join ? a.splits : 0;
     }
@@ -88,7 +101,7 @@ Plan plan(const AttnLaunch& c, bool wide) {
         a.set_o = reinterpret_cast<float*>(take((size_t)a.sets * a.set_rows * c.D * 4));
         a.live = reinterpret_cast<int*>(take((size_t)c.N * 4));
     } else if (p.join) {
-        if (few_rows(a)) a.row_info = reinterpret_cast<int2*>(take((size_t)c.N * c.HK * 8));
+        if (few_rows(a)) a.row_info = reinterpret_cast<int2*>(take((size_t)c.N * a.c.HK * 8));
         else a.cut = reinterpret_cast<int4*>(take((size_t)a.workers * 16));
         a.slot_ml = reinterpret_cast<float2*>(take((size_t)a.workers * 2 * p.bm * 8));
         a.slot_o = reinterpret_cast<float*>(take((size_t)a.workers * 2 * p.bm * c.D * 4));

@@ -22,6 +22,7 @@ namespace attn {
 struct Fp4Args {
     Args a;
     Fp4Cache cache;
+    int share;           // of the call's key heads as the kernels see them, so many in a row are one of the cache's
     uint32_t g_inverse;  // floor(2^16 / G) + 1: r * g_inverse >> 16 is r / G for the short form's rows, as r * G < 2^16
 };
 
@@ -251,6 +252,7 @@ struct Short4 {
     // The wave's tile of every unit from t0 on, of a run of n rows that begins at `begin`; nothing from unit t1 on.
     __device__ __forceinline__ void open(const Fp4Args& f, long long begin, int hk, int t0, int t1, int n) {
         const int j0 = t0 * C::UNIT + keys_of * C::BN, D = f.a.c.D;
+        if (f.share > 1) hk /= f.share;
         left = uniform(min(n, t1 * C::UNIT) - j0);
         const int tail = left & (C::BN - 1);  // of the one tile that may be shorter, if it is this wave's
         kc.open(f.cache.k.codes, begin + j0, hk, 1, C::BN, tail, D / 2);
@@ -600,7 +602,7 @@ __device__ __forceinline__ void finish_piece(Short4<C>& b, const Run& run, long 
     if (again) {
         using TS = typename C::TS;
         const float s2 = a.negate ? -a.s2 : a.s2;
-        const Fp4Keys keys = fp4_keys(f.cache, run.begin, run.hk);
+        const Fp4Keys keys = fp4_keys(f.cache, run.begin, run.hk / f.share);
 #pragma unroll 1
         for (int r = b.wave; r < rows; r += C::W) {
             const int i = r / a.G, g = r - i * a.G, seen = min(max(run.n - run.T + 1 + i, 0), run.n);

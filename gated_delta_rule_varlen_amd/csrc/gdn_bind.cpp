@@ -9,11 +9,13 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include "gdn.h"
 
@@ -125,19 +127,14 @@ struct Call {
     // The four tensors of a 4-bit cache of D elements a head; as many heads as the first one has.
     bool cache(PyObject* o, gdn_fp4_cache* to, int64_t* of_heads) {
         if (failed) return false;
-        PyObject* four = PySequence_Fast(o, "cache must be the four tensors k_codes, k_scales, v_codes, v_scales");
-        if (four == nullptr) {
-            failed = true;
-            return false;
-        }
-        if (PySequence_Fast_GET_SIZE(four) != 4) {
-            refuse(PyExc_ValueError, "cache must be the four tensors k_codes, k_scales, v_codes, v_scales");
+        if (!(PyTuple_Check(o) || PyList_Check(o)) || PySequence_Fast_GET_SIZE(o) != 4) {
+            refuse(PyExc_TypeError, "cache must be a tuple of four tensors: k_codes, k_scales, v_codes, v_scales");
         } else {
             static const char* const names[4] = {"cache: k_codes", "cache: k_scales", "cache: v_codes", "cache: v_scales"};
             void** const to_p[4] = {&to->k_codes, &to->k_scales, &to->v_codes, &to->v_scales};
             int64_t* const to_s[4] = {to->k_codes_stride, to->k_scales_stride, to->v_codes_stride, to->v_scales_stride};
             for (int i = 0; i < 4 && !failed; ++i) {
-                const at::Tensor* t = tensor(PySequence_Fast_GET_ITEM(four, i), names[i]);
+                const at::Tensor* t = tensor(PySequence_Fast_GET_ITEM(o, i), names[i]);
                 if (t == nullptr || !placed(*t, at::kByte, names[i])) break;
                 const int64_t width = i % 2 == 0 ? D / 2 : D / 32;
                 if (i == 0) *of_heads = t->dim() == 3 ? t->size(1) : 0;
@@ -155,7 +152,6 @@ struct Call {
                 }
             }
         }
-        Py_DECREF(four);
         return !failed;
     }
     int32_t narrow(int64_t x, const char* what) {
@@ -385,6 +381,50 @@ PyObject* fp4_rows(PyObject*, PyObject* const* x, Py_ssize_t count) {
     END_HANDLE_TH_ERRORS
 }
 
+// fp4_read(cache, offsets, N, past, kv_begin, dtype, dev_status, stream) -> (status, k, v), with new k and v
+PyObject* fp4_read(PyObject*, PyObject* const* x, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    if (count != 8 || fp4_read_fn == nullptr) {
+        PyErr_SetString(PyExc_TypeError, "fp4_read: 8 arguments, after connect");
+        return nullptr;
+    }
+    Call c;
+    if (!(PyTuple_Check(x[0]) || PyList_Check(x[0])) || PySequence_Fast_GET_SIZE(x[0]) != 4)
+        c.refuse(PyExc_TypeError, "cache must be a tuple of four tensors: k_codes, k_scales, v_codes, v_scales");
+    const at::Tensor* codes = c.failed ? nullptr : c.tensor(PySequence_Fast_GET_ITEM(x[0], 0), "cache: k_codes");
+    const at::Tensor* off = c.tensor(x[1], "offsets");
+    if (!c.failed && (codes->dim() != 3 || !codes->is_cuda())) c.refuse(PyExc_ValueError, "cache: k_codes must be a device tensor [rows, heads, D/2]");
+    if (!c.failed && !THPDtype_Check(x[5])) c.refuse(PyExc_TypeError, "dtype must be a torch.dtype");
+    if (c.failed) return nullptr;
+    c.dtype = reinterpret_cast<THPDtype*>(x[5])->scalar_type;
+    c.dev = codes->get_device();
+    c.D = 2 * codes->size(2);
+    if (dtype_code(c.dtype) < 0) c.refuse(PyExc_TypeError, "dtype: unsupported dtype %s", at::toString(c.dtype));
+    const int64_t N = PyLong_AsLongLong(x[2]), HK = codes->size(1), B = off->numel() - 1;
+    if (c.failed || PyErr_Occurred()) return nullptr;
+    gdn_fp4_rows_desc d{};
+    gdn_fp4_cache cache{};
+    int64_t heads = 0;
+    d.B = c.narrow(B, "B");
+    d.N = c.narrow(N, "N");
+    d.HK = c.narrow(HK, "HK");
+    d.D = c.narrow(c.D, "D");
+    d.dtype = dtype_code(c.dtype);
+    if (!c.cache(x[0], &cache, &heads)) return nullptr;
+    const auto offsets = (const int32_t*)c.flat(x[1], B + 1, at::kInt, "offsets");
+    const auto past = (const int32_t*)c.flat(x[3], B, at::kInt, "past");
+    const auto kv_begin = (const int64_t*)c.flat(x[4], B, at::kLong, "kv_begin");
+    const auto status = (int32_t*)c.flat(x[6], 1, at::kInt, "dev_status");
+    const hipStream_t stream = stream_of(x[7]);
+    if (c.failed || PyErr_Occurred()) return nullptr;
+    const c10::DeviceGuard on(codes->device());
+    Made k(Py_None, {N, HK, c.D}, *codes, c.dtype), v(Py_None, {N, HK, c.D}, *codes, c.dtype);
+    for (int64_t* s : {d.k_stride, d.v_stride}) s[0] = HK * c.D, s[1] = c.D;
+    const gdn_status st = fp4_read_fn(&d, &cache, offsets, past, kv_begin, k.t.data_ptr(), v.t.data_ptr(), status, stream);
+    return Py_BuildValue("iNN", (int)st, k.release(), v.release());
+    END_HANDLE_TH_ERRORS
+}
+
 // attention_fp4(q, cache, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse, workspace, dev_status, stream)
 //   -> (status, out, lse)
 PyObject* attention_fp4(PyObject*, PyObject* const* x, Py_ssize_t count) {
@@ -568,6 +608,7 @@ PyObject* connect(PyObject*, PyObject* args) {
 PyMethodDef methods[] = {{"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, nullptr},
                          {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, nullptr},
                          {"fp4_rows", (PyCFunction)(void (*)(void))fp4_rows, METH_FASTCALL, nullptr},
+                         {"fp4_read", (PyCFunction)(void (*)(void))fp4_read, METH_FASTCALL, nullptr},
                          {"attention_fp4", (PyCFunction)(void (*)(void))attention_fp4, METH_FASTCALL, nullptr},
                          {"residual_norm", (PyCFunction)(void (*)(void))residual_norm, METH_FASTCALL, nullptr},
                          {"gated_norm", (PyCFunction)(void (*)(void))gated_norm, METH_FASTCALL, nullptr},

@@ -301,6 +301,11 @@ def test_the_binding_takes_device_tensors_only(abi):
         gdn.gated_norm(x, x, activation="tanh")
     with pytest.raises(ValueError):
         gdn.cache_read_fp4_varlen(cache, off)  # how many tokens
+    for bad in ((), cache[:3], tuple(cache) + (x,), [3] * 4, iter(cache), None, "abcd"):
+        with pytest.raises((TypeError, ValueError)):
+            gdn.cache_read_fp4_varlen(bad, off, N=4)
+    with pytest.raises((TypeError, ValueError)):
+        gdn.cache_read_fp4_varlen(cache, off, N=4, dtype=3)
     for rows, HK, D in ((-1, 1, 64), (5, 0, 64), (5, 1, 48), (5, 1, 288)):
         with pytest.raises(ValueError):
             gdn.fp4_cache(rows, HK, D, device="cpu")

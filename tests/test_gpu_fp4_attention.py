@@ -91,6 +91,19 @@ def test_blocks(torch, kind, D, G):
     Case(torch, kind, 2, G, D, BLOCKS, cache_layout="rows").check(f"blocks {kind} {G}x{D}")
 
 
+@pytest.mark.parametrize("G,most", [(8, 8), (8, 5), (4, 16), (5, 9), (9, 7), (3, 21), (1, 40), (1, 64)])
+def test_heads_divided_among_blocks(torch, G, most):
+    """Wide fp32 rows: a key head's query heads in one block, in several, and where they cannot be divided."""
+    lengths = [(most, 200), (1, 1), (most - 1, 40), (2, 900), (0, 3)]
+    c = Case(torch, "f32", 2, G, 160, lengths)
+    c.check(f"fp32 {most} x {G}")
+    c.cache[3][c.begin[0] + 199, 1, 2] = 255  # and a value without a number in the last row
+    import gated_delta_rule_varlen_amd as gdn
+
+    out = torch.isnan(gdn.attention_fp4_varlen(**c.dev(), max_q=most)[0].cpu())
+    assert out[most - 1, G:, 64:96].all() and out.sum() == 32 * G
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 256])
 def test_prompts(torch, kind, D):

@@ -130,6 +130,28 @@ def test_rows_past_32_bits(torch):
     assert (cache.k_codes[: rows - 5] != 0).sum() == 0 and (cache.v_scales[rows - 2:] != 0).sum() == 0
 
 
+def test_the_binding_refuses_a_bad_cache(torch):
+    import gated_delta_rule_varlen_amd as gdn
+
+    c, off = gdn.fp4_cache(9, 2, 64), offsets_of(torch, [4])
+    x = torch.zeros(4, 2, 64, device="cuda")
+    at = dict(kv_len=off[1:], kv_begin=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    bad = [c[:3], iter(c), tuple(t.cpu() for t in c), c._replace(v_scales=c.v_scales[:5]), c._replace(k_codes=c.k_codes.int()),
+           c._replace(k_scales=c.k_scales[:, :1]), c._replace(v_codes=c.v_codes[:, :, :16]), [None] * 4,
+           c._replace(k_codes=torch.zeros(9, 2, 64, dtype=torch.uint8, device="cuda")[:, :, ::2])]
+    for cache in bad:
+        for call in (lambda: gdn.cache_write_fp4_varlen(x, x, off, cache=cache), lambda: gdn.cache_read_fp4_varlen(cache, off, N=4),
+                     lambda: gdn.cache_read_fp4_varlen(cache, off, k_out=x), lambda: gdn.attention_fp4_varlen(x, cache, off, **at)):
+            with pytest.raises((TypeError, ValueError)):
+                call()
+    with pytest.raises((TypeError, ValueError)):
+        gdn.cache_read_fp4_varlen(c, off, N=4, dtype=torch.float64)
+    with pytest.raises(gdn.GdnError):
+        gdn.attention_fp4_varlen(x, c, off, kv_len=None, kv_begin=None)
+    with pytest.raises(ValueError):  # three heads of a cache with two
+        gdn.cache_write_fp4_varlen(torch.zeros(4, 3, 64, device="cuda"), torch.zeros(4, 3, 64, device="cuda"), off, cache=c)
+
+
 @pytest.mark.parametrize("bad", ["first", "last", "falls", "past", "begin", "end"])
 def test_malformed_calls_write_nothing(torch, bad):
     import gated_delta_rule_varlen_amd as gdn
