@@ -44,13 +44,16 @@ Plan plan(const AttnLaunch& c, bool wide) {
     a.splits = 1;
     a.set_rows = (long long)c.N * c.H;
     p.dp = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
-    // Where a key head's rows are too many for the short form's registers (fp32, wider than 128), its query heads are divided
-    // among so many blocks that they are not: keys are read more than once, which bounds nothing there.  (26 sequences of
-    // 7 tokens and 131 keys, H 32, HK 4, D 160: 149 us in the long form, so 24.)
+    // Wider than 128, a key head's rows that are too many for the short form's registers are divided by query heads among so
+    // many blocks that they are not: keys are read more than once, which bounds nothing there.  In half precision up to
+    // 128 rows (20 sequences of 9 tokens over 3000 to 9000 keys, H 16, HK 2, D 256: 58 us, in the long form, whose tiles
+    // have 256 rows, 80; at widths 128 and 64 it is 43 and 40, 18 and 16, 27 and 40); in fp32, whose long form runs on
+    // fp32 matrix instructions, where 32 rows or fewer are left (26 of 7 tokens and 131 keys, H 32, HK 4, D 160: 24 and 149).
     p.f.share = 1;
-    if (short_rows<T>(p.dp) < 64 && (long long)c.max_q * a.G <= 64) {
+    const long long all_rows = (long long)c.max_q * a.G, fit = short_rows<T>(p.dp);
+    if (p.dp == 256 && all_rows > fit && (T::code == GDN_F32 || all_rows <= 128)) {
         int share = 1;
-        while (share <= a.G && (a.G % share != 0 || (long long)c.max_q * (a.G / share) > short_rows<T>(p.dp))) ++share;
+        while (share <= a.G && (a.G % share != 0 || (long long)c.max_q * (a.G / share) > fit)) ++share;
         if (share <= a.G) {
             p.f.share = share;
             a.G /= share;

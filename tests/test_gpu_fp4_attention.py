@@ -91,12 +91,13 @@ def test_blocks(torch, kind, D, G):
     Case(torch, kind, 2, G, D, BLOCKS, cache_layout="rows").check(f"blocks {kind} {G}x{D}")
 
 
-@pytest.mark.parametrize("G,most", [(8, 8), (8, 5), (4, 16), (5, 9), (9, 7), (3, 21), (1, 40), (1, 64)])
-def test_heads_divided_among_blocks(torch, G, most):
-    """Wide fp32 rows: a key head's query heads in one block, in several, and where they cannot be divided."""
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("G,most", [(8, 8), (8, 5), (4, 16), (5, 9), (9, 7), (3, 21), (1, 40), (1, 64), (8, 9), (12, 9), (2, 50), (16, 32)])
+def test_heads_divided_among_blocks(torch, kind, G, most):
+    """Wide rows: a key head's query heads in one block, in several, and where they cannot be divided."""
     lengths = [(most, 200), (1, 1), (most - 1, 40), (2, 900), (0, 3)]
-    c = Case(torch, "f32", 2, G, 160, lengths)
-    c.check(f"fp32 {most} x {G}")
+    c = Case(torch, kind, 2, G, 160, lengths)
+    c.check(f"{kind} {most} x {G}")
     c.cache[3][c.begin[0] + 199, 1, 2] = 255  # and a value without a number in the last row
     import gated_delta_rule_varlen_amd as gdn
 
