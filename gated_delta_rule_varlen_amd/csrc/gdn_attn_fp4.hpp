@@ -766,6 +766,28 @@ struct Long4 : Block<C> {
         if constexpr (C::DP == 256) asm volatile("" : "+v"(x));
         return x;
     }
+    // Thread x's row of a tile of keys or values, its run of elements there, and the order in which it writes the run's
+    // pieces: piece i ^ turn at step i.  LDS takes 16 bytes of eight neighbours a cycle, over 128 bytes of banks, so these are
+    // such that the places of eight neighbours differ modulo 8 (values of fp32 operands: in pairs).  With neighbours along
+    // a row 40% of LDS's busy cycles were conflicts at width 128 (24748 tokens over up to 7100 keys 1372 us, so 1309; 2000
+    // tokens of fp32 at width 256 831 us, so 753).
+    template <bool V>
+    static __device__ __forceinline__ int row_of(int x) {
+        if constexpr (!C::HALF) return x >> 6 << 3 | (x & 7);
+        else if constexpr (C::RB == 512) return x >> 5 << 1 | (x >> 2 & 1);
+        else if constexpr (C::RB == 128) return x >> 4 << 2 | (x >> 1 & 2) | (x >> 3 & 1);
+        else return V ? x >> 6 << 4 | (x >> 1 & 3) << 2 | (x >> 4 & 3) : x >> 4 << 2 | (x >> 1 & 3);
+    }
+    static __device__ __forceinline__ int part_of(int x) {
+        if constexpr (!C::HALF) return x >> 3 & 7;
+        else if constexpr (C::RB == 512) return (x >> 1 & 12) | (x & 3);
+        else return C::RB == 128 ? x & 3 : (x >> 2 & 2) | (x & 1);
+    }
+    template <bool V>
+    static __device__ __forceinline__ int turn_of(int x) {
+        return V && C::HALF ? x >> 2 & 1 : 0;
+    }
+    static_assert(C::HALF ? U == (C::RB == 256 ? 32 : 16) && C::RB <= 512 : U == 32 && C::RB == 1024, "the threads' places");
     __device__ __forceinline__ Rsrc rows_of(const char* p, int j0, int left, long long stride, int width) const {
         const int rows = min(left, C::BN);
         return __builtin_amdgcn_make_buffer_rsrc((void*)(p + j0 * stride), 0, rows > 0 ? (rows - 1) * (int)stride + width : 0, kRsrc);
@@ -776,7 +798,7 @@ struct Long4 : Block<C> {
         const Fp4Half& h = V ? cache.v : cache.k;
         const int j0 = real ? tile * C::BN : 0, left = real ? B::run_n - j0 : 0, D = B::a.c.D;
         const Rsrc rc = rows_of(V ? s.vc : s.kc, j0, left, h.codes.row, D / 2), rs = rows_of(V ? s.vs : s.ks, j0, left, h.scales.row, D / 32);
-        const int x = thread(), row = x / UPR, e = x % UPR * U;
+        const int x = thread(), row = row_of<V>(x), e = part_of(x) * U;
         const int c_off = e < D ? row * (int)h.codes.row + e / 2 : kOutside, s_off = e < D ? row * (int)h.scales.row + e / 32 : kOutside;
         Half& to = V ? v : k;
         if constexpr (U == 32) {
@@ -792,18 +814,19 @@ struct Long4 : Block<C> {
     // Writes them to a stage of the ring.
     template <bool V>
     __device__ __forceinline__ void put(int stage) {
-        const int tid = thread(), row = tid / UPR, run_at = tid % UPR;
+        const int tid = thread(), row = row_of<V>(tid), run_at = part_of(tid), turn = turn_of<V>(tid);
         char* at = B::lds + stage * C::STAGE + (V ? C::KTILE + C::template row_at<C::VSTEP>(row) : C::template row_at<C::KSTEP>(row));
         const int sw = V ? C::place_v(row) : C::place_k(row);
         const Half& x = V ? v : k;
         const float scale = fp4::scale_of(x.scale);
+        const uint32_t other = -turn;
 #pragma unroll
         for (int i = 0; i < U / 8; ++i) {
             if constexpr (C::HALF) {
                 u32x4 w;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = widen2<T>(x.codes[i], scale, j);
-                *reinterpret_cast<u32x4*>(at + (((run_at * (U / 8) + i) ^ sw) * 16)) = w;
+                for (int j = 0; j < 4; ++j) w[j] = widen2<T>((x.codes[i] & ~other) | (x.codes[i ^ 1] & other), scale, j);
+                *reinterpret_cast<u32x4*>(at + (((run_at * (U / 8) + (i ^ turn)) ^ sw) * 16)) = w;
             } else {
                 float y[8];
                 fp4::values(x.codes[i], x.scale, y);
