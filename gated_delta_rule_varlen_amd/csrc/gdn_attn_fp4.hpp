@@ -9,8 +9,19 @@
 // two keys.
 //
 // A block's four waves take 32 keys each of every 128, each with places of its own in LDS and nothing shared until a run's
-// end, where their sums are joined.  Scales are asked for two tiles at a time, as a tile's are half a load.  All runs lie end to end and are cut into equal parts, one a block, as in the
-// short form there.
+// end, where their sums are joined.  Scales are asked for two tiles at a time, as a tile's are half a load.  All runs lie
+// end to end and are cut into equal parts, one a block, as in the short form there.
+//
+// Measured (bf16; the floor is the bytes at a 1 GiB copy's 5.2 TB/s): 256 sequences of up to 4096 keys (H 32, HK 8, D 128,
+// 604 MB) 122 to 126 us of 116: its loads alone take 114.5, its work without them 90, the joining launch 5.  One token over 131072
+// keys (HK 2, D 256, 71 MB) 24 to 25 of 13.7: 19 and the joining launch's 6.  Drafts of five tokens over 1000 to 8000 keys
+// (64 sequences, D 256, 167 MB) 73 to 75 of 32: bound by the products and the vector work of 40 rows (matrix
+// instructions busy 23% of cycles, vector ones 53%).  Tried: codes to registers without LDS 152 us on the first of
+// these; loads that leave the caches as they are, without the hint, 138; a barrier a tile, no gain.
+//
+// Long form (prompts): see Long4.  24748 tokens over up to 7100 keys (H 32, HK 8, D 128) 1309 to 1446 us by card, 0.93 to
+// 1.03 PFLOP/s of the 1.34 that a large library product reaches: matrix instructions are busy 46% of cycles, the rest
+// is the vector work of the softmax and the widening (6.3 vector instructions for one of theirs), and power holds the clock.
 #pragma once
 
 #include "gdn_attn.hpp"
@@ -1174,7 +1185,7 @@ __global__ __launch_bounds__(X::C::NT, X::C::WAVES) void long4_kernel(Fp4Args f)
 
 // Row tiles and waves of the short form, for `tiles` tiles of 16 rows.  Up to four tiles a wave (WAVES: of a SIMD, as the
 // registers leave room for); at width 256 two, and two groups of waves for more.  (40 rows over 64 caches of 1000 to 8000
-// keys, D 256: 90 us with three tiles a wave and one wave a SIMD.)
+// keys, D 256: 74 us, 90 with three tiles a wave and one wave a SIMD.)
 template <typename T, int DP, int TILES>
 struct Short4For {
     static constexpr bool F32IO = T::code == GDN_F32;

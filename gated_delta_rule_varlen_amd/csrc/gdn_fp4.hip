@@ -2,6 +2,12 @@
 //
 // A thread takes eight elements of a head: four neighbours hold a block of 32 and find its largest element among
 // themselves.  Codes of eight elements are 32 bits, so a wave's loads and stores are whole segments.
+//
+// e is the least with max|x| <= 6 * 2^e, from the bits of the largest element and without a logarithm; the conversion rounds
+// x / 2^e to the nearest code.  Bound by bytes: 24748 tokens of 8 heads of 128 written (101 MB of bf16 to 27 MB) take 21 to 23
+// us and come back in 21 to 22, 5.5 to 6 TB/s; 64 tokens 3.3 and 5.2, the check of the call and one chain of loads.
+// A wave a row took 63 us there and back; loads and stores past the caches 51 against 47; two or eight tokens on their way
+// instead of four, no difference.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

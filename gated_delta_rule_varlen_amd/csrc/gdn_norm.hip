@@ -1,6 +1,11 @@
 // gdn_norm.hip -- the norms before and behind a block: residual_norm over whole rows of the residual stream, gated_norm over
 // the heads of a mixer's output.  Both read every input once and write every output once, and hold a row in
-// registers between its sums and its results.
+// registers between its sums and its results; squares, sums and roots are fp32, each output is rounded once.
+//
+// Both are bound by bytes where there are many rows (a 1 GiB copy reaches 5.2 TB/s): residual_norm of 24748 rows of 4096 (bf16
+// beside an fp32 stream, norm of the block's output and channel scales, 1.22 GB) 246 to 248 us, 4.9 TB/s; gated_norm of
+// 9111 x 16 heads of 64 fp16 elements (56 MB) 10.9 us, 5.1 TB/s.  With few rows they are one launch: 256 rows of 4096
+// 4.2 us, 256 x 32 heads of 128 4.1 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -72,6 +77,7 @@ __device__ __forceinline__ void load_vector(const float* p, float* to) {
 
 // RT threads a row, P spans of 16 bytes of x a thread.  A block goes over rows with the next one on its way, and keeps the
 // vectors in registers where they are few (P <= 2): read again for every row they are as many bytes from L2 as the row.
+// (Both, and even shares of rows, against a wave a row that reads every row twice: 609 us, so 248, on the 24748 rows above.)
 template <typename T, typename R, int RT, int P>
 __global__ __launch_bounds__(RT < 256 ? 256 : RT) void residual_norm_kernel(ResidualNormLaunch a) {
     using TS = typename T::storage;
