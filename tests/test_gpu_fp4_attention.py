@@ -185,13 +185,7 @@ def test_same_bits_again(torch):
             assert all((bits(a) == bits(b)).all() for a, b in zip(first, again))
 
 
-@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("which", ["keys", "values"])
-@pytest.mark.parametrize("lengths", [[(4, 40), (4, 300)], [(70, 170)], [(9, 200), (1, 5)]])
-def test_blocks_without_numbers(torch, kind, which, lengths):
-    """A scale byte of 255 in the last row of each sequence: only the last token may see it; and in one row
-    that all of a sequence's tokens see."""
-    c = Case(torch, kind, 2, 4, 64, lengths)
+def check_without_numbers(torch, c, G, which):
     clean = c.check("clean")
     scales = c.cache[1 if which == "keys" else 3]
     for b, n in enumerate(c.n):
@@ -207,20 +201,37 @@ def test_blocks_without_numbers(torch, kind, which, lengths):
             end += t
             last[end - 1] = True
         hit = torch.isnan(out.cpu().float())
-        assert not hit[~last].any() and not hit[:, 4:].any(), "tokens that do not see the row, and the other head"
+        assert not hit[~last].any() and not hit[:, G:].any(), "tokens that do not see the row, and the other head"
         if which == "keys":
-            assert hit[last, :4].all() and torch.isnan(lse.cpu()[last, :4]).all()
+            assert hit[last, :G].all() and torch.isnan(lse.cpu()[last, :G]).all()
         else:
-            assert hit[last, :4, 32:].all() and not hit[:, :, :32].any() and not torch.isnan(lse).any()
+            assert hit[last, :G, 32:64].all() and not hit[:, :, :32].any() and not hit[:, :, 64:].any() and not torch.isnan(lse).any()
         # the other rows have what they had, to the bound between two sums of the same terms
         k, v = c.values()
         k, v = torch.nan_to_num(k), torch.nan_to_num(v)
-        ref = attention_ref(c.q, k, v, c.T, c.begin, c.n, kind=kind)
-        by = 3.0 if kind == "f32" else 1.0
-        for rows, heads in ((~last, slice(0, 4)), (slice(None), slice(4, 8))):
+        ref = attention_ref(c.q, k, v, c.T, c.begin, c.n, kind=c.kind)
+        by = 3.0 if c.kind == "f32" else 1.0
+        for rows, heads in ((~last, slice(0, G)), (slice(None), slice(G, 2 * G))):
             assert_within(out[:, heads][rows], ref[0][:, heads][rows], by * ref[2][:, heads][rows], f"{which} out")
             assert_within(lse[:, heads][rows], ref[1][:, heads][rows], by * ref[3][:, heads][rows], f"{which} lse")
     assert not torch.isnan(clean[0]).any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("which", ["keys", "values"])
+@pytest.mark.parametrize("lengths", [[(4, 40), (4, 300)], [(70, 170)], [(9, 200), (1, 5)]])
+def test_blocks_without_numbers(torch, kind, which, lengths):
+    """A scale byte of 255 in the last row of each sequence: only the last token may see it."""
+    check_without_numbers(torch, Case(torch, kind, 2, 4, 64, lengths), 4, which)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("which", ["keys", "values"])
+@pytest.mark.parametrize("D,G,lengths", [(128, 4, [(4, 40), (4, 300)]), (128, 8, [(5, 3000), (2, 40)]), (256, 8, [(5, 4000), (2, 40)]),
+                                         (192, 8, [(9, 400), (2, 30)]), (128, 4, [(90, 300)]), (256, 4, [(90, 300), (40, 70)])])
+def test_blocks_without_numbers_in_wide_rows(torch, kind, which, D, G, lengths):
+    """The same where row tiles share a block, where heads are divided among blocks, and in prompts."""
+    check_without_numbers(torch, Case(torch, kind, 2, G, D, lengths), G, which)
 
 
 def test_cache_of_no_rows_and_no_tokens(torch):
@@ -268,12 +279,13 @@ def test_malformed_calls_write_nothing(torch, bad, lengths):
     assert (bits(out) == before[0]).all() and (bits(lse) == before[1]).all()
 
 
-@pytest.mark.parametrize("lengths", [[(1, 3000), (1, 1), (1, 77)], [(5, 900), (2, 60)], [(90, 400), (3, 3)]])
-def test_streams_and_graphs(torch, lengths):
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("lengths", [[(1, 3000), (1, 1), (1, 77)], [(5, 900), (2, 60)], [(25, 900), (2, 60)], [(90, 400), (3, 3)]])
+def test_streams_and_graphs(torch, lengths, D):
     """Two graphs with a workspace each, replayed in turn; another stream; lengths that change between replays."""
     import gated_delta_rule_varlen_amd as gdn
 
-    cases = [Case(torch, "bf16", 2, 4, 64, lengths, seed=s) for s in (1, 2)]
+    cases = [Case(torch, "bf16", 2, 4, D, lengths, seed=s) for s in (1, 2)]
     runs = []
     for c in cases:
         out, lse = c.check("eager")
