@@ -81,13 +81,17 @@ Plan plan(const AttnLaunch& c, bool wide) {
         a.workers = (int)std::max(1ll, std::min((long long)kCUs * s.per_cu, units));
         p.join = c.N > 0 && a.workers > 1;
     } else {
-        // row tiles and key parts as for a plain cache
+        // Row tiles as for a plain cache.  As many key parts as leave room for all blocks at once, one a CU at width 256 and two
+        // below: each part writes fp32 sums of its rows.  (Parts until every CU has two blocks or more, and now: 15 sequences
+        // of 226 to 452 tokens, H 8, HK 2, D 160, 68 us and 36; four of 300 tokens and 4300 keys, H 16, HK 2, D 256, 163 and
+        // 106; one of 2000, H 32, HK 8, D 128, 78 and 55.  One part wherever half of the CUs have a block: one of 700 there 25
+        // instead of 29, but in fp32 one of 500 and 3500 keys 167 instead of 89.)
         const Shape s = with_long4<T>(p.dp, [](auto x) { return shape_of<typename decltype(x)::C>(); });
         p.bm = s.bm;
         p.lds = s.ring;
         const long long most = (rows + s.bm - 1) / s.bm, slots = (long long)c.N * a.G / s.bm + c.B;
         const long long tiles = std::min(most * c.B, slots) * a.c.HK;
-        a.splits = (int)std::max(1ll, std::min(std::min((2 * kCUs + tiles - 1) / std::max(1ll, tiles), c.kv_rows / kPartKeys), 64ll));
+        a.splits = (int)std::max(1ll, std::min({(p.dp == 256 ? 1 : 2) * kCUs / std::max(1ll, tiles), c.kv_rows / kPartKeys, 64ll}));
         p.blocks = slots * a.c.HK * a.splits;
         p.join = a.to_sets = a.splits > 1;
         a.sets = p.join ? a.splits : 0;
