@@ -54,6 +54,39 @@ __device__ __forceinline__ Fp4Keys fp4_keys(const Fp4Cache& c, long long begin, 
     return Fp4Keys{at(c.k.codes), at(c.k.scales), at(c.v.codes), at(c.v.scales)};
 }
 
+// Two elements' values as matrix operands of type OP.
+template <typename OP>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes, float scale, int pair) {
+    // the pair is part of the instruction
+    switch (pair) {
+#define GDN_PAIR(p)                                                                                                    \
+    case p:                                                                                                            \
+        if constexpr (OP::code == GDN_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, p)); \
+        else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, p));
+        GDN_PAIR(0)
+        GDN_PAIR(1)
+        GDN_PAIR(2)
+        default: GDN_PAIR(3)
+#undef GDN_PAIR
+    }
+}
+
+// Eight elements' values as the products have them: rounded to fp16 (to an infinity past its range) with fp16 queries,
+// so that a row that is done again has the values it had; otherwise exact.
+template <typename T>
+__device__ __forceinline__ void operand_values(uint32_t codes, uint32_t scale_byte, float* y) {
+    if constexpr (T::code == GDN_F16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = widen2<F16>(codes, fp4::scale_of(scale_byte), i);
+            y[2 * i] = to_f32<F16>((uint16_t)w);
+            y[2 * i + 1] = to_f32<F16>((uint16_t)(w >> 16));
+        }
+    } else {
+        fp4::values(codes, scale_byte, y);
+    }
+}
+
 // Row q over the keys j0 .. j1 - 1 plainly, by a wave: the largest score to base 2, the sum of exponentials and, four
 // elements a lane (4 * lane ..), their products with the values.
 struct RowSums {
@@ -75,7 +108,7 @@ __device__ __forceinline__ RowSums plain_row(const typename T::storage* q, const
 #pragma unroll 1
             for (int x = 0; x < D / 8; ++x) {
                 float k[8];
-                fp4::values(reinterpret_cast<const uint32_t*>(codes)[x], scales[x / 4], k);
+                operand_values<T>(reinterpret_cast<const uint32_t*>(codes)[x], scales[x / 4], k);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y = fmaf(to_f32<T>(q[8 * x + e]), k[e], y);
             }
@@ -92,8 +125,8 @@ __device__ __forceinline__ RowSums plain_row(const typename T::storage* q, const
             const float pj = __shfl(p, j);
             if (4 * lane >= D) continue;
             float v[8];
-            fp4::values(*reinterpret_cast<const uint16_t*>(s.vc + (j0 + j) * c.v.codes.row + 2 * lane),
-                        *reinterpret_cast<const uint8_t*>(s.vs + (j0 + j) * c.v.scales.row + lane / 8), v);
+            operand_values<T>(*reinterpret_cast<const uint16_t*>(s.vc + (j0 + j) * c.v.codes.row + 2 * lane),
+                              *reinterpret_cast<const uint8_t*>(s.vs + (j0 + j) * c.v.scales.row + lane / 8), v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) r.o[e] = fmaf(pj, v[e], r.o[e]);
         }
@@ -139,22 +172,6 @@ struct Cfg4 {
     static __device__ __forceinline__ int place_k(int r) { return DP == 64 ? (r >> 3) & 1 : DP == 128 ? (r >> 2) & 3 : (r >> 1) & 7; }
     static __device__ __forceinline__ int row_of(int place) { return (place & 16) + (place & 3) * 4 + ((place >> 2) & 3); }
 };
-
-template <typename OP>
-__device__ __forceinline__ uint32_t widen2(uint32_t codes, float scale, int pair) {
-    // the pair is part of the instruction
-    switch (pair) {
-#define GDN_PAIR(p)                                                                                                    \
-    case p:                                                                                                            \
-        if constexpr (OP::code == GDN_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, p)); \
-        else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, p));
-        GDN_PAIR(0)
-        GDN_PAIR(1)
-        GDN_PAIR(2)
-        default: GDN_PAIR(3)
-#undef GDN_PAIR
-    }
-}
 
 // The parts of two fp32 numbers as operands.
 template <typename OP, int PARTS>

@@ -490,7 +490,8 @@ gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc *desc, size_t *byte
  * gdn_attention_fp4_varlen -- gdn_attention_varlen with k and v the values of a cache: arguments, formula, masks and
  * errors as there (out = q included), except that kv_begin and kv_len are required, desc->prefix_len is 0, its strides of k,
  * v and the prefix are not read, desc->kv_rows = cache->rows, and D is a multiple of 32 (GDN_ERR_SHAPE).  With fp16 queries
- * the cache's values are operands in fp16: those of scales past 2^13 may be infinite.
+ * the cache's values are those rounded to fp16: infinite past 65504, which scales past 2^13 can reach, and with fewer bits for
+ * scales below 2^-23.
  *
  * Tensors (element (row, head, j) at row*stride[0] + head*stride[1] + j, strides in bytes):
  *   k_codes, v_codes [rows, HK, D/2] uint8    16-byte aligned, strides multiples of 16 (GDN_ERR_ALIGN), rows at most 1 MiB
