@@ -166,6 +166,8 @@ struct Cfg4 {
     static_assert(RG <= 2 && 16 * ROW * 4 <= NS * STAGE, "the waves' sums take the tiles' place");
     // Rows whose sums fit the second half, while the next piece's first tile is on its way to the first.
     static constexpr int EARLY = RT * RG == 1 ? STAGE / (ROW * 4) : 0;
+    // The largest scale byte of which every value is a finite operand: 6 * 2^13 in fp16, 6 * 2^125 in bf16.
+    static constexpr int FINITE = OP::code == GDN_F16 ? 127 + 13 : 127 + 125;
     static constexpr float BIAS = T::code == GDN_F16 ? 4.0f : 0.0f, LAG = 8.0f;
     // Codes in LDS: 16-byte pieces (a block each) of key r at place piece ^ place_k(r), so that the 16 rows that are read
     // at a time lie in different banks; values in the order of row_of, so that four groups' rows are neighbours.
@@ -499,13 +501,14 @@ struct Short4 {
             }
             scale[x] = scale_at(vst[(place + grp) * C::SLOTS + block / C::SB], block % C::SB);
         }
-        // 0 * NaN is NaN: where rows differ in what they see, a value without a number would reach rows that must not
-        // see it.  Such a tile is found here, and the piece's rows are done again plainly.
+        // 0 times NaN or an infinity is NaN: where rows differ in what they see, a value that is not finite as an operand would
+        // reach rows that must not see it.  Such a tile is found by its scales, and the piece's rows are done again plainly: a
+        // tile whose codes are small enough for the scale to be harmless only costs that.
         if (vis_lo < min(j0 + C::BN, n)) {
             uint32_t most = 0;
 #pragma unroll
             for (int x = 0; x < 8; ++x) most = max(most, __float_as_uint(scale[x]) & 0x7f800000u);
-            spoiled |= __builtin_amdgcn_ballot_w64(most == 0x7f800000u) != 0;
+            spoiled |= __builtin_amdgcn_ballot_w64(most > (uint32_t)C::FINITE << 23) != 0;
         }
 #pragma unroll
         for (int y = 0; y < VD; y += 2) {

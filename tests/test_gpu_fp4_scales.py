@@ -58,3 +58,15 @@ def test_infinite_operands_in_rows_done_again(torch, which, D, G, lengths):
         c.cache[scales - 1][c.begin[b], 0, 16:32] = 0x77
         c.cache[3][c.begin[b] + n - 1, 0, 0] = 255
     check(torch, c, f"{which} {D}")
+
+
+@pytest.mark.parametrize("kind,byte", [("f16", 141), ("f16", 150), ("f16", 252), ("f16", 254), ("bf16", 253), ("bf16", 254), ("f32", 253),
+                                       ("f32", 254)])
+@pytest.mark.parametrize("D,G,lengths", FORMS)
+def test_infinite_values_behind_a_mask(torch, kind, byte, D, G, lengths):
+    """In the last row of each sequence, which only the last token sees."""
+    c = Case(torch, kind, 2, G, D, lengths)
+    for b, n in enumerate(c.n):
+        c.cache[3][c.begin[b] + n - 1, 0, 1] = byte
+        c.cache[2][c.begin[b] + n - 1, 0, 16:32] = 0x77
+    check(torch, c, f"{kind} {byte} {D}")
