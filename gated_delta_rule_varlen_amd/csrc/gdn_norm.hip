@@ -204,6 +204,21 @@ hipError_t residual_for(const ResidualNormLaunch& a, hipStream_t stream) {
     return hipErrorInvalidValue;  // 32768 elements are 4096 pieces
 }
 
+// 1 / (1 + exp(-g)).  In fp32 to a few roundings for every g: the exponential's argument is exact and never positive, so it
+// does not overflow, and the quotient is rounded once (9111 x 32 heads of 128, 448 MB, 88 us as before; 9111 x 16 of 64 from
+// caches 19.5 instead of 17.9).  The half types take the chip's exponential and reciprocal: the
+// rounded argument is off by |g| 2^-24, which for gates that do not vanish (|g| < 88) is 2^-17 relative, a sixtieth of
+// fp16's own rounding; below -87 the gate is zero.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+    if constexpr (T::code == GDN_F32) {
+        const float e = expf(-fabsf(g));
+        return (g < 0.0f ? e : 1.0f) / (1.0f + e);
+    } else {
+        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+    }
+}
+
 // A head's row: L lanes of a wave, P pieces of 16 bytes each.  A block goes over rows with the next ones on their way.
 template <typename T, int L, int P>
 __global__ __launch_bounds__(256) void gated_norm_kernel(GatedNormLaunch a, uint32_t h_inverse) {
@@ -258,7 +273,7 @@ __global__ __launch_bounds__(256) void gated_norm_kernel(GatedNormLaunch a, uint
             const bool real = (p * L + j) * VEC < a.V;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float g = cur.z[p].get(i), s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+                const float g = cur.z[p].get(i), s = sigmoid<T>(g);
                 act[p][i] = a.sigmoid ? s : g * s;
                 y[p][i] = cur.x[p].get(i);
                 if (a.gate_first) y[p][i] *= act[p][i];
