@@ -312,7 +312,8 @@ hipError_t gated_for(const GatedNormLaunch& a, hipStream_t stream) {
     if (pieces <= 64) return start_gated<T, 64, 1>(a, stream);
     if (pieces <= 128) return start_gated<T, 64, 2>(a, stream);
     if (pieces <= 256) return start_gated<T, 64, 4>(a, stream);
-    return start_gated<T, 64, 8>(a, stream);
+    if constexpr (sizeof(typename T::storage) == 4) return start_gated<T, 64, 8>(a, stream);
+    return hipErrorInvalidValue;  // 2048 elements are 256 pieces
 }
 
 }  // namespace
