@@ -173,14 +173,16 @@ struct Range {
         r = u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)bytes, (uint32_t)kRsrc};
     }
 };
+// The statement carries the five wait states that a vector memory instruction needs behind a vector one that wrote a scalar
+// register it reads (a spilled one comes back by v_readlane), as the compiler adds none ahead of assembly.
 // STREAM: the bytes are read by this block alone (decode of 256 sequences: 357 us, without the hint 408).
 template <bool STREAM>
 __device__ __forceinline__ void load_to_lds(const Range& s, uint32_t at, int voff, int soff) {
     if constexpr (STREAM)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
                      ::"s"(at), "v"(voff), "s"(s.r), "s"(soff) : "m0", "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                      ::"s"(at), "v"(voff), "s"(s.r), "s"(soff) : "m0", "memory");
 }
 

@@ -199,7 +199,7 @@ __device__ __forceinline__ float scale_at(uint32_t x, uint32_t at) {
 template <int BYTES>
 __device__ __forceinline__ void stream_to_lds(u32x4 s, uint32_t at, int voff, int soff) {
     static_assert(BYTES == 1 || BYTES == 2 || BYTES == 4 || BYTES == 16, "bytes");
-#define GDN_LOAD(op) asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t" op " %1, %2, %3 offen nt lds" ::"s"(at), "v"(voff), "s"(s), "s"(soff) : "m0", "memory")
+#define GDN_LOAD(op) asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\t" op " %1, %2, %3 offen nt lds" ::"s"(at), "v"(voff), "s"(s), "s"(soff) : "m0", "memory")
     if constexpr (BYTES == 16) GDN_LOAD("buffer_load_dwordx4");
     else if constexpr (BYTES == 4) GDN_LOAD("buffer_load_dword");
     else if constexpr (BYTES == 2) GDN_LOAD("buffer_load_ushort");
