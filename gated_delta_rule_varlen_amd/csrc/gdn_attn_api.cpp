@@ -117,6 +117,7 @@ gdn_status fp4_rows(const gdn_fp4_rows_desc* d, const void* k, const void* v, co
     gdn::Fp4RowsLaunch a{};
     if ((st = check_cache(cache, d->HK, d->D, &a.cache)) != GDN_OK) return st;
     if (d->N > (1 << 27) - 8) return GDN_ERR_OVERFLOW;  // tokens of one launch
+    if ((long long)d->HK * d->D > INT_MAX - 4096) return GDN_ERR_OVERFLOW;  // pieces of a token
     if (kv_begin == nullptr && cache->rows < d->N) return GDN_ERR_SHAPE;  // rows are token indices
     if ((st = head_rows(k, d->k_stride, d->N, d->HK, d->D, d->dtype, &a.k)) != GDN_OK) return st;
     if ((st = head_rows(v, d->v_stride, d->N, d->HK, d->D, d->dtype, &a.v)) != GDN_OK) return st;

@@ -499,8 +499,8 @@ gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc *desc, size_t *byte
  *   k, v, k_out, v_out [N, HK, D] dtype       required unless N == 0, strides in elements, multiples of 16 bytes
  *   past [B] int32 NULL = zeros; kv_begin [B] int64
  * Constraints of the write and the read: B >= 1, N >= 0, HK >= 1, D a multiple of 32 up to 256 (GDN_ERR_SHAPE), strides not
- * negative, N at most 2^27 - 8 and N*HK at most 2^31 - 4097 (GDN_ERR_OVERFLOW), no two tokens name one row of a write, inputs and
- * outputs do not overlap.  Malformed offsets and rows outside [0, rows) of a sequence with tokens write nothing
+ * negative, N at most 2^27 - 8, N*HK and HK*D at most 2^31 - 4097, B*HK at most 2^31 - 1 (GDN_ERR_OVERFLOW), no two tokens name one row
+ * of a write, inputs and outputs do not overlap.  Malformed offsets and rows outside [0, rows) of a sequence with tokens write nothing
  * (GDN_ERR_OFFSETS in *dev_status).
  * ---------------------------------------------------------------------------------------------- */
 typedef struct gdn_fp4_cache {
