@@ -513,7 +513,8 @@ def attention_fp4_varlen(q: torch.Tensor, cache, offsets: torch.Tensor, *, kv_le
                          workspace=None, dev_status=None):
     """attention_varlen over a cache in 4 bits (gdn_attention_fp4_varlen): q [N, H, D]; the keys and values of sequence b
     are what rows kv_begin[b] .. kv_begin[b] + kv_len[b] - 1 of the cache stand for, its own new tokens last.  The other
-    arguments are attention_varlen's.  Returns (out [N, H, D], lse [N, H] fp32, or None unless asked for)."""
+    arguments are attention_varlen's: max_q left at None is right, but makes prompts of single tokens and drafts, which take
+    2.5 times as long.  Returns (out [N, H, D], lse [N, H] fp32, or None unless asked for)."""
     st, out, lse = (_native or _marshal()).attention_fp4(q, cache, offsets, kv_len, kv_begin, max_q, scale, out, lse, return_lse,
                                                          workspace, dev_status, _raw_stream(q))
     if st:

@@ -19,9 +19,14 @@
 // instructions busy 23% of cycles, vector ones 53%).  Tried: codes to registers without LDS 152 us on the first of
 // these; loads that leave the caches as they are, without the hint, 138; a barrier a tile, no gain.
 //
-// Long form (prompts): see Long4.  24748 tokens over up to 7100 keys (H 32, HK 8, D 128) 1309 to 1446 us by card, 0.93 to
-// 1.03 PFLOP/s of the 1.34 that a large library product reaches: matrix instructions are busy 46% of cycles, the rest
+// fp32 takes 150 us for the first of these (125 at the floor, 123 to 126 in bf16), 52 for single tokens over 1000 to 8000 keys at D 256
+// (floor 31, bf16 41) and 171 for the drafts (33, 74): every product is made three times, and the kernels for one tile of
+// rows at width 256 and four at 128 spill 7 to 17 vector registers.
+//
+// Long form (prompts): see Long4.  24748 tokens over up to 7100 keys (H 32, HK 8, D 128) 1309 to 1446 us by card (1309 on one),
+// 0.93 to 1.03 PFLOP/s of the 1.34 that a large library product reaches: matrix instructions are busy 46% of cycles, the rest
 // is the vector work of the softmax and the widening (6.3 vector instructions for one of theirs), and power holds the clock.
+// That kernel spills 6 vector registers, those of fp32 at widths 128 and 256 8 and 21.
 #pragma once
 
 #include "gdn_attn.hpp"
@@ -37,8 +42,9 @@ struct Fp4Args {
     uint32_t g_inverse;  // floor(2^16 / G) + 1: r * g_inverse >> 16 is r / G for the short form's rows, as r * G < 2^16
 };
 
-// The kernel's argument, read again: what a loop does not need is not worth scalar registers across it (with all of it
-// held, 130 of them were spilled, and read back in the loop).
+// The kernel's argument, read again: what a loop does not need is not worth scalar registers across it.  With all of it held
+// 130 of them were spilled and read back in the loop; 68 to 165 still are in the kernels that go over pieces, the more the
+// wider the rows, but most come back once a piece.
 __device__ __forceinline__ const Fp4Args& args_again() {
     auto p = (const __attribute__((address_space(4))) Fp4Args*)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(p));
@@ -189,8 +195,8 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* to, int step)
     }
 }
 
-// A number whose exponent is the byte at `at` of x, as the conversions look at nothing else of a scale (checked over all
-// exponents with the other bits at random).
+// A number whose exponent is the byte at `at` of x, as the conversions look at nothing else of a scale: sign and fraction are
+// bits of its neighbours.
 __device__ __forceinline__ float scale_at(uint32_t x, uint32_t at) {
     return __uint_as_float(__builtin_amdgcn_alignbit(x, x, 8 * at + 9));
 }
@@ -482,6 +488,9 @@ struct Short4 {
                 e[i] = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], c, -ref[rt]));
                 l[rt] += e[i];
             }
+            // Operands of the second product: in the half types one part, rounded to the type, as over a plain cache.  The rounding
+            // is half a step of a probability, as the output's own is of the output; a second part would double the products.
+            // The sum is of the unrounded ones.
 #pragma unroll
             for (int i = 0; i < 4; ++i) split2<OP, PARTS>(e[2 * i], e[2 * i + 1], &p[rt][0][i], 4);
         }

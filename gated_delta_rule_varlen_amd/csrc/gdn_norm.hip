@@ -3,7 +3,9 @@
 // registers between its sums and its results; squares, sums and roots are fp32, each output is rounded once.
 //
 // Both are bound by bytes where there are many rows (a 1 GiB copy reaches 5.2 TB/s): residual_norm of 24748 rows of 4096 (bf16
-// beside an fp32 stream, norm of the block's output and channel scales, 1.22 GB) 244 to 248 us, 4.9 TB/s; gated_norm of
+// beside an fp32 stream, norm of the block's output and channel scales, 1.22 GB) 244 to 248 us, 4.9 TB/s; in fp32 332, 4.9;
+// 4096 rows of 32768 in bf16 220, 4.9, but beside an fp32 stream 440, 3.7, and in fp32 1003, 2.1: four and eight pieces of both
+// rows, this one and the next, pass the 128 registers that 1024 threads leave (43 and 148 spilled).  gated_norm of
 // 9111 x 16 heads of 64 fp16 elements (56 MB) 10.9 us, 5.1 TB/s.  With few rows they are one launch: 256 rows of 4096
 // 4.2 us, 256 x 32 heads of 128 4.1 us.
 #include <hip/hip_runtime.h>

@@ -483,6 +483,8 @@ gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc *desc, size_t *byte
  *         type; what passes 6 * 2^125 (fp16: 49152) becomes that
  *     code = the nearest to x / 2^e, ties to the even code, with the sign of x
  * A block with an infinity or NaN gets the scale byte 255 (and codes 0), and reads as NaN throughout.
+ * Codes and scale bytes are those of the OCP microscaling formats (E2M1 and E8M0), the choice of e is not: theirs is
+ * floor(log2 max|x|) - 2, which saturates what passes 6 * 2^e.  A cache of either is read alike (scale bytes 1 to 255).
  *
  * gdn_cache_read_fp4_varlen -- the way back: k_out[t], v_out[t] = what row kv_begin[b] + past[b] + i stands for, rounded
  * to the type where it is no number of it.
@@ -491,7 +493,8 @@ gdn_status gdn_attention_workspace_bytes(const gdn_attn_desc *desc, size_t *byte
  * errors as there (out = q included), except that kv_begin and kv_len are required, desc->prefix_len is 0, its strides of k,
  * v and the prefix are not read, desc->kv_rows = cache->rows, and D is a multiple of 32 (GDN_ERR_SHAPE).  With fp16 queries
  * the cache's values are those rounded to fp16: infinite past 65504, which scales past 2^13 can reach, and with fewer bits for
- * scales below 2^-23.
+ * scales below 2^-23.  fp32 queries are multiplied as sums of three bf16 numbers (but not over D > 128 with
+ * max_q > 32): exactly for magnitudes of 2^-100 to 3.39e38, above which a query counts as infinite.
  *
  * Tensors (element (row, head, j) at row*stride[0] + head*stride[1] + j, strides in bytes):
  *   k_codes, v_codes [rows, HK, D/2] uint8    16-byte aligned, strides multiples of 16 (GDN_ERR_ALIGN), rows at most 1 MiB
