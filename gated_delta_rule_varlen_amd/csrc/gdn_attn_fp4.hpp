@@ -13,13 +13,13 @@
 // end to end and are cut into equal parts, one a block, as in the short form there.
 //
 // Measured (bf16; the floor is the bytes at a 1 GiB copy's 5.2 TB/s): 256 sequences of up to 4096 keys (H 32, HK 8, D 128,
-// 604 MB) 122 to 126 us of 116: its loads alone take 114.5, its work without them 90, the joining launch 5.  One token over 131072
+// 604 MB) 122 to 128 us of 116: its loads alone take 114.5, its work without them 90, the joining launch 5.  One token over 131072
 // keys (HK 2, D 256, 71 MB) 24 to 25 of 13.7: 19 and the joining launch's 6.  Drafts of five tokens over 1000 to 8000 keys
 // (64 sequences, D 256, 167 MB) 73 to 75 of 32: bound by the products and the vector work of 40 rows (matrix
 // instructions busy 23% of cycles, vector ones 53%).  Tried: codes to registers without LDS 152 us on the first of
 // these; loads that leave the caches as they are, without the hint, 138; a barrier a tile, no gain.
 //
-// fp32 takes 150 us for the first of these (125 at the floor, 123 to 126 in bf16), 52 for single tokens over 1000 to 8000 keys at D 256
+// fp32 takes 150 us for a batch like the first of these (floor 125, bf16 123), 52 for single tokens over 1000 to 8000 keys at D 256
 // (floor 31, bf16 41) and 171 for the drafts (33, 74): every product is made three times, and the kernels for one tile of
 // rows at width 256 and four at 128 spill 7 to 17 vector registers.
 //
